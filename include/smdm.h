@@ -327,6 +327,133 @@ smdm_status smdm_forward_stepcausal_noalloc(const smdm_config* cfg, const smdm_w
                                             const int32_t* d_logit_rows, int n_rows,
                                             float* d_logits, cudaStream_t stream);
 
+/* ---------------------------------------------------------------------------------------------
+ * The training form's ends.  smdm_forward_stepcausal runs the training form up to its logits;
+ * the entry points below are what a program that scores or trains on a trajectory needs around
+ * it, at the two ends whose cost grows with the vocabulary: the embedding, the RMSNorm in front
+ * of the LM head, and the head's cross entropy (the per-row term of the masked diffusion
+ * objective, -E[(1/t) log p(X0 | Xt)]), each with its gradient.
+ *
+ * They need no handle.  Common rules:
+ *  - Row-major tensors on the current device; `ld` arguments are row strides in ELEMENTS, at
+ *    least the row's width; outputs without an ld are contiguous.  Pointers lie on their
+ *    element's boundary; any width is served, rows on 16-byte boundaries fastest.
+ *  - Outputs are overwritten, and must not overlap the inputs or the workspace, but for
+ *    smdm_rmsnorm_grad's grad_x, which may be its grad_add.
+ *  - d_workspace: caller memory, 256-byte aligned, of at least the matching *_workspace_bytes
+ *    (0 for an invalid shape).  Nothing is kept in it between calls; calls that share one must
+ *    be ordered, two captured graphs that share one included.
+ *  - d_status: optional device word; kernels OR 1 (a bounded wait gave up: outputs invalid) or
+ *    2 (a target or id beyond its table, handled as one that takes no part) into it.  The
+ *    caller clears and reads it.
+ *  - Results do not depend on timing: a call with the same inputs gives the same bits.
+ *  - Sums, softmax statistics and norms are fp32; outputs are rounded once at the end.
+ *  - SMDM_EINVAL: null, misaligned or inconsistent arguments; SMDM_ESHAPE: a size beyond what is
+ *    served; SMDM_ENOMEM: a small workspace; SMDM_ECUDA: a CUDA call failed.  Nothing is
+ *    launched after the first three.  0 rows are valid (a weight's gradient is then zero).
+ * ------------------------------------------------------------------------------------------- */
+typedef struct {
+  int rows;            /* 0 .. 2^24 */
+  int d_model;         /* 1 .. 65536 */
+  int vocab;           /* 1 .. 2^24 */
+  int dtype;           /* hidden, lm_head and their gradients: SMDM_F32 or SMDM_BF16 */
+  long long ld_hidden; /* row strides, elements */
+  long long ld_head;
+} smdm_head_shape;
+
+/* Workspace of smdm_head_loss (grad == 0) or smdm_head_loss_grad (grad != 0). */
+size_t smdm_head_loss_workspace_bytes(const smdm_head_shape* shape, int grad);
+
+/* Cross entropy of the LM head, without storing logits: with z_v = hidden_r . lm_head_v,
+ *   lse_r = log sum_v exp(z_v),   nll_r = lse_r - z_target(r)
+ * into d_nll and d_lse, fp32 [rows].  A row with a negative target takes no part: nll = lse = 0,
+ * and nothing that its hidden row holds (NaN included) reaches any output.  bf16 lm_head rows
+ * that lie on 16-byte boundaries (d_model and ld_head multiples of 8) are read in place; the
+ * tensor must then start on one too (SMDM_EINVAL). */
+smdm_status smdm_head_loss(const smdm_head_shape* shape, const void* d_hidden,
+                           const void* d_lm_head, const int32_t* d_target, float* d_nll,
+                           float* d_lse, void* d_workspace, size_t bytes, uint32_t* d_status,
+                           cudaStream_t stream);
+
+/* Its gradient, from lse of smdm_head_loss and d_grad_nll [rows], the gradient with respect to
+ * nll (the rows' loss weights times the upstream gradient): with
+ *   D_rv = grad_nll_r (exp(z_rv - lse_r) - [v = target(r)])
+ * grad_hidden = D lm_head [rows][d_model] (zero for rows that take no part) and
+ * grad_lm_head = D^T hidden [vocab][d_model].  Either output may be NULL.  D exists one piece of
+ * the vocabulary at a time (at most 256 MiB of it, or 256 columns). */
+smdm_status smdm_head_loss_grad(const smdm_head_shape* shape, const void* d_hidden,
+                                const void* d_lm_head, const int32_t* d_target,
+                                const float* d_lse, const float* d_grad_nll, void* d_grad_hidden,
+                                void* d_grad_lm_head, void* d_workspace, size_t bytes,
+                                uint32_t* d_status, cudaStream_t stream);
+
+typedef struct {
+  int rows;          /* 0 .. 2^24 */
+  int d_model;       /* 1 .. 8192 */
+  int x_dtype;       /* x, grad_x and grad_add */
+  int dtype;         /* gain, y, grad_y and grad_gain */
+  long long ld_x;    /* row strides, elements: of x, and of y (grad_y) */
+  long long ld_y;
+  float eps;         /* >= 0 */
+} smdm_rmsnorm_shape;
+
+/* y = x rstd gain with rstd = (mean x^2 + eps)^(-1/2); d_rstd (optional, fp32 [rows]) is what
+ * the gradient needs. */
+smdm_status smdm_rmsnorm(const smdm_rmsnorm_shape* shape, const void* d_x, const void* d_gain,
+                         void* d_y, float* d_rstd, cudaStream_t stream);
+
+size_t smdm_rmsnorm_grad_workspace_bytes(const smdm_rmsnorm_shape* shape);
+
+/* With u = grad_y gain:  grad_x = rstd (u - x rstd^2 mean(u x)) + grad_add,
+ * grad_gain = sum over rows of grad_y x rstd.  d_grad_add (optional, contiguous, x's type): the
+ * gradient that reaches x past the norm (the residual branch). */
+smdm_status smdm_rmsnorm_grad(const smdm_rmsnorm_shape* shape, const void* d_x,
+                              const void* d_gain, const float* d_rstd, const void* d_grad_y,
+                              const void* d_grad_add, void* d_grad_x, void* d_grad_gain,
+                              void* d_workspace, size_t bytes, cudaStream_t stream);
+
+typedef struct {
+  int rows;          /* ids, 0 .. 2^24 */
+  int d_model;       /* 1 .. 65536 */
+  int n_emb;         /* table rows, 1 .. 2^24 */
+  int dtype;         /* table and its gradient */
+  int out_dtype;     /* embedded rows and their gradient */
+  long long ld;      /* row stride, elements: of the table (smdm_embed) or of grad_out */
+  float scale;       /* 1, or the factor of a model that scales its embeddings */
+} smdm_embed_shape;
+
+/* out_i = scale * table[ids_i]; a negative id gives a row of zeros (padding). */
+smdm_status smdm_embed(const smdm_embed_shape* shape, const int32_t* d_ids, const void* d_table,
+                       void* d_out, uint32_t* d_status, cudaStream_t stream);
+
+size_t smdm_embed_grad_workspace_bytes(const smdm_embed_shape* shape);
+
+/* grad_table_v = scale * sum of grad_out_i over the rows with ids_i = v, [n_emb][d_model], every
+ * row written (zeros for an id that does not occur).  The rows are sorted by id and added in
+ * row order, so a token that fills half of the rows ([MASK]) costs what it would cost spread
+ * out, and the result does not depend on timing. */
+smdm_status smdm_embed_grad(const smdm_embed_shape* shape, const int32_t* d_ids,
+                            const void* d_grad_out, void* d_grad_table, void* d_workspace,
+                            size_t bytes, uint32_t* d_status, cudaStream_t stream);
+
+/* The loss of the training form: smdm_forward_stepcausal's forward over n step-labelled rows,
+ * then for the rows in d_loss_rows (n_rows of them, at most max_rows) the final RMSNorm and
+ * smdm_head_loss against d_target [n_rows] instead of logits.  The normalised rows are rounded
+ * to the model's dtype and multiplied with the lm_head as given.
+ *  - d_nll, d_lse: fp32 [n_rows].
+ *  - d_grad_nll NULL: the loss only.  Otherwise the gradients through the head: d_grad_x, fp32
+ *    [n_rows][d_model], with respect to the residual rows that the last layer leaves;
+ *    d_grad_final_norm [d_model] and d_grad_lm_head [vocab][d_model] in the model's dtype; all
+ *    three are then required.  A row listed twice gets one gradient row per listing.
+ *  - d_workspace: smdm_loss_stepcausal_workspace_bytes(cfg, n_rows, grad). */
+size_t smdm_loss_stepcausal_workspace_bytes(const smdm_config* cfg, int n_rows, int grad);
+smdm_status smdm_loss_stepcausal(smdm_handle* h, const int32_t* d_ids, const int32_t* d_pos,
+                                 const int32_t* d_type, const int32_t* d_label, int n,
+                                 const int32_t* d_loss_rows, int n_rows, const int32_t* d_target,
+                                 float* d_nll, float* d_lse, const float* d_grad_nll,
+                                 float* d_grad_x, void* d_grad_final_norm, void* d_grad_lm_head,
+                                 void* d_workspace, size_t bytes, cudaStream_t stream);
+
 /* Synchronise `stream` and return the device status word (0 = no device-side error) and clear
  * it.  Returns SMDM_ETIMEOUT / SMDM_EDEVICE when a bit is set. */
 smdm_status smdm_device_status(smdm_handle* h, unsigned* h_bits, cudaStream_t stream);

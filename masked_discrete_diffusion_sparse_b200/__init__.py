@@ -36,7 +36,11 @@ EXPORTED = ["smdm_workspace_bytes", "smdm_create", "smdm_destroy", "smdm_last_er
             "smdm_dense_step", "smdm_generate",
             "smdm_forward_stepcausal", "smdm_debug_mask", "smdm_debug_rows",
             "smdm_context_length", "smdm_device_status", "smdm_profile_begin",
-            "smdm_profile_end", "smdm_forward_stepcausal_noalloc"]
+            "smdm_profile_end", "smdm_forward_stepcausal_noalloc",
+            "smdm_head_loss_workspace_bytes", "smdm_head_loss", "smdm_head_loss_grad",
+            "smdm_rmsnorm", "smdm_rmsnorm_grad_workspace_bytes", "smdm_rmsnorm_grad",
+            "smdm_embed", "smdm_embed_grad_workspace_bytes", "smdm_embed_grad",
+            "smdm_loss_stepcausal_workspace_bytes", "smdm_loss_stepcausal"]
 
 K_CLASSES = ["pack", "norm", "gemm_qkv", "attn", "gemm_o", "gemm_gateup", "gemm_down",
              "gemm_lmhead", "unmask", "other"]
@@ -82,6 +86,24 @@ class smdm_plan(ctypes.Structure):
 class smdm_profile(ctypes.Structure):
     _fields_ = [("launches", ctypes.c_ulonglong), ("class_launches", ctypes.c_ulonglong * 10),
                 ("class_ms", ctypes.c_double * 10)]
+
+
+class smdm_head_shape(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int), ("d_model", ctypes.c_int), ("vocab", ctypes.c_int),
+                ("dtype", ctypes.c_int), ("ld_hidden", ctypes.c_longlong),
+                ("ld_head", ctypes.c_longlong)]
+
+
+class smdm_rmsnorm_shape(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int), ("d_model", ctypes.c_int), ("x_dtype", ctypes.c_int),
+                ("dtype", ctypes.c_int), ("ld_x", ctypes.c_longlong),
+                ("ld_y", ctypes.c_longlong), ("eps", ctypes.c_float)]
+
+
+class smdm_embed_shape(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int), ("d_model", ctypes.c_int), ("n_emb", ctypes.c_int),
+                ("dtype", ctypes.c_int), ("out_dtype", ctypes.c_int), ("ld", ctypes.c_longlong),
+                ("scale", ctypes.c_float)]
 
 
 _lib = None
@@ -136,6 +158,24 @@ def lib() -> ctypes.CDLL:
                                                   ctypes.POINTER(smdm_weights), vp, vp, vp, vp,
                                                   i32, vp, i32, vp, vp]
     L.smdm_forward_stepcausal_noalloc.restype = st
+    sz = ctypes.c_size_t
+    hs, ns, es = (ctypes.POINTER(t) for t in (smdm_head_shape, smdm_rmsnorm_shape,
+                                              smdm_embed_shape))
+    for name, args, res in [
+            ("smdm_head_loss_workspace_bytes", [hs, i32], sz),
+            ("smdm_head_loss", [hs, vp, vp, vp, vp, vp, vp, sz, vp, vp], st),
+            ("smdm_head_loss_grad", [hs, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp, vp], st),
+            ("smdm_rmsnorm", [ns, vp, vp, vp, vp, vp], st),
+            ("smdm_rmsnorm_grad_workspace_bytes", [ns], sz),
+            ("smdm_rmsnorm_grad", [ns, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp], st),
+            ("smdm_embed", [es, vp, vp, vp, vp, vp], st),
+            ("smdm_embed_grad_workspace_bytes", [es], sz),
+            ("smdm_embed_grad", [es, vp, vp, vp, vp, sz, vp, vp], st),
+            ("smdm_loss_stepcausal_workspace_bytes", [ctypes.POINTER(smdm_config), i32, i32], sz),
+            ("smdm_loss_stepcausal", [vp, vp, vp, vp, vp, i32, vp, i32] + [vp] * 8 + [sz, vp],
+             st)]:
+        getattr(L, name).argtypes = args
+        getattr(L, name).restype = res
     _lib = L
     return L
 
@@ -298,6 +338,38 @@ class Model:
             ids.numel(), _ptr(_i32(logit_rows)), logit_rows.numel(), _ptr(logits),
             _stream(stream)))
 
+    def smdm_loss_stepcausal(self, ids, pos, types, labels, loss_rows, target, nll, lse, workspace,
+                             grad_nll=None, grad_x=None, grad_final_norm=None, grad_lm_head=None,
+                             stream=None):
+        """Training-form forward over the step-labelled rows, then the cross entropy of the rows
+        in loss_rows against target (int32, negative: takes no part) into nll and lse (fp32).
+        With grad_nll (fp32, the loss weight of every row) also the gradients through the head:
+        grad_x (fp32 [n_rows][d_model]), grad_final_norm and grad_lm_head (model dtype).
+        workspace: uint8 tensor of smdm_loss_stepcausal_workspace_bytes."""
+        m = loss_rows.numel()
+        d, v = self.cfg.d_model, self.cfg.vocab
+        dt = torch.float32 if self.cfg.dtype == SMDM_F32 else torch.bfloat16
+        for t in (pos, types, labels):
+            _shape(t, (ids.numel(),), "pos / types / labels")
+        for name, t, shape, want in (
+                ("target", target, (m,), torch.int32), ("nll", nll, (m,), torch.float32),
+                ("lse", lse, (m,), torch.float32), ("grad_nll", grad_nll, (m,), torch.float32),
+                ("grad_x", grad_x, (m, d), torch.float32),
+                ("grad_final_norm", grad_final_norm, (d,), dt),
+                ("grad_lm_head", grad_lm_head, (v, d), dt)):
+            if t is not None:
+                _shape(t, shape, name)
+                _typed(t, want, name)
+        self._check(lib().smdm_loss_stepcausal(
+            self.h, _ptr(_i32(ids)), _ptr(_i32(pos)), _ptr(_i32(types)), _ptr(_i32(labels)),
+            ids.numel(), _ptr(_i32(loss_rows)), m, _ptr(target), _ptr(nll), _ptr(lse),
+            _ptr(grad_nll), _ptr(grad_x), _ptr(grad_final_norm), _ptr(grad_lm_head),
+            _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream)))
+
+    def smdm_loss_stepcausal_workspace_bytes(self, n_rows: int, grad: bool = False) -> int:
+        return _bytes(lib().smdm_loss_stepcausal_workspace_bytes(ctypes.byref(self.cfg), n_rows,
+                                                                 1 if grad else 0))
+
     def smdm_debug_mask(self, types, labels, bitmap, stream=None):
         self._check(lib().smdm_debug_mask(self.h, _ptr(_i32(types)), _ptr(_i32(labels)),
                                           types.numel(), _ptr(bitmap), _stream(stream)))
@@ -354,6 +426,206 @@ def smdm_forward_stepcausal_noalloc(cfg: smdm_config, weights: dict, ids, pos, t
         _ptr(logits), _stream(stream))
     if s != SMDM_OK:
         raise SmdmError(s, "smdm_forward_stepcausal_noalloc failed")
+
+
+# --- the training form's ends (no handle) -----------------------------------------------------
+_DTYPES = {torch.float32: SMDM_F32, torch.bfloat16: SMDM_BF16}
+
+
+def _dtype(t) -> int:
+    dt = t.dtype if isinstance(t, torch.Tensor) else t
+    if dt in (SMDM_F32, SMDM_BF16) and not isinstance(dt, torch.dtype):
+        return dt
+    if dt not in _DTYPES:
+        raise ValueError(f"expected float32 or bfloat16, got {dt}")
+    return _DTYPES[dt]
+
+
+def _typed(t: torch.Tensor, dt: torch.dtype, name: str):
+    if t.dtype != dt:
+        raise ValueError(f"{name}: expected {dt}, got {t.dtype}")
+
+
+def _shape(t: torch.Tensor, shape: tuple, name: str):
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def _bytes(n: int) -> int:
+    if n == 0:
+        raise SmdmError(SMDM_ESHAPE, "invalid shape")
+    return n
+
+
+def _rows(t: torch.Tensor, name: str):
+    """Pointer and row stride of a 2-D tensor whose rows are contiguous."""
+    if t.dim() != 2:
+        raise ValueError(f"{name}: expected a 2-D tensor")
+    n, d = t.shape
+    ld = t.stride(0) if n > 1 else d
+    if d > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name}: the elements of a row must be contiguous")
+    if ld < d:
+        raise ValueError(f"{name}: rows overlap")
+    if not t.is_cuda:
+        raise ValueError("expected a CUDA tensor")
+    return (ctypes.c_void_p(t.data_ptr()) if t.numel() else None), ld
+
+
+def _call(fn: str, stream, tensors, *args):
+    """Run one entry point on the tensors' device and the given (or that device's current)
+    stream; a tensor used on another stream than the current one is recorded there, so that the
+    allocator does not hand its memory out while the kernels run."""
+    ts = [t for t in tensors if t is not None]
+    dev = ts[0].device
+    if any(t.device != dev for t in ts):
+        raise ValueError("all tensors must be on one device")
+    if stream is not None and stream.device != dev:
+        raise ValueError(f"the stream is on {stream.device}, the tensors on {dev}")
+    with torch.cuda.device(dev):
+        cur = torch.cuda.current_stream(dev)
+        s = cur if stream is None else stream
+        if s != cur:
+            for t in ts:
+                t.record_stream(s)
+        r = getattr(lib(), fn)(*args, ctypes.c_void_p(s.cuda_stream))
+    if r != SMDM_OK:
+        raise SmdmError(r, f"{fn} failed")
+
+
+def _status(t: Optional[torch.Tensor]):
+    if t is not None and (t.numel() < 1 or t.element_size() != 4):
+        raise ValueError("status: expected a 32-bit integer tensor of one element")
+    return _ptr(t)
+
+
+def _ws(t: torch.Tensor):
+    return _ptr(t), t.numel() * t.element_size()
+
+
+def _head_shape(hidden, lm_head, target):
+    if lm_head.dtype != hidden.dtype:
+        raise ValueError("hidden and lm_head must share their dtype")
+    h, ld_h = _rows(hidden, "hidden")
+    w, ld_w = _rows(lm_head, "lm_head")
+    n, d = hidden.shape
+    _shape(lm_head, (lm_head.shape[0], d), "lm_head")
+    _shape(target, (n,), "target")
+    s = smdm_head_shape(n, d, lm_head.shape[0], _dtype(hidden), ld_h, ld_w)
+    return s, h, w
+
+
+def smdm_head_loss_workspace_bytes(rows: int, d_model: int, vocab: int, dtype,
+                                   grad: bool = False) -> int:
+    """dtype: torch.float32, torch.bfloat16 or the SMDM_* constant."""
+    s = smdm_head_shape(rows, d_model, vocab, _dtype(dtype), d_model, d_model)
+    return _bytes(lib().smdm_head_loss_workspace_bytes(ctypes.byref(s), 1 if grad else 0))
+
+
+def smdm_head_loss(hidden, lm_head, target, nll, lse, workspace, status=None, stream=None):
+    """Cross entropy of the LM head without its logits: hidden [R][d] and lm_head [V][d] (float32
+    or bfloat16, rows may lie apart), target int32 [R] (negative: the row takes no part) ->
+    nll, lse (fp32 [R])."""
+    s, h, w = _head_shape(hidden, lm_head, target)
+    for name, t in (("nll", nll), ("lse", lse)):
+        _shape(t, (s.rows,), name)
+        _typed(t, torch.float32, name)
+    ws, nb = _ws(workspace)
+    _call("smdm_head_loss", stream, (hidden, lm_head, target, nll, lse, workspace, status),
+          ctypes.byref(s), h, w, _ptr(_i32(target)), _ptr(nll), _ptr(lse), ws, nb,
+          _status(status))
+
+
+def smdm_head_loss_grad(hidden, lm_head, target, lse, grad_nll, grad_hidden, grad_lm_head,
+                        workspace, status=None, stream=None):
+    """Gradient of smdm_head_loss: lse from it and grad_nll (fp32 [R], the rows' weights) ->
+    grad_hidden [R][d] and grad_lm_head [V][d] in hidden's dtype (either may be None)."""
+    s, h, w = _head_shape(hidden, lm_head, target)
+    for name, t in (("lse", lse), ("grad_nll", grad_nll)):
+        _shape(t, (s.rows,), name)
+        _typed(t, torch.float32, name)
+    for name, t, shape in (("grad_hidden", grad_hidden, (s.rows, s.d_model)),
+                           ("grad_lm_head", grad_lm_head, (s.vocab, s.d_model))):
+        if t is not None:
+            _shape(t, shape, name)
+            _typed(t, hidden.dtype, name)
+    ws, nb = _ws(workspace)
+    _call("smdm_head_loss_grad", stream,
+          (hidden, lm_head, target, lse, grad_nll, grad_hidden, grad_lm_head, workspace, status),
+          ctypes.byref(s), h, w, _ptr(_i32(target)), _ptr(lse), _ptr(grad_nll),
+          _ptr(grad_hidden), _ptr(grad_lm_head), ws, nb, _status(status))
+
+
+def smdm_rmsnorm(x, gain, y, rstd=None, eps: float = 1e-6, stream=None):
+    """y = x rstd gain, rstd = (mean x^2 + eps)^(-1/2): x [R][d] and y [R][d] (rows may lie
+    apart), gain [d] in y's dtype, rstd fp32 [R] (optional, for the gradient)."""
+    px, ld_x = _rows(x, "x")
+    py, ld_y = _rows(y, "y")
+    _shape(y, x.shape, "y")
+    _shape(gain, (x.shape[1],), "gain")
+    _typed(gain, y.dtype, "gain")
+    if rstd is not None:
+        _shape(rstd, (x.shape[0],), "rstd")
+        _typed(rstd, torch.float32, "rstd")
+    s = smdm_rmsnorm_shape(x.shape[0], x.shape[1], _dtype(x), _dtype(y), ld_x, ld_y, eps)
+    _call("smdm_rmsnorm", stream, (x, gain, y, rstd), ctypes.byref(s), px, _ptr(gain), py,
+          _ptr(rstd))
+
+
+def smdm_rmsnorm_grad_workspace_bytes(rows: int, d_model: int) -> int:
+    s = smdm_rmsnorm_shape(rows, d_model, SMDM_F32, SMDM_F32, d_model, d_model, 0.0)
+    return _bytes(lib().smdm_rmsnorm_grad_workspace_bytes(ctypes.byref(s)))
+
+
+def smdm_rmsnorm_grad(x, gain, rstd, grad_y, grad_x, grad_gain, workspace, grad_add=None,
+                      stream=None):
+    """Gradient of smdm_rmsnorm: grad_x [R][d] in x's dtype (plus grad_add, the gradient that
+    reaches x past the norm; the two may be one tensor) and grad_gain [d]."""
+    px, ld_x = _rows(x, "x")
+    pg, ld_y = _rows(grad_y, "grad_y")
+    n, d = x.shape
+    _shape(grad_y, (n, d), "grad_y")
+    for name, t, shape, want in (
+            ("gain", gain, (d,), grad_y.dtype), ("grad_gain", grad_gain, (d,), grad_y.dtype),
+            ("rstd", rstd, (n,), torch.float32), ("grad_x", grad_x, (n, d), x.dtype),
+            ("grad_add", grad_add, (n, d), x.dtype)):
+        if t is not None:
+            _shape(t, shape, name)
+            _typed(t, want, name)
+    s = smdm_rmsnorm_shape(n, d, _dtype(x), _dtype(grad_y), ld_x, ld_y, 0.0)
+    ws, nb = _ws(workspace)
+    _call("smdm_rmsnorm_grad", stream,
+          (x, gain, rstd, grad_y, grad_x, grad_gain, workspace, grad_add), ctypes.byref(s), px,
+          _ptr(gain), _ptr(rstd), pg, _ptr(grad_add), _ptr(grad_x), _ptr(grad_gain), ws, nb)
+
+
+def smdm_embed(ids, table, out, scale: float = 1.0, status=None, stream=None):
+    """out[i] = scale * table[ids[i]] (float32 or bfloat16 each); a negative id gives zeros."""
+    pt, ld = _rows(table, "table")
+    _shape(ids, (out.shape[0],), "ids")
+    _shape(out, (out.shape[0], table.shape[1]), "out")
+    s = smdm_embed_shape(ids.numel(), table.shape[1], table.shape[0], _dtype(table), _dtype(out),
+                         ld, scale)
+    _call("smdm_embed", stream, (ids, table, out, status), ctypes.byref(s), _ptr(_i32(ids)), pt,
+          _ptr(out), _status(status))
+
+
+def smdm_embed_grad_workspace_bytes(rows: int, d_model: int, n_emb: int) -> int:
+    s = smdm_embed_shape(rows, d_model, n_emb, SMDM_F32, SMDM_F32, d_model, 1.0)
+    return _bytes(lib().smdm_embed_grad_workspace_bytes(ctypes.byref(s)))
+
+
+def smdm_embed_grad(ids, grad_out, grad_table, workspace, scale: float = 1.0, status=None,
+                    stream=None):
+    """grad_table[v] = scale * sum of grad_out[i] over ids[i] == v, every row written."""
+    pg, ld = _rows(grad_out, "grad_out")
+    _shape(ids, (grad_out.shape[0],), "ids")
+    _shape(grad_table, (grad_table.shape[0], grad_out.shape[1]), "grad_table")
+    s = smdm_embed_shape(ids.numel(), grad_out.shape[1], grad_table.shape[0], _dtype(grad_table),
+                         _dtype(grad_out), ld, scale)
+    ws, nb = _ws(workspace)
+    _call("smdm_embed_grad", stream, (ids, grad_out, grad_table, workspace, status),
+          ctypes.byref(s), _ptr(_i32(ids)), pg, _ptr(grad_table), ws, nb, _status(status))
 
 
 def make_config(n_layers, d_model, n_heads, d_head, d_ffn, vocab, n_reg=64, dtype=SMDM_BF16,

@@ -11,31 +11,16 @@
 #include <vector>
 
 #include "attn.h"
+#include "ends.h"
 #include "gemm.h"
+#include "head.h"
 #include "misc.h"
 #include "smdm.h"
+#include "tensormap.h"
 
 using namespace smdm;
 
 namespace {
-
-typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
-                                  const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
-                                  const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiledFn get_encode_fn() {
-  static EncodeTiledFn fn = nullptr;
-  if (!fn) {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) ==
-            cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<EncodeTiledFn>(p);
-  }
-  return fn;
-}
 
 // 2-D fp16 tensor map: `inner` contiguous elements per row, `outer` rows, 128-byte swizzle (the
 // GEMMs' operands: the fp16 weight copies and the fp16 activations).
@@ -347,10 +332,10 @@ smdm_status fail(smdm_handle* h, smdm_status st, const char* fmt, ...) {
 struct Launch {
   smdm_handle* h;
   cudaStream_t st;
-  Launch(smdm_handle* h_, int cls, cudaStream_t st_) : h(h_), st(st_) {
+  Launch(smdm_handle* h_, int cls, cudaStream_t st_, int kernels = 1) : h(h_), st(st_) {
     Profiler& p = h->prof;
-    p.launches++;
-    p.class_launches[cls]++;
+    p.launches += kernels;
+    p.class_launches[cls] += kernels;
     if (p.on && p.timed) {
       if (p.used * 2 + 2 > p.ev.size()) {
         cudaEvent_t a, b;
@@ -1297,15 +1282,12 @@ smdm_status smdm_generate(smdm_handle* h, int batch, const int32_t* d_prompts, i
   return SMDM_OK;
 }
 
-smdm_status smdm_forward_stepcausal(smdm_handle* h, const int32_t* d_ids, const int32_t* d_pos,
-                                    const int32_t* d_type, const int32_t* d_label, int n,
-                                    const int32_t* d_logit_rows, int n_rows, float* d_logits,
-                                    cudaStream_t st) {
-  if (!h) return SMDM_EINVAL;
-  if (!d_ids || !d_pos || !d_type || !d_label || !d_logit_rows || !d_logits)
-    return fail(h, SMDM_EINVAL, "null argument");
-  if (n < 1 || n > h->cfg.max_rows || n_rows < 1 || n_rows > h->cfg.max_rows)
-    return fail(h, SMDM_ESHAPE, "n=%d / n_rows=%d outside [1, max_rows]", n, n_rows);
+// Pack a step-labelled sequence of n rows and run it through the layers; the rows in `sel`
+// (n_sel of them) get logits when `logits` is given.
+static smdm_status run_stepcausal(smdm_handle* h, const int32_t* d_ids, const int32_t* d_pos,
+                                  const int32_t* d_type, const int32_t* d_label, int n,
+                                  const int32_t* d_sel, int n_sel, float* d_logits,
+                                  cudaStream_t st) {
   LinearPackArgs a{};
   a.mode = kPackTrain;
   a.n = n;
@@ -1320,7 +1302,7 @@ smdm_status smdm_forward_stepcausal(smdm_handle* h, const int32_t* d_ids, const 
   a.rows = h->rows;
   a.status = h->status();
   { Launch lg_(h, SMDM_K_PACK, st); CK(launch_pack_linear(a, st)); }
-  { Launch lg_(h, SMDM_K_OTHER, st); CK(launch_gather_rows(d_logit_rows, n_rows, n, h->rows.qrow, h->status(), st)); }
+  { Launch lg_(h, SMDM_K_OTHER, st); CK(launch_gather_rows(d_sel, n_sel, n, h->rows.qrow, h->status(), st)); }
   // bf16 models: per-row key bounds and per-query-tile key-tile lists, so the attention skips
   // the 128-key tiles in which no key is visible to a query tile
   const bool bound = h->bf16;
@@ -1342,9 +1324,145 @@ smdm_status smdm_forward_stepcausal(smdm_handle* h, const int32_t* d_ids, const 
   f.scratch_kv = true;
   f.n_seg = 1;
   f.seg[0] = AttnSeg{0, 0, n, n, 0};
-  f.n_logit = n_rows;
+  f.n_logit = d_logits ? n_sel : 0;
   f.logits = d_logits;
   return forward(h, f, st);
+}
+
+smdm_status smdm_forward_stepcausal(smdm_handle* h, const int32_t* d_ids, const int32_t* d_pos,
+                                    const int32_t* d_type, const int32_t* d_label, int n,
+                                    const int32_t* d_logit_rows, int n_rows, float* d_logits,
+                                    cudaStream_t st) {
+  if (!h) return SMDM_EINVAL;
+  if (!d_ids || !d_pos || !d_type || !d_label || !d_logit_rows || !d_logits)
+    return fail(h, SMDM_EINVAL, "null argument");
+  if (n < 1 || n > h->cfg.max_rows || n_rows < 1 || n_rows > h->cfg.max_rows)
+    return fail(h, SMDM_ESHAPE, "n=%d / n_rows=%d outside [1, max_rows]", n, n_rows);
+  return run_stepcausal(h, d_ids, d_pos, d_type, d_label, n, d_logit_rows, n_rows, d_logits, st);
+}
+
+namespace {
+
+// Workspace of the training form's loss: the loss rows of the residual stream, their norm, and
+// what the head's loss (and the gradients) need.
+struct LossLayout {
+  size_t x, hid, rstd, ghid, head, head_bytes, norm, total;
+};
+
+LossLayout loss_layout(const smdm_config* c, int n_rows, bool grad) {
+  LossLayout L{};
+  const size_t d = c->d_model, es = c->dtype == SMDM_BF16 ? 2 : 4;
+  const bool f32 = c->dtype == SMDM_F32;
+  size_t off = 0;
+  auto take = [&](size_t bytes) {
+    const size_t o = off;
+    off = align_up(off + bytes, 1024);
+    return o;
+  };
+  L.x = take(n_rows * d * 4);
+  L.hid = take(n_rows * d * es);
+  L.rstd = take((size_t)n_rows * 4);
+  L.head_bytes = head_workspace_bytes(n_rows, c->d_model, c->vocab, f32, false);
+  if (grad) {
+    L.ghid = take(n_rows * d * es);
+    L.norm = take(rmsnorm_grad_bytes(n_rows, c->d_model));
+    L.head_bytes = std::max(L.head_bytes,
+                            head_workspace_bytes(n_rows, c->d_model, c->vocab, f32, true));
+  }
+  L.head = take(L.head_bytes);
+  L.total = off;
+  return L;
+}
+
+}  // namespace
+
+size_t smdm_loss_stepcausal_workspace_bytes(const smdm_config* cfg, int n_rows, int grad) {
+  if (!config_ok(cfg, nullptr) || n_rows < 1 || n_rows > cfg->max_rows) return 0;
+  return loss_layout(cfg, n_rows, grad != 0).total;
+}
+
+smdm_status smdm_loss_stepcausal(smdm_handle* h, const int32_t* d_ids, const int32_t* d_pos,
+                                 const int32_t* d_type, const int32_t* d_label, int n,
+                                 const int32_t* d_loss_rows, int n_rows, const int32_t* d_target,
+                                 float* d_nll, float* d_lse, const float* d_grad_nll,
+                                 float* d_grad_x, void* d_grad_final_norm, void* d_grad_lm_head,
+                                 void* d_workspace, size_t bytes, cudaStream_t st) {
+  if (!h) return SMDM_EINVAL;
+  if (!d_ids || !d_pos || !d_type || !d_label || !d_loss_rows || !d_target || !d_nll || !d_lse)
+    return fail(h, SMDM_EINVAL, "null argument");
+  const bool grad = d_grad_nll != nullptr;
+  if (grad != (d_grad_x != nullptr) || grad != (d_grad_final_norm != nullptr) ||
+      grad != (d_grad_lm_head != nullptr))
+    return fail(h, SMDM_EINVAL, "gradients need grad_nll and all three outputs");
+  if (n < 1 || n > h->cfg.max_rows || n_rows < 1 || n_rows > h->cfg.max_rows)
+    return fail(h, SMDM_ESHAPE, "n=%d / n_rows=%d outside [1, max_rows]", n, n_rows);
+  const smdm_config& c = h->cfg;
+  const LossLayout L = loss_layout(&c, n_rows, grad);
+  if (!d_workspace || reinterpret_cast<uintptr_t>(d_workspace) % 256)
+    return fail(h, SMDM_EINVAL, "the workspace must be 256-byte aligned device memory");
+  if (bytes < L.total)
+    return fail(h, SMDM_ENOMEM, "workspace of %zu bytes, %zu needed", bytes, L.total);
+  if (head_needs_aligned_weight(c.d_model, c.d_model, !h->bf16) &&
+      reinterpret_cast<uintptr_t>(h->lm_head) % 16)
+    return fail(h, SMDM_EINVAL, "lm_head must start on a 16-byte boundary");
+  smdm_status s = run_stepcausal(h, d_ids, d_pos, d_type, d_label, n, d_loss_rows, n_rows, nullptr,
+                                 st);
+  if (s) return s;
+  uint8_t* ws = static_cast<uint8_t*>(d_workspace);
+  float* x = reinterpret_cast<float*>(ws + L.x);
+  float* rstd = reinterpret_cast<float*>(ws + L.rstd);
+  const int d = c.d_model;
+  {
+    // (the listed rows were checked and copied into rows.qrow by the forward)
+    Launch lg_(h, SMDM_K_OTHER, st);
+    CK(launch_gather_f32(h->at<float>(h->L.x), h->rows.qrow, n_rows, n, d, x, h->status(), st));
+  }
+  RmsArgs na{};
+  na.rows = n_rows;
+  na.d = d;
+  na.x_f32 = true;
+  na.f32 = !h->bf16;
+  na.ld_x = na.ld_y = d;
+  na.eps = c.rms_eps;
+  na.x = x;
+  na.gain = h->final_norm;
+  na.y = ws + L.hid;
+  na.rstd_out = rstd;
+  { Launch lg_(h, SMDM_K_NORM, st); CK(launch_train_rmsnorm(na, st)); }
+  HeadArgs ha{};
+  ha.rows = n_rows;
+  ha.d = d;
+  ha.vocab = c.vocab;
+  ha.f32 = !h->bf16;
+  ha.ld_hidden = ha.ld_head = d;
+  ha.hidden = ws + L.hid;
+  ha.head = h->lm_head;
+  ha.target = d_target;
+  ha.nll = d_nll;
+  ha.lse_out = d_lse;
+  ha.ws = ws + L.head;
+  ha.status = h->status();
+  {
+    Launch lg_(h, SMDM_K_GEMM_LMHEAD, st, head_loss_launches(ha));
+    CK(launch_head_loss(ha, st));
+  }
+  if (!grad) return SMDM_OK;
+  ha.nll = ha.lse_out = nullptr;
+  ha.lse = d_lse;
+  ha.grad_nll = d_grad_nll;
+  ha.grad_hidden = ws + L.ghid;
+  ha.grad_head = d_grad_lm_head;
+  {
+    Launch lg_(h, SMDM_K_GEMM_LMHEAD, st, head_grad_launches(ha));
+    CK(launch_head_grad(ha, st));
+  }
+  na.rstd = rstd;
+  na.grad_y = ws + L.ghid;
+  na.grad_x = d_grad_x;
+  na.grad_gain = d_grad_final_norm;
+  na.ws = reinterpret_cast<float*>(ws + L.norm);
+  { Launch lg_(h, SMDM_K_NORM, st, 2); CK(launch_train_rmsnorm_grad(na, st)); }
+  return SMDM_OK;
 }
 
 smdm_status smdm_debug_mask(smdm_handle* h, const int32_t* d_type, const int32_t* d_label, int n,

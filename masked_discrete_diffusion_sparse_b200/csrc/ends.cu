@@ -1,0 +1,733 @@
+// The two ends of the training form around the transformer's layers: RMSNorm with its gradient,
+// and the embedding lookup with the gradient of its table.  Both move bytes: what bounds them is
+// HBM, so every row is read once, held in registers and written once.
+#include "ends.h"
+
+#include <algorithm>
+
+namespace smdm {
+
+namespace {
+
+SMDM_DEV void load4(const float* p, float* v) {
+  const float4 u = *reinterpret_cast<const float4*>(p);
+  v[0] = u.x; v[1] = u.y; v[2] = u.z; v[3] = u.w;
+}
+SMDM_DEV void load4(const __nv_bfloat16* p, float* v) {
+  const uint2 u = *reinterpret_cast<const uint2*>(p);
+  v[0] = __uint_as_float(u.x << 16); v[1] = __uint_as_float(u.x & 0xffff0000u);
+  v[2] = __uint_as_float(u.y << 16); v[3] = __uint_as_float(u.y & 0xffff0000u);
+}
+SMDM_DEV uint32_t bf2(float a, float b) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+SMDM_DEV void store4(float* p, const float* v) {
+  *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+}
+SMDM_DEV void store4(__nv_bfloat16* p, const float* v) {
+  *reinterpret_cast<uint2*>(p) = make_uint2(bf2(v[0], v[1]), bf2(v[2], v[3]));
+}
+template <int VEC, typename T>
+SMDM_DEV void load_v(const T* p, float* v) {
+  if constexpr (VEC == 4) load4(p, v);
+  else v[0] = to_f<T>(*p);
+}
+template <int VEC, typename T>
+SMDM_DEV void store_v(T* p, const float* v) {
+  if constexpr (VEC == 4) store4(p, v);
+  else *p = from_f<T>(v[0]);
+}
+
+int device_sms() {
+  int dev = 0, n = 148;
+  if (cudaGetDevice(&dev) == cudaSuccess)
+    cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
+  return n;
+}
+
+bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+
+// Sum over the TPR threads of a row (a warp, or the whole CTA).
+template <int TPR>
+SMDM_DEV float row_sum(float s, float* red) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  if constexpr (TPR > 32) {
+    const int warp = threadIdx.x >> 5;
+    __syncthreads();                  // the previous row's sums have been read
+    if ((threadIdx.x & 31) == 0) red[warp] = s;
+    __syncthreads();
+    s = 0.f;
+#pragma unroll
+    for (int i = 0; i < TPR / 32; ++i) s += red[i];
+  }
+  return s;
+}
+
+constexpr int kNormThreads = 256;
+
+// y = x r gain, r = (mean x^2 + eps)^-1/2.  TPR threads per row, NU units of VEC elements each.
+template <typename X, typename T, int TPR, int VEC, int NU>
+__global__ void __launch_bounds__(kNormThreads) train_rms_kernel(RmsArgs a) {
+  griddep_launch();
+  griddep_wait();
+  __shared__ float red[32];
+  constexpr int RPC = kNormThreads / TPR;
+  const int tid = threadIdx.x % TPR;
+  const int row = blockIdx.x * RPC + threadIdx.x / TPR;
+  if (RPC > 1 && row >= a.rows) return;
+  const int units = a.d / VEC;
+  const X* x = static_cast<const X*>(a.x) + (size_t)row * a.ld_x;
+  float v[NU * VEC];
+  float ss = 0.f;
+#pragma unroll
+  for (int u = 0; u < NU; ++u) {
+    const int i = tid + u * TPR;
+    if (i < units) {
+      load_v<VEC>(x + (size_t)i * VEC, v + u * VEC);
+#pragma unroll
+      for (int k = 0; k < VEC; ++k) ss += v[u * VEC + k] * v[u * VEC + k];
+    }
+  }
+  ss = row_sum<TPR>(ss, red);
+  const float r = 1.f / sqrtf(ss / (float)a.d + a.eps);
+  if (a.rstd_out && tid == 0) a.rstd_out[row] = r;
+  T* y = static_cast<T*>(a.y) + (size_t)row * a.ld_y;
+  const T* gain = static_cast<const T*>(a.gain);
+#pragma unroll
+  for (int u = 0; u < NU; ++u) {
+    const int i = tid + u * TPR;
+    if (i < units) {
+      float g[VEC];
+      load_v<VEC>(gain + (size_t)i * VEC, g);
+#pragma unroll
+      for (int k = 0; k < VEC; ++k) g[k] *= v[u * VEC + k] * r;
+      store_v<VEC>(y + (size_t)i * VEC, g);
+    }
+  }
+}
+
+// u = gy gain;  gx = r (u - x r^2 mean(u x)) + add;  ggain = sum over rows of gy x r.
+// Persistent CTAs: the gain and this CTA's share of its gradient stay in registers over all the
+// CTA's rows; the shares go to ws[CTA][d] and are added up in order by rms_gain_kernel.
+template <typename X, typename T, int TPR, int VEC, int NU>
+__global__ void __launch_bounds__(kNormThreads) train_rms_grad_kernel(RmsArgs a) {
+  griddep_launch();
+  griddep_wait();
+  __shared__ float red[32];
+  constexpr int RPC = kNormThreads / TPR;
+  const int tid = threadIdx.x % TPR, sub = threadIdx.x / TPR;
+  const int units = a.d / VEC;
+  float gain[NU * VEC], acc[NU * VEC];
+#pragma unroll
+  for (int u = 0; u < NU; ++u) {
+    const int i = tid + u * TPR;
+#pragma unroll
+    for (int k = 0; k < VEC; ++k) gain[u * VEC + k] = acc[u * VEC + k] = 0.f;
+    if (i < units) load_v<VEC>(static_cast<const T*>(a.gain) + (size_t)i * VEC, gain + u * VEC);
+  }
+  for (int row = blockIdx.x * RPC + sub; row < a.rows; row += gridDim.x * RPC) {
+    const X* x = static_cast<const X*>(a.x) + (size_t)row * a.ld_x;
+    const T* gy = static_cast<const T*>(a.grad_y) + (size_t)row * a.ld_y;
+    const X* ad = a.add ? static_cast<const X*>(a.add) + (size_t)row * a.d : nullptr;
+    const float r = a.rstd[row];
+    float v[NU * VEC], g[NU * VEC];
+    float dot = 0.f;
+#pragma unroll
+    for (int u = 0; u < NU; ++u) {
+      const int i = tid + u * TPR;
+      if (i < units) {
+        load_v<VEC>(x + (size_t)i * VEC, v + u * VEC);
+        load_v<VEC>(gy + (size_t)i * VEC, g + u * VEC);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < NU; ++u) {
+      if (tid + u * TPR < units) {
+#pragma unroll
+        for (int k = 0; k < VEC; ++k) {
+          const int e = u * VEC + k;
+          acc[e] += g[e] * (v[e] * r);
+          g[e] *= gain[e];
+          dot += g[e] * v[e];
+        }
+      }
+    }
+    dot = row_sum<TPR>(dot, red);
+    const float c = dot / (float)a.d * r * r;
+    X* gx = static_cast<X*>(a.grad_x) + (size_t)row * a.d;
+#pragma unroll
+    for (int u = 0; u < NU; ++u) {
+      const int i = tid + u * TPR;
+      if (i < units) {
+        float o[VEC];
+#pragma unroll
+        for (int k = 0; k < VEC; ++k) o[k] = r * (g[u * VEC + k] - v[u * VEC + k] * c);
+        if (ad) {
+          float w[VEC];
+          load_v<VEC>(ad + (size_t)i * VEC, w);
+#pragma unroll
+          for (int k = 0; k < VEC; ++k) o[k] += w[k];
+        }
+        store_v<VEC>(gx + (size_t)i * VEC, o);
+      }
+    }
+  }
+  float* ws = a.ws + (size_t)blockIdx.x * a.d;
+  if constexpr (RPC == 1) {
+#pragma unroll
+    for (int u = 0; u < NU; ++u) {
+      const int i = tid + u * TPR;
+      if (i < units) store_v<VEC>(ws + (size_t)i * VEC, acc + u * VEC);
+    }
+  } else {
+    // the warps' shares in order, through shared memory
+    extern __shared__ float sh[];
+    for (int w = 0; w < RPC; ++w) {
+      if (sub == w) {
+#pragma unroll
+        for (int u = 0; u < NU; ++u) {
+          const int i = tid + u * TPR;
+          if (i < units) {
+#pragma unroll
+            for (int k = 0; k < VEC; ++k) {
+              float* s = sh + (size_t)i * VEC + k;
+              *s = (w ? *s : 0.f) + acc[u * VEC + k];
+            }
+          }
+        }
+      }
+      __syncthreads();
+    }
+    for (int i = threadIdx.x; i < a.d; i += kNormThreads) ws[i] = sh[i];
+  }
+}
+
+// Columns of ws[parts][d] added up: 32 columns and 32 part groups per CTA.
+template <typename T>
+__global__ void __launch_bounds__(1024) rms_gain_kernel(const float* ws, int parts, int d, T* out) {
+  griddep_launch();
+  griddep_wait();
+  __shared__ float sh[32][33];
+  const int lane = threadIdx.x & 31, g = threadIdx.x >> 5;
+  const int c = blockIdx.x * 32 + lane;
+  float s = 0.f;
+  if (c < d)
+#pragma unroll 8
+    for (int p = g; p < parts; p += 32) s += ws[(size_t)p * d + c];
+  sh[g][lane] = s;
+  __syncthreads();
+  // warp g adds up column g
+  s = sh[lane][g];
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  if (lane == 0 && blockIdx.x * 32 + g < d) out[blockIdx.x * 32 + g] = from_f<T>(s);
+}
+
+// ------------------------------------------------------------------------------------------
+// Embedding
+// ------------------------------------------------------------------------------------------
+// One warp per row; 8 elements per lane and turn.  A negative id gives a row of zeros.
+template <typename T, typename O, bool VECT>
+__global__ void __launch_bounds__(256) embed_kernel(EmbedArgs a) {
+  griddep_launch();
+  griddep_wait();
+  const int lane = threadIdx.x & 31;
+  const int row = blockIdx.x * 8 + (threadIdx.x >> 5);
+  if (row >= a.rows) return;
+  const int id = a.ids[row];
+  const bool on = id >= 0 && id < a.n_emb;
+  if (id >= a.n_emb && a.status && lane == 0) atomicOr(a.status, kStatusBounds);
+  const T* t = static_cast<const T*>(a.table) + (size_t)(on ? id : 0) * a.ld_table;
+  O* o = static_cast<O*>(a.out) + (size_t)row * a.d;
+  if constexpr (VECT) {
+#pragma unroll 4
+    for (int c = lane * 8; c < a.d; c += 256) {
+      float v[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[k] = 0.f;
+      if (on) {
+        load4(t + c, v);
+        load4(t + c + 4, v + 4);
+      }
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[k] *= a.scale;
+      store4(o + c, v);
+      store4(o + c + 4, v + 4);
+    }
+  } else {
+    for (int c = lane; c < a.d; c += 32) o[c] = from_f<O>(on ? to_f<T>(t[c]) * a.scale : 0.f);
+  }
+}
+
+// Sorting (id, row) pairs as 64-bit words: all different, so any sorting method is a stable one
+// and the sums below always add a token's rows in the same order.
+constexpr int kChunk = 2048, kWays = 8;
+
+// Each CTA sorts one chunk of kChunk words in shared memory (bitonic network).
+__global__ void __launch_bounds__(1024) embed_sort_kernel(const int* ids, int n, int n_emb,
+                                                          unsigned long long* out,
+                                                          uint32_t* status) {
+  griddep_launch();
+  griddep_wait();
+  __shared__ unsigned long long s[kChunk];
+  const int base = blockIdx.x * kChunk;
+  for (int i = threadIdx.x; i < kChunk; i += 1024) {
+    const int r = base + i;
+    unsigned key = 0xffffffffu;            // behind every id
+    if (r < n) {
+      const int id = ids[r];
+      if (id >= 0 && id < n_emb) key = (unsigned)id;
+      else {
+        key = (unsigned)n_emb;             // takes no part
+        if (id >= n_emb && status) atomicOr(status, kStatusBounds);
+      }
+    }
+    s[i] = ((unsigned long long)key << 32) | (unsigned)r;
+  }
+  __syncthreads();
+  for (int k = 2; k <= kChunk; k <<= 1)
+    for (int j = k >> 1; j > 0; j >>= 1) {
+      const int t = threadIdx.x;
+      const int i = ((t & ~(j - 1)) << 1) | (t & (j - 1)), l = i | j;
+      const unsigned long long x = s[i], y = s[l];
+      if ((x > y) == ((i & k) == 0)) {
+        s[i] = y;
+        s[l] = x;
+      }
+      __syncthreads();
+    }
+  for (int i = threadIdx.x; i < kChunk; i += 1024)
+    if (base + i < n) out[base + i] = s[i];
+}
+
+// Merge groups of kWays sorted runs of `run` words: a word's place is its place in its own run
+// plus the number of smaller words in each of the others, found by one lane per run.
+__global__ void __launch_bounds__(256) embed_merge_kernel(const unsigned long long* in, int n,
+                                                          int run, unsigned long long* out) {
+  griddep_launch();
+  griddep_wait();
+  const long long t = (long long)blockIdx.x * 256 + threadIdx.x;
+  const int way = (int)(t % kWays);
+  const long long i = t / kWays;
+  const bool in_range = i < n;
+  const unsigned long long x = in_range ? in[i] : 0;
+  const long long group = i / ((long long)run * kWays) * run * kWays;
+  const long long lo0 = group + (long long)way * run;
+  int rank = 0;
+  if (in_range && lo0 < n) {
+    if (i >= lo0 && i < lo0 + run) {
+      rank = (int)(i - lo0);
+    } else {
+      const unsigned long long* b = in + lo0;
+      int lo = 0, hi = (int)min((long long)run, n - lo0);
+      while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if (b[mid] < x) lo = mid + 1;
+        else hi = mid;
+      }
+      rank = lo;
+    }
+  }
+#pragma unroll
+  for (int o = kWays / 2; o > 0; o >>= 1) rank += __shfl_xor_sync(0xffffffffu, rank, o);
+  if (in_range && way == 0) out[group + rank] = x;
+}
+
+struct EmbedGradArgs {
+  EmbedArgs e;
+  const unsigned long long* list;   // sorted (id, row); id n_emb: takes no part
+  float* part;                      // [pieces][2][d]
+  int per, pieces, slabs;           // list entries per piece; 256-column slabs
+  int sum_ctas;                     // CTAs that sum; the others clear rows without tokens
+};
+
+constexpr int kZeroIds = 32;        // table rows that one clearing CTA looks at
+
+SMDM_DEV int key_of(unsigned long long w) { return (int)(w >> 32); }
+
+// Sum the rows of every token.  One warp takes `per` sorted entries and 256 columns; a run of
+// one token that lies within the piece is written at once, rounded from its fp32 sum; one that
+// goes on in the next piece leaves its part in slot 1 of the piece where it starts and in slot 0
+// of every later one (embed_join_kernel adds them up in order).  The remaining CTAs clear the
+// rows of tokens that do not occur.
+template <typename T, typename O, bool VECT>
+__global__ void __launch_bounds__(256) embed_sum_kernel(EmbedGradArgs a) {
+  griddep_launch();
+  griddep_wait();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int n = a.e.rows, d = a.e.d;
+  T* table = static_cast<T*>(a.e.grad_table);
+  if ((int)blockIdx.x >= a.sum_ctas) {
+    __shared__ unsigned s_present;
+    const int v0 = (blockIdx.x - a.sum_ctas) * kZeroIds;
+    if (warp == 0) {
+      const unsigned long long x = (unsigned long long)(unsigned)(v0 + lane) << 32;
+      int lo = 0, hi = n;
+      while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if (a.list[mid] < x) lo = mid + 1;
+        else hi = mid;
+      }
+      const bool here = lo < n && key_of(a.list[lo]) == v0 + lane;
+      const unsigned m = __ballot_sync(0xffffffffu, here);
+      if (lane == 0) s_present = m;
+    }
+    __syncthreads();
+    const unsigned present = s_present;
+    for (int i = warp; i < kZeroIds; i += 8) {
+      if (v0 + i >= a.e.n_emb || ((present >> i) & 1u)) continue;
+      T* o = table + (size_t)(v0 + i) * d;
+      if constexpr (VECT) {
+        const float z[4] = {0.f, 0.f, 0.f, 0.f};
+        for (int c = lane * 4; c < d; c += 128) store4(o + c, z);
+      } else {
+        for (int c = lane; c < d; c += 32) o[c] = from_f<T>(0.f);
+      }
+    }
+    return;
+  }
+  const int job = blockIdx.x * 8 + warp;
+  const int piece = job / a.slabs, slab = job % a.slabs;
+  if (piece >= a.pieces) return;
+  const int i0 = piece * a.per, i1 = min(n, i0 + a.per);
+  // this lane's columns: 8 in a row, or 8 that lie 32 apart
+  auto col = [&](int j) { return VECT ? slab * 256 + lane * 8 + j : slab * 256 + j * 32 + lane; };
+  float acc[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) acc[j] = 0.f;
+  const O* g = static_cast<const O*>(a.e.grad_out);
+  const int prev_key = i0 > 0 ? key_of(a.list[i0 - 1]) : -1;
+  const int next_key = i1 < n ? key_of(a.list[i1]) : -1;
+  int run_first = 1;       // the current run is the piece's first
+  constexpr int kAhead = 8;
+  for (int b = i0; b < i1; b += 32) {
+    const unsigned long long mine = b + lane < i1 ? a.list[b + lane] : 0;
+    const int cnt = min(32, i1 - b);
+    // the key that follows this batch of entries
+    const int after = b + 32 < i1 ? key_of(a.list[b + 32]) : next_key;
+    for (int h = 0; h < cnt; h += kAhead) {
+      float v[kAhead][8];
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
+        const unsigned long long w = __shfl_sync(0xffffffffu, mine, (h + k) & 31);
+        if (h + k < cnt && key_of(w) < a.e.n_emb) {
+          const O* r = g + (size_t)(unsigned)w * a.e.ld_grad;
+          if constexpr (VECT) {
+            if (col(0) < d) {
+              load4(r + col(0), v[k]);
+              load4(r + col(0) + 4, v[k] + 4);
+            }
+          } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[k][j] = col(j) < d ? to_f<O>(r[col(j)]) : 0.f;
+          }
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
+        const int key = key_of(__shfl_sync(0xffffffffu, mine, (h + k) & 31));
+        const int nk = key_of(__shfl_sync(0xffffffffu, mine, (h + k + 1) & 31));
+        if (h + k >= cnt || key >= a.e.n_emb) continue;      // uniform over the warp
+#pragma unroll
+        for (int j = 0; j < 8; ++j) acc[j] += v[k][j];
+        const bool last = h + k + 1 >= cnt;
+        const int following = last ? after : nk;
+        const bool piece_end = last && b + 32 >= i1;
+        if (following == key && !piece_end) continue;        // the run goes on
+        const bool from_before = run_first && key == prev_key;
+        const bool goes_on = piece_end && following == key;
+        if (from_before || goes_on) {
+          float* p = a.part + ((size_t)piece * 2 + (from_before ? 0 : 1)) * d;
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            if (col(j) < d) p[col(j)] = acc[j];
+        } else {
+          T* o = table + (size_t)key * d;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) acc[j] *= a.e.scale;
+          if constexpr (VECT) {
+            if (col(0) < d) {
+              store4(o + col(0), acc);
+              store4(o + col(0) + 4, acc + 4);
+            }
+          } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              if (col(j) < d) o[col(j)] = from_f<T>(acc[j]);
+          }
+        }
+        run_first = 0;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) acc[j] = 0.f;
+      }
+    }
+  }
+}
+
+// Add up the parts of every run that starts in one piece and goes on in the next: eight groups
+// of warps take every eighth part in order, then the groups are added in order.  Every CTA finds
+// all such runs itself (pieces of 256 threads at a time) and takes every gridDim-th (run,
+// column block); a CTA per piece would mostly start CTAs that have nothing to do.
+template <typename T, int VEC>
+__global__ void __launch_bounds__(256) embed_join_kernel(EmbedGradArgs a) {
+  griddep_launch();
+  griddep_wait();
+  constexpr int kCols = 32 * VEC;
+  __shared__ int s_run[256];
+  __shared__ int s_warp[8];
+  __shared__ float sh[8][kCols];
+  const int d = a.e.d;
+  const int lane = threadIdx.x & 31, grp = threadIdx.x >> 5;
+  const int blocks = (d + kCols - 1) / kCols;
+  T* table = static_cast<T*>(a.e.grad_table);
+  long long job0 = 0;                      // jobs of the earlier batches of pieces
+  for (int p0 = 0; p0 + 1 < a.pieces; p0 += 256) {
+    const int p = p0 + threadIdx.x;
+    bool starts = false;
+    if (p + 1 < a.pieces) {
+      const int i0 = p * a.per, i1 = i0 + a.per;
+      const int key = key_of(a.list[i1 - 1]);
+      starts = key < a.e.n_emb && key_of(a.list[i1]) == key &&
+               !(i0 > 0 && key_of(a.list[i0 - 1]) == key);
+    }
+    const unsigned m = __ballot_sync(0xffffffffu, starts);
+    __syncthreads();                       // the previous batch's list has been read
+    if (lane == 0) s_warp[grp] = __popc(m);
+    __syncthreads();
+    int at = 0, runs = 0;
+    for (int w = 0; w < 8; ++w) {
+      if (w < grp) at += s_warp[w];
+      runs += s_warp[w];
+    }
+    if (starts) s_run[at + __popc(m & ((1u << lane) - 1u))] = p;
+    __syncthreads();
+    const long long jobs = (long long)runs * blocks;
+    // this CTA's jobs of the batch
+    long long j = ((long long)blockIdx.x - job0 % gridDim.x + gridDim.x) % gridDim.x;
+    for (; j < jobs; j += gridDim.x) {
+      const int first = s_run[j / blocks];
+      const int c = (int)(j % blocks) * kCols + lane * VEC;
+      const int key = key_of(a.list[(size_t)(first + 1) * a.per]);
+      int cnt = 0;                         // later pieces that begin with this token
+      while (true) {
+        const int q = first + 1 + cnt + threadIdx.x;
+        const int k = __syncthreads_count(q < a.pieces && key_of(a.list[(size_t)q * a.per]) == key);
+        cnt += k;
+        if (k < 256) break;
+      }
+      // part 0: slot 1 of the first piece; part k: slot 0 of the k-th piece after it
+      float s[VEC];
+#pragma unroll
+      for (int k = 0; k < VEC; ++k) s[k] = 0.f;
+      if (c < d) {
+#pragma unroll 4
+        for (int k = grp; k <= cnt; k += 8) {
+          float v[VEC];
+          load_v<VEC>(a.part + ((size_t)(first + k) * 2 + (k == 0 ? 1 : 0)) * d + c, v);
+#pragma unroll
+          for (int e = 0; e < VEC; ++e) s[e] += v[e];
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) sh[grp][lane * VEC + e] = s[e];
+      __syncthreads();
+      if (threadIdx.x < kCols) {
+        const int cc = (int)(j % blocks) * kCols + threadIdx.x;
+        float t = 0.f;
+        for (int g = 0; g < 8; ++g) t += sh[g][threadIdx.x];
+        if (cc < d) table[(size_t)key * d + cc] = from_f<T>(t * a.e.scale);
+      }
+      __syncthreads();
+    }
+    job0 += jobs;
+  }
+}
+
+__global__ void __launch_bounds__(256) gather_f32_kernel(const float* x, const int* index, int rows,
+                                                         int n, int d, float* out,
+                                                         uint32_t* status) {
+  griddep_launch();
+  griddep_wait();
+  const int lane = threadIdx.x & 31;
+  const int row = blockIdx.x * 8 + (threadIdx.x >> 5);
+  if (row >= rows) return;
+  int r = index[row];
+  if (r < 0 || r >= n) {
+    if (lane == 0 && status) atomicOr(status, kStatusBounds);
+    r = 0;
+  }
+  for (int c = lane * 4; c < d; c += 128)
+    *reinterpret_cast<float4*>(out + (size_t)row * d + c) =
+        *reinterpret_cast<const float4*>(x + (size_t)r * d + c);
+}
+
+// ------------------------------------------------------------------------------------------
+// Host side
+// ------------------------------------------------------------------------------------------
+size_t up_to(size_t x, size_t a) { return (x + a - 1) / a * a; }
+
+// Threads per row: a warp up to 1024 elements (32 per lane), then the whole CTA.
+int norm_tpr(int d) { return d <= 1024 ? 32 : 256; }
+
+int norm_grad_ctas(int rows, int d) {
+  const int tpr = norm_tpr(d), rpc = std::max(1, 256 / tpr);
+  return std::min((rows + rpc - 1) / rpc, device_sms() * 2);
+}
+
+template <typename X, typename T, int TPR, int VEC, int NU>
+cudaError_t rms_one(const RmsArgs& a, bool grad, cudaStream_t st) {
+  constexpr int B = kNormThreads, RPC = B / TPR;
+  if (!grad)
+    return launch_pdl(train_rms_kernel<X, T, TPR, VEC, NU>, dim3((a.rows + RPC - 1) / RPC),
+                      dim3(B), 0, st, 1, a);
+  return launch_pdl(train_rms_grad_kernel<X, T, TPR, VEC, NU>, dim3(norm_grad_ctas(a.rows, a.d)),
+                    dim3(B), RPC > 1 ? (size_t)a.d * 4 : 0, st, 1, a);
+}
+
+template <typename X, typename T>
+cudaError_t rms_types(const RmsArgs& a, bool grad, cudaStream_t st) {
+  // four elements at a time where every row starts on their alignment
+  bool v4 = a.d % 4 == 0 && a.ld_x % 4 == 0 && a.ld_y % 4 == 0 && aligned(a.x, 4 * sizeof(X)) &&
+            aligned(a.gain, 4 * sizeof(T));
+  if (!grad) v4 = v4 && aligned(a.y, 4 * sizeof(T));
+  else
+    v4 = v4 && aligned(a.grad_y, 4 * sizeof(T)) && aligned(a.grad_x, 4 * sizeof(X)) &&
+         aligned(a.add, 4 * sizeof(X));
+  const int tpr = norm_tpr(a.d);
+  if (v4) {
+    if (tpr == 32) {
+      return a.d <= 512 ? rms_one<X, T, 32, 4, 4>(a, grad, st) : rms_one<X, T, 32, 4, 8>(a, grad, st);
+    }
+    return a.d <= 4096 ? rms_one<X, T, 256, 4, 4>(a, grad, st)
+                       : rms_one<X, T, 256, 4, 8>(a, grad, st);
+  }
+  if (tpr == 32) return rms_one<X, T, 32, 1, 32>(a, grad, st);
+  return rms_one<X, T, 256, 1, 32>(a, grad, st);
+}
+
+cudaError_t rms_any(const RmsArgs& a, bool grad, cudaStream_t st) {
+  if (a.x_f32) return a.f32 ? rms_types<float, float>(a, grad, st)
+                            : rms_types<float, __nv_bfloat16>(a, grad, st);
+  return a.f32 ? rms_types<__nv_bfloat16, float>(a, grad, st)
+               : rms_types<__nv_bfloat16, __nv_bfloat16>(a, grad, st);
+}
+
+struct EmbedPlan {
+  int chunks, per, pieces, slabs;
+  size_t list[2], part, total;
+};
+
+EmbedPlan embed_plan(int rows, int d) {
+  EmbedPlan p{};
+  p.chunks = (rows + kChunk - 1) / kChunk;
+  p.slabs = (d + 255) / 256;
+  // entries of one warp: enough warps to fill the device, few enough parts
+  const long long warps = (long long)device_sms() * 32;
+  p.per = 8;
+  while (p.per < 128 && (long long)rows * p.slabs / (2 * p.per) >= warps) p.per *= 2;
+  p.pieces = (rows + p.per - 1) / p.per;
+  size_t off = 0;
+  auto take = [&](size_t b) {
+    const size_t o = off;
+    off = up_to(off + b, 256);
+    return o;
+  };
+  p.list[0] = take((size_t)rows * 8);
+  p.list[1] = take(p.chunks > 1 ? (size_t)rows * 8 : 0);
+  p.part = take((size_t)p.pieces * 2 * d * 4);
+  p.total = off;
+  return p;
+}
+
+template <typename T, typename O>
+cudaError_t embed_types(const EmbedArgs& a, cudaStream_t st) {
+  const bool v = a.d % 8 == 0 && a.ld_table % 8 == 0 && aligned(a.table, 16) && aligned(a.out, 16);
+  const dim3 grid((a.rows + 7) / 8);
+  return v ? launch_pdl(embed_kernel<T, O, true>, grid, dim3(256), 0, st, 1, a)
+           : launch_pdl(embed_kernel<T, O, false>, grid, dim3(256), 0, st, 1, a);
+}
+
+template <typename T, typename O>
+cudaError_t embed_grad_types(const EmbedGradArgs& g, cudaStream_t st) {
+  const EmbedArgs& a = g.e;
+  const bool v = a.d % 8 == 0 && a.ld_grad % 8 == 0 && aligned(a.grad_out, 16) &&
+                 aligned(a.grad_table, 16);
+  const dim3 grid(g.sum_ctas + (a.n_emb + kZeroIds - 1) / kZeroIds);
+  const cudaError_t e = v ? launch_pdl(embed_sum_kernel<T, O, true>, grid, dim3(256), 0, st, 1, g)
+                          : launch_pdl(embed_sum_kernel<T, O, false>, grid, dim3(256), 0, st, 1, g);
+  if (e != cudaSuccess || g.pieces < 2) return e;
+  const dim3 jgrid(device_sms() * 2);
+  return a.d % 4 == 0 ? launch_pdl(embed_join_kernel<T, 4>, jgrid, dim3(256), 0, st, 1, g)
+                      : launch_pdl(embed_join_kernel<T, 1>, jgrid, dim3(256), 0, st, 1, g);
+}
+
+}  // namespace
+
+cudaError_t launch_train_rmsnorm(const RmsArgs& a, cudaStream_t st) { return rms_any(a, false, st); }
+
+size_t rmsnorm_grad_bytes(int rows, int d) {
+  return std::max<size_t>(256, up_to((size_t)norm_grad_ctas(rows, d) * d * 4, 256));
+}
+
+cudaError_t launch_train_rmsnorm_grad(const RmsArgs& a, cudaStream_t st) {
+  const cudaError_t e = rms_any(a, true, st);
+  if (e != cudaSuccess) return e;
+  const int parts = norm_grad_ctas(a.rows, a.d);
+  const dim3 grid((a.d + 31) / 32);
+  return a.f32 ? launch_pdl(rms_gain_kernel<float>, grid, dim3(1024), 0, st, 1,
+                            (const float*)a.ws, parts, a.d, static_cast<float*>(a.grad_gain))
+               : launch_pdl(rms_gain_kernel<__nv_bfloat16>, grid, dim3(1024), 0, st, 1,
+                            (const float*)a.ws, parts, a.d,
+                            static_cast<__nv_bfloat16*>(a.grad_gain));
+}
+
+cudaError_t launch_embed(const EmbedArgs& a, cudaStream_t st) {
+  if (a.f32) return a.out_f32 ? embed_types<float, float>(a, st)
+                              : embed_types<float, __nv_bfloat16>(a, st);
+  return a.out_f32 ? embed_types<__nv_bfloat16, float>(a, st)
+                   : embed_types<__nv_bfloat16, __nv_bfloat16>(a, st);
+}
+
+size_t embed_grad_bytes(int rows, int d, int n_emb) {
+  (void)n_emb;
+  return std::max<size_t>(256, embed_plan(rows, d).total);
+}
+
+cudaError_t launch_embed_grad(const EmbedArgs& a, cudaStream_t st) {
+  const EmbedPlan p = embed_plan(a.rows, a.d);
+  uint8_t* ws = static_cast<uint8_t*>(a.ws);
+  unsigned long long* list[2] = {reinterpret_cast<unsigned long long*>(ws + p.list[0]),
+                                 reinterpret_cast<unsigned long long*>(ws + p.list[1])};
+  cudaError_t e = launch_pdl(embed_sort_kernel, dim3(p.chunks), dim3(1024), 0, st, 1, a.ids, a.rows,
+                             a.n_emb, list[0], a.status);
+  if (e != cudaSuccess) return e;
+  int cur = 0;
+  for (long long run = kChunk; run < a.rows; run *= kWays, cur ^= 1) {
+    const long long threads = (long long)a.rows * kWays;
+    e = launch_pdl(embed_merge_kernel, dim3((unsigned)((threads + 255) / 256)), dim3(256), 0, st, 1,
+                   (const unsigned long long*)list[cur], a.rows, (int)run, list[cur ^ 1]);
+    if (e != cudaSuccess) return e;
+  }
+  EmbedGradArgs g{};
+  g.e = a;
+  g.list = list[cur];
+  g.part = reinterpret_cast<float*>(ws + p.part);
+  g.per = p.per;
+  g.pieces = p.pieces;
+  g.slabs = p.slabs;
+  g.sum_ctas = (int)(((long long)p.pieces * p.slabs + 7) / 8);
+  if (a.f32) return a.out_f32 ? embed_grad_types<float, float>(g, st)
+                              : embed_grad_types<float, __nv_bfloat16>(g, st);
+  return a.out_f32 ? embed_grad_types<__nv_bfloat16, float>(g, st)
+                   : embed_grad_types<__nv_bfloat16, __nv_bfloat16>(g, st);
+}
+
+cudaError_t launch_gather_f32(const float* x, const int* index, int rows, int n, int d, float* out,
+                              uint32_t* status, cudaStream_t st) {
+  return launch_pdl(gather_f32_kernel, dim3((rows + 7) / 8), dim3(256), 0, st, 1, x, index, rows, n,
+                    d, out, status);
+}
+
+}  // namespace smdm

@@ -1,0 +1,1239 @@
+// Cross entropy of the LM head without the logits, and its gradient.
+//
+//   z_rv = h_r . w_v          lse_r = log sum_v exp(z_rv)         nll_r = lse_r - z_r,t(r)
+//   D_rv = g_r (exp(z_rv - lse_r) - [v = t(r)])     dH = D W      dW = D^T H
+//
+// The loss makes one product (2 R V d operations, R = rows that take part) and keeps one
+// (maximum, sum of exponentials) pair per row and column group instead of the logits.  The
+// gradient makes the product again, piece of the vocabulary by piece, writes D for the piece
+// (bf16, at most kPieceBytes of it), and multiplies it from both sides: 6 R V d operations.
+//
+// Rows with a negative target are left out before the first product: `head_rows_kernel` lists the
+// others and copies them together, so that they cost nothing and what they hold (NaN, garbage
+// of a padded batch) reaches no sum.  When every row takes part the rows are read in place.
+//
+// One kernel does all products (`head_gemm_kernel`): persistent CTAs (or pairs, cta_group::2),
+// 128 x BN (256 x 256) tiles, TMA loads into an mbarrier ring, tcgen05.mma into one of two
+// accumulators in tensor memory while eight warps drain the other one.  K-major and MN-major
+// operands differ in their boxes and descriptors only, so D and W are multiplied as they lie.
+//
+// bf16: products of the given values, fp32 sums.  D is rounded to bf16 (half a step, 2^-8
+// relative to each of its values), the width of the gradients that come out of it.
+// fp32: every operand is split into three bf16 parts (8 + 8 + 8 significant bits) and the six
+// products that reach 2^-16 of the largest are summed, smallest first (2^-23 is left out).
+#include "head.h"
+
+#include <algorithm>
+
+#include "tensormap.h"
+
+namespace smdm {
+
+namespace {
+
+constexpr int kThreads = 320;        // producer warp, MMA warp, 8 epilogue warps
+constexpr int kEpiWarps = 8;
+constexpr int kABytes = 128 * 128;   // 128 rows x 64 bf16
+constexpr int kStagingBytes = kEpiWarps * 4096;
+constexpr int kMaxStages = 8;
+constexpr int kSmemLimit = 227 * 1024;
+constexpr size_t kPieceBytes = size_t(256) << 20;   // D (and split weights) held at once
+constexpr float kLog2e = 1.4426950408889634f;
+
+enum Mode : int { kLoss = 0, kDlog = 1, kGrad = 2 };
+
+// Device-side counts, written by head_rows_kernel.
+struct HeadMeta {
+  int n;       // rows that take part
+  int dense;   // 1: all of them do, and the caller's hidden is read in place
+};
+
+struct HeadDev {
+  const HeadMeta* meta;
+  const int* row_idx;       // row that takes part -> row of the caller's tensors
+  const int* target;
+  int d, v0, vc;            // width; first column and columns of this piece
+  int w_row0;               // row of the weight map that holds column v0
+  int terms;                // 1 (bf16) or 6 (fp32 as three bf16 parts)
+  int h_plane, w_plane, d_plane;   // rows between the parts of H, W, D in their maps
+  int a_box;                // rows of A that one box brings (K-major H)
+  int nstages, staging_off, bar_off;
+  // loss
+  float2* part;             // [column group][r_pad]
+  int part0;                // first column group of this piece
+  int r_pad;
+  float* tlogit;            // [r_pad]
+  // D
+  const float* lse;
+  const float* grad_nll;
+  __nv_bfloat16* dlog;      // [parts][r_pad][ld_dlog]
+  int ld_dlog;
+  // gradients
+  int do_h, do_w, splits;
+  float* acc;               // [splits][r_pad][d_pad] or null: dH is written directly
+  int acc_add;              // add to acc (a later piece)
+  int d_pad;
+  void* out_h;              // [rows][d]
+  void* out_w;              // row v0 of [vocab][d]
+  int vec_ok;               // output rows start on 16-byte boundaries
+  uint32_t* status;
+};
+
+__host__ __device__ constexpr uint32_t idesc_bf16(int M, int N, int a_mn, int b_mn) {
+  return idesc_f16(M, N, a_mn, b_mn) | (1u << 7) | (1u << 10);   // A and B formats: bf16
+}
+
+// One unit of work: a tile of a product and the K range of it.
+struct Unit {
+  int kind;      // 0: H x W^T (loss, D); 1: dH; 2: dW
+  int m0, n0;    // first row / column
+  int k0, nk;    // first 64-wide K chunk, chunks
+  int split;
+};
+
+constexpr int kTileCost = 6;
+
+// The work of one slot (CTA or pair) p of P.  Loss and D: tiles round robin, in groups of 16 row
+// tiles so that a group's rows stay in L2 while the weights pass once.  Gradients: the dH units
+// round robin, then the dW tiles so that every slot ends at about the same number of K chunks
+// (a tile's fixed cost counted as kTileCost chunks).
+template <int kMode, int CG, int BN>
+struct Schedule {
+  int p, P, n, kc, mt, nt;
+  int kw, nh, nw, mt_w, nt_d, my_h, qa, my_w, n_rem;
+  int kch, kper;
+
+  SMDM_DEV Schedule(const HeadDev& a, int n_, int p_, int P_) : p(p_), P(P_), n(n_) {
+    constexpr int MT = 128 * CG;
+    mt = (n + MT - 1) / MT;
+    if constexpr (kMode != kGrad) {
+      kc = (a.d + 63) >> 6;
+      nt = (a.vc + BN - 1) / BN;
+    } else {
+      nt_d = (a.d + BN - 1) / BN;
+      kch = (a.vc + 63) >> 6;
+      kper = (kch + a.splits - 1) / a.splits;
+      kw = (n + 63) >> 6;
+      mt_w = (a.vc + MT - 1) / MT;
+      nh = a.do_h ? mt * nt_d * a.splits : 0;
+      nw = a.do_w ? mt_w * nt_d : 0;
+      const int c = nh / P;
+      n_rem = nh % P;                       // slots with c + 1 dH units
+      my_h = c + (p < n_rem ? 1 : 0);
+      // finishing time T of all slots, raised from the mean until every dW tile fits.  In fp32:
+      // every thread of the grid computes the same values, and rounding only moves the balance.
+      const float ch = (float)kper * a.terms + kTileCost, cw = (float)kw * a.terms + kTileCost;
+      auto fit = [&](float T, float used) {
+        return T > used ? (int)fminf(__fdividef(T - used, cw), (float)nw) : 0;
+      };
+      float T = ((float)nh * ch + (float)nw * cw) / (float)P;
+      int qb;
+      while (true) {
+        qa = fit(T, (c + 1) * ch);          // dW tiles of the slots with c + 1 dH units
+        qb = fit(T, c * ch);
+        if ((long long)n_rem * qa + (long long)(P - n_rem) * qb >= nw) break;
+        T += 0.25f * cw + T * 1e-6f;
+      }
+      my_w = p < n_rem ? qa : qb;
+    }
+  }
+
+  SMDM_DEV bool get(const HeadDev& a, int i, Unit& u) const {
+    constexpr int MT = 128 * CG;
+    if constexpr (kMode != kGrad) {
+      const long long t = (long long)p + (long long)i * P;
+      if (t >= (long long)mt * nt) return false;
+      constexpr int G = 16;
+      const int per = G * nt;
+      const int g = (int)(t / per), in = (int)(t % per);
+      const int gm = min(G, mt - g * G);
+      u.kind = 0;
+      u.m0 = (g * G + in % gm) * MT;
+      u.n0 = (in / gm) * BN;
+      u.k0 = 0;
+      u.nk = kc;
+      u.split = 0;
+      return true;
+    } else {
+      if (i < my_h) {
+        const int t = p + i * P;
+        const int tile = t / a.splits;
+        u.kind = 1;
+        u.split = t % a.splits;
+        u.m0 = (tile % mt) * MT;
+        u.n0 = (tile / mt) * BN;
+        u.k0 = u.split * kper;
+        u.nk = max(0, min(kper, kch - u.k0));
+        return true;
+      }
+      const int t = i - my_h;
+      if (t >= my_w) return false;
+      // rounds in which every slot has a tile, then those of the slots with fewer dH units
+      const int q = t < qa ? t * P + p : qa * P + (t - qa) * (P - n_rem) + (p - n_rem);
+      if (q >= nw) return false;
+      u.kind = 2;
+      u.split = 0;
+      u.m0 = (q / nt_d) * MT;
+      u.n0 = (q % nt_d) * BN;
+      u.k0 = 0;
+      u.nk = kw;
+      return true;
+    }
+  }
+};
+
+// The two parts' planes of term t, smallest products first.
+SMDM_DEV int term_a(int terms, int t) { return terms == 1 ? 0 : (0x021010 >> (4 * (5 - t))) & 15; }
+SMDM_DEV int term_b(int terms, int t) { return terms == 1 ? 0 : (0x201100 >> (4 * (5 - t))) & 15; }
+
+// x = p0 + p1 + p2 with bf16 parts; an infinity or NaN stays in the first part alone.
+SMDM_DEV void split3(float x, __nv_bfloat16& p0, __nv_bfloat16& p1, __nv_bfloat16& p2) {
+  p0 = __float2bfloat16_rn(x);
+  float r = x - __bfloat162float(p0);
+  if (!(fabsf(x) <= 3.3895314e38f)) r = 0.f;
+  p1 = __float2bfloat16_rn(r);
+  p2 = __float2bfloat16_rn(r - __bfloat162float(p1));
+}
+
+SMDM_DEV float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+SMDM_DEV uint32_t pack_bf16(float a, float b) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// A warp's 32 rows x 128 (or 64) bytes, swizzled by row so that neither the writes (a lane per
+// row) nor the reads (lanes along a row) collide on banks.
+template <int RB>
+SMDM_DEV uint8_t* stage_at(uint8_t* st, int row, int chunk) {
+  constexpr int C = RB / 16;
+  return st + row * RB + ((chunk ^ ((RB == 128 ? row : row >> 1) & (C - 1))) << 4);
+}
+
+// Write the staged rows to global memory: RB bytes of every row, at column `col` (elements) of
+// the row that `row_ptr(row)` gives (null: skip), of which `cols` columns exist.
+template <typename T, int RB, typename RowPtr>
+SMDM_DEV void flush_rows(uint8_t* st, int lane, int col, int cols, bool vec, RowPtr row_ptr) {
+  constexpr int C = RB / 16, E = 16 / (int)sizeof(T), RPI = 32 / C;
+  __syncwarp();
+#pragma unroll
+  for (int it = 0; it < C; ++it) {
+    const int row = it * RPI + lane / C, chunk = lane % C;
+    const int c0 = col + chunk * E;
+    T* dst = row_ptr(row);
+    if (dst && c0 < cols) {
+      const uint4 v = *reinterpret_cast<const uint4*>(stage_at<RB>(st, row, chunk));
+      if (vec && c0 + E <= cols) {
+        *reinterpret_cast<uint4*>(dst + c0) = v;
+      } else {
+        const T* e = reinterpret_cast<const T*>(&v);
+#pragma unroll
+        for (int k = 0; k < E; ++k)
+          if (c0 + k < cols) dst[c0 + k] = e[k];
+      }
+    }
+  }
+  __syncwarp();
+}
+
+// 32 values of this lane's row -> staging chunks starting at chunk c0.
+template <int RB>
+SMDM_DEV void stage_bf16(uint8_t* st, int lane, int c0, const float* v) {
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    uint4 w;
+    w.x = pack_bf16(v[8 * k + 0], v[8 * k + 1]);
+    w.y = pack_bf16(v[8 * k + 2], v[8 * k + 3]);
+    w.z = pack_bf16(v[8 * k + 4], v[8 * k + 5]);
+    w.w = pack_bf16(v[8 * k + 6], v[8 * k + 7]);
+    *reinterpret_cast<uint4*>(stage_at<RB>(st, lane, c0 + k)) = w;
+  }
+}
+SMDM_DEV void stage_f32(uint8_t* st, int lane, const float* v) {
+#pragma unroll
+  for (int k = 0; k < 8; ++k)
+    *reinterpret_cast<float4*>(stage_at<128>(st, lane, k)) =
+        make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+}
+
+// kMode: what is computed.  CG: CTAs per tile (2: a pair on two SMs, M = 256).  BN: tile
+// columns.  F32: the outputs (and D's parts) are the fp32 path's.
+template <int kMode, int CG, int BN, bool F32>
+__global__ void __launch_bounds__(kThreads, 1)
+    head_gemm_kernel(const __grid_constant__ CUtensorMap tm_h,    // caller's hidden (K-major box)
+                     const __grid_constant__ CUtensorMap tm_hc,   // listed rows, or same box
+                     const __grid_constant__ CUtensorMap tm_w,    // weights
+                     const __grid_constant__ CUtensorMap tm_dk,   // D, K-major box
+                     const __grid_constant__ CUtensorMap tm_dm,   // D, MN-major box
+                     const HeadDev a) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~uintptr_t(1023));
+  constexpr int kBRows = BN / CG;                    // rows (columns of the product) of B here
+  constexpr int kStage = kABytes + kBRows * 128;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + a.bar_off);
+  uint64_t* full = bars;
+  uint64_t* empty = bars + kMaxStages;
+  uint64_t* acc_full = bars + 2 * kMaxStages;
+  uint64_t* acc_empty = acc_full + 2;
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(acc_empty + 2);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = CG == 2 ? cluster_ctarank() : 0u;
+  const bool leader = rank == 0;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < a.nstages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&acc_full[i], 1);
+      mbar_init(&acc_empty[i], kEpiWarps * CG);
+    }
+    *abort_flag = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(&tm_hc);
+    tma_prefetch_desc(&tm_w);
+  }
+  if constexpr (CG == 2) cluster_sync_all();
+  if (warp == 1) {
+    if constexpr (CG == 2) {
+      tmem_alloc_pair(tmem_holder, 2 * BN);
+      tmem_relinquish_pair();
+    } else {
+      tmem_alloc(tmem_holder, 2 * BN);
+      tmem_relinquish();
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tbase = *tmem_holder;
+  griddep_launch();
+  griddep_wait();
+
+  const int n = a.meta->n;
+  const bool dense = a.meta->dense != 0;
+  const Schedule<kMode, CG, BN> sch(a, n, blockIdx.x / CG, gridDim.x / CG);
+  auto lead_addr = [&](uint64_t* bar) -> uint32_t {
+    return CG == 2 ? mapa_shared(smem_u32(bar), 0) : smem_u32(bar);
+  };
+
+  if (warp == 0) {
+    if (lane == 0) {
+      const uint64_t pol = policy_evict_normal();
+      int stage = 0;
+      uint32_t phase = 0;
+      Unit u;
+      bool ok = true;
+      const CUtensorMap* th = dense ? &tm_h : &tm_hc;
+      const int h_plane = dense ? 0 : a.h_plane;
+      for (int i = 0; ok && sch.get(a, i, u); ++i) {
+        const int m0 = u.m0 + (int)rank * 128;
+        const int n0 = u.n0 + (int)rank * kBRows;
+        for (int t = 0; ok && t < a.terms; ++t) {
+          const int pa = term_a(a.terms, t), pb = term_b(a.terms, t);
+          for (int k = u.k0; k < u.k0 + u.nk; ++k) {
+            if (!mbar_wait(&empty[stage], phase ^ 1, abort_flag, a.status)) { ok = false; break; }
+            uint8_t* A = smem + stage * kStage;
+            uint8_t* B = A + kABytes;
+            const int ab = u.kind == 0 ? a.a_box * 128 : kABytes;
+            if (leader) mbar_arrive_expect_tx(&full[stage], CG * (ab + kBRows * 128));
+            const uint32_t fb = lead_addr(&full[stage]);
+            auto load = [&](uint8_t* dst, const CUtensorMap* m, int x, int y) {
+              if constexpr (CG == 2) tma_load_2d_pair(dst, m, fb, x, y, pol);
+              else tma_load_2d(dst, m, &full[stage], x, y, pol);
+            };
+            if constexpr (kMode != kGrad) {
+              load(A, th, k * 64, pa * h_plane + m0);
+              load(B, &tm_w, k * 64, a.w_row0 + pb * a.w_plane + n0);
+            } else if (u.kind == 1) {   // dH: D (K = columns, contiguous), W (N contiguous)
+              load(A, &tm_dk, k * 64, pa * a.d_plane + m0);
+#pragma unroll
+              for (int j = 0; j < kBRows / 64; ++j)
+                load(B + j * 8192, &tm_w, n0 + j * 64, a.w_row0 + pb * a.w_plane + k * 64);
+            } else {                    // dW: D (M contiguous), H (N contiguous)
+#pragma unroll
+              for (int j = 0; j < 2; ++j)
+                load(A + j * 8192, &tm_dm, m0 + j * 64, pa * a.d_plane + k * 64);
+#pragma unroll
+              for (int j = 0; j < kBRows / 64; ++j)
+                load(B + j * 8192, th, n0 + j * 64, pb * h_plane + k * 64);
+            }
+            if (++stage == a.nstages) { stage = 0; phase ^= 1; }
+          }
+        }
+      }
+      if constexpr (CG == 2) {
+        // The pair's MMA completions arrive on these barriers from the first CTA: wait until
+        // every stage is released so that no arrival lands after this CTA has exited.
+        for (int s = 0; ok && s < a.nstages; ++s) {
+          if (!mbar_wait(&empty[stage], phase ^ 1, abort_flag, a.status)) break;
+          if (++stage == a.nstages) { stage = 0; phase ^= 1; }
+        }
+      }
+    }
+  } else if (warp == 1) {
+    if (lane == 0 && leader) {
+      int stage = 0, acc = 0;
+      uint32_t phase = 0, acc_phase = 0;
+      Unit u;
+      bool ok = true;
+      for (int i = 0; ok && sch.get(a, i, u); ++i) {
+        const int total = u.nk * a.terms;
+        if (total == 0) continue;          // nothing to sum: the epilogue writes zeros
+        if (!mbar_wait(&acc_empty[acc], acc_phase ^ 1, abort_flag, a.status)) break;
+        tc_fence_after();
+        const uint32_t d = tbase + acc * BN;
+        const int a_mn = u.kind == 2, b_mn = u.kind != 0;
+        const uint32_t idesc = idesc_bf16(128 * CG, BN, a_mn, b_mn);
+        // K-major: the next 16 K values lie 32 bytes on; MN-major: 16 rows of 128 bytes on,
+        // with 8192 bytes between 64-element runs along M or N
+        const uint32_t a_lbo = a_mn ? 8192 : 16, b_lbo = b_mn ? 8192 : 16;
+        const uint32_t a_step = a_mn ? 2048 >> 4 : 32 >> 4, b_step = b_mn ? 2048 >> 4 : 32 >> 4;
+        for (int c = 0; c < total; ++c) {
+          if (!mbar_wait(&full[stage], phase, abort_flag, a.status)) { ok = false; break; }
+          tc_fence_after();
+          const uint32_t a_addr = smem_u32(smem + stage * kStage);
+          const uint64_t ad = sdesc_sw128(a_addr, a_lbo, 1024);
+          const uint64_t bd = sdesc_sw128(a_addr + kABytes, b_lbo, 1024);
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk) {
+            const uint32_t accum = (c > 0 || kk > 0) ? 1u : 0u;
+            if constexpr (CG == 2)
+              umma_f16_pair(d, ad + kk * a_step, bd + kk * b_step, idesc, accum);
+            else
+              umma_f16(d, ad + kk * a_step, bd + kk * b_step, idesc, accum);
+          }
+          if constexpr (CG == 2) umma_commit_pair(&empty[stage]);
+          else umma_commit(&empty[stage]);
+          if (++stage == a.nstages) { stage = 0; phase ^= 1; }
+        }
+        if (!ok) break;
+        if constexpr (CG == 2) umma_commit_pair(&acc_full[acc]);
+        else umma_commit(&acc_full[acc]);
+        acc ^= 1;
+        if (acc == 0) acc_phase ^= 1;
+      }
+    }
+  } else {
+    // Epilogue: a warp reads the 32 accumulator rows of its lane quarter (warp % 4), one row per
+    // lane; warps 2-5 take the tile's first half of the columns, warps 6-9 the second.
+    const int q = warp & 3, half = (warp - 2) >> 2;
+    constexpr int HC = BN / 2;             // columns of a half
+    uint8_t* st = smem + a.staging_off + (warp - 2) * 4096;
+    int acc = 0;
+    uint32_t acc_phase = 0;
+    Unit u;
+    for (int i = 0; sch.get(a, i, u); ++i) {
+      const int row = u.m0 + (int)rank * 128 + q * 32 + lane;   // row of the product
+      const bool empty_sum = u.nk == 0;
+      const uint32_t tacc = tbase + (uint32_t(q * 32) << 16) + acc * BN + half * HC;
+      int my_row = 0, tgt = -1;
+      float lse = 0.f, g = 0.f;
+      if (kMode != kGrad || u.kind == 1) {
+        if (row < n) {
+          my_row = a.row_idx[row];
+          if constexpr (kMode != kGrad) tgt = a.target[my_row] - a.v0 - u.n0 - half * HC;
+          if constexpr (kMode == kDlog) {
+            lse = a.lse[my_row];
+            g = a.grad_nll[my_row];
+          }
+        }
+      }
+      if (!empty_sum) {
+        // a wait that gave up only flags the status word; the results are then garbage but the
+        // kernel ends
+        mbar_wait_sleep(&acc_full[acc], acc_phase, abort_flag, a.status);
+        tc_fence_after();
+      }
+      auto load = [&](int c, float* v) {
+        if (!empty_sum) {
+          tmem_ld32(tacc + c * 32, v);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 32; ++j) v[j] = 0.f;
+        }
+      };
+      const int ccol = u.n0 + half * HC;   // first column of this half
+      if constexpr (kMode == kLoss) {
+        // running maximum and sum of this row over the half's columns
+        const int ncol = min(HC, a.vc - ccol);
+        float m = -INFINITY, s = 0.f;
+#pragma unroll 1
+        for (int c = 0; c < HC / 32; ++c) {
+          if (c * 32 >= ncol) break;
+          float v[32];
+          load(c, v);
+          if (c * 32 + 32 > ncol) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              if (c * 32 + j >= ncol) v[j] = -INFINITY;
+          }
+          float x[4] = {v[0], v[1], v[2], v[3]};
+#pragma unroll
+          for (int j = 4; j < 32; ++j) x[j & 3] = fmaxf(x[j & 3], v[j]);
+          const float mn = fmaxf(m, fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])));
+          // the target's logit, in the few chunks that hold one
+          const int rel = tgt - c * 32;
+          const bool mine = row < n && rel >= 0 && rel < 32;
+          if (__any_sync(0xffffffffu, mine)) {
+            float tv = 0.f;
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              if (j == rel) tv = v[j];
+            if (mine) a.tlogit[row] = tv;
+          }
+          float y[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int j = 0; j < 32; ++j) y[j & 3] += ex2((v[j] - mn) * kLog2e);
+          s = s * ex2((m - mn) * kLog2e) + ((y[0] + y[1]) + (y[2] + y[3]));
+          m = mn;
+        }
+        if (row < n)
+          a.part[(size_t)(a.part0 + 2 * (u.n0 / BN) + half) * a.r_pad + row] = make_float2(m, s);
+      } else if constexpr (kMode == kDlog) {
+        constexpr int PC = (!F32 && HC >= 64) ? 2 : 1;   // 32-column blocks per staged pass
+        constexpr int RB = 64 * PC;
+        const int planes = F32 ? 3 : 1;
+        auto rp = [&](int plane) {
+          return [&, plane](int r) {
+            return a.dlog + ((size_t)plane * a.d_plane + (row - lane + r)) * a.ld_dlog;
+          };
+        };
+#pragma unroll 1
+        for (int c = 0; c < HC / 32; c += PC) {
+#pragma unroll
+          for (int s2 = 0; s2 < PC; ++s2) {
+            float v[32];
+            load(c + s2, v);
+            const int col = ccol + (c + s2) * 32;
+            // rows past the last one and columns past the vocabulary become zeros: the products
+            // that follow read them
+            const int lim = row < n ? a.vc - col : 0;
+            const int rel = tgt - (c + s2) * 32;
+#pragma unroll
+            for (int j = 0; j < 32; ++j) {
+              float p = ex2((v[j] - lse) * kLog2e);
+              if (j == rel) p -= 1.f;
+              v[j] = j < lim ? p * g : 0.f;
+            }
+            if constexpr (!F32) {
+              stage_bf16<RB>(st, lane, s2 * 4, v);
+            } else {
+              for (int pl = 0; pl < planes; ++pl) {
+                float w[32];
+#pragma unroll
+                for (int j = 0; j < 32; ++j) {
+                  __nv_bfloat16 p0, p1, p2;
+                  split3(v[j], p0, p1, p2);
+                  w[j] = __bfloat162float(pl == 0 ? p0 : pl == 1 ? p1 : p2);
+                }
+                stage_bf16<RB>(st, lane, 0, w);
+                flush_rows<__nv_bfloat16, RB>(st, lane, col, a.ld_dlog, true, rp(pl));
+              }
+            }
+          }
+          if constexpr (!F32)
+            flush_rows<__nv_bfloat16, RB>(st, lane, ccol + c * 32, a.ld_dlog, true, rp(0));
+        }
+      } else if (u.kind == 1 && a.acc) {
+        // fp32 sums of this piece and K range
+        float* base = a.acc + (size_t)u.split * a.r_pad * a.d_pad;
+#pragma unroll 1
+        for (int c = 0; c < HC / 32; ++c) {
+          const int col = ccol + c * 32;
+          float v[32];
+          load(c, v);
+          stage_f32(st, lane, v);
+          if (a.acc_add) {
+            __syncwarp();
+#pragma unroll
+            for (int it = 0; it < 8; ++it) {
+              const int r = it * 4 + (lane >> 3), ch = lane & 7;
+              if (row - lane + r < n && col + ch * 4 < a.d_pad) {
+                float4* s4 = reinterpret_cast<float4*>(stage_at<128>(st, r, ch));
+                const float4 o = *reinterpret_cast<const float4*>(
+                    base + (size_t)(row - lane + r) * a.d_pad + col + ch * 4);
+                float4 w = *s4;
+                w.x += o.x; w.y += o.y; w.z += o.z; w.w += o.w;
+                *s4 = w;
+              }
+            }
+          }
+          flush_rows<float, 128>(st, lane, col, a.d_pad, true, [&](int r) -> float* {
+            return row - lane + r < n ? base + (size_t)(row - lane + r) * a.d_pad : nullptr;
+          });
+        }
+      } else {
+        // a gradient in its own type: dH rows at the caller's rows, dW rows in order
+        using T = typename std::conditional<F32, float, __nv_bfloat16>::type;
+        const int lim = u.kind == 1 ? n : a.vc;
+        T* base = static_cast<T*>(u.kind == 1 ? a.out_h : a.out_w);
+        auto rp = [&](int r) -> T* {
+          const int rr = row - lane + r;
+          const int at = u.kind == 1 ? __shfl_sync(0xffffffffu, my_row, r) : rr;
+          return rr < lim ? base + (size_t)at * a.d : nullptr;
+        };
+        constexpr int PC = (!F32 && HC >= 64) ? 2 : 1;
+        constexpr int RB = F32 ? 128 : 64 * PC;
+#pragma unroll 1
+        for (int c = 0; c < HC / 32; c += PC) {
+#pragma unroll
+          for (int s2 = 0; s2 < PC; ++s2) {
+            float v[32];
+            load(c + s2, v);
+            if constexpr (F32) stage_f32(st, lane, v);
+            else stage_bf16<RB>(st, lane, s2 * 4, v);
+          }
+          flush_rows<T, RB>(st, lane, ccol + c * 32, a.d, a.vec_ok != 0, rp);
+        }
+      }
+      if (!empty_sum) {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          if constexpr (CG == 2) mbar_arrive_cluster(lead_addr(&acc_empty[acc]));
+          else mbar_arrive(&acc_empty[acc]);
+        }
+        acc ^= 1;
+        if (acc == 0) acc_phase ^= 1;
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if constexpr (CG == 2) cluster_sync_all();
+  if (warp == 1) {
+    tc_fence_after();
+    if constexpr (CG == 2) tmem_dealloc_pair(tbase, 2 * BN);
+    else tmem_dealloc(tbase, 2 * BN);
+  }
+}
+
+// ------------------------------------------------------------------------------------------
+// Rows
+// ------------------------------------------------------------------------------------------
+struct RowsArgs {
+  int rows, d, d_pad, vocab, r_pad, per;   // per: rows of one CTA
+  bool f32, in_place, vec;
+  long long ld;
+  const void* hidden;
+  const int* target;
+  HeadMeta* meta;
+  int* row_idx;
+  __nv_bfloat16* out;          // [parts][r_pad][d_pad]
+  float *nll, *lse;            // loss: zero for the rows that take no part
+  void* grad_hidden;           // gradient: likewise
+  bool gvec;
+  uint32_t* status;
+};
+
+// Copy (or split) one row of width d into d_pad bf16 columns, by one warp.
+SMDM_DEV void copy_row(const RowsArgs& a, int src, int dst, int lane) {
+  const size_t plane = (size_t)a.r_pad * a.d_pad;
+  __nv_bfloat16* o = a.out + (size_t)dst * a.d_pad;
+  if (!a.f32) {
+    const __nv_bfloat16* x = static_cast<const __nv_bfloat16*>(a.hidden) + (size_t)src * a.ld;
+    if (a.vec) {   // d % 8 == 0, rows on 16-byte boundaries
+      for (int c = lane * 8; c < a.d_pad; c += 256)
+        *reinterpret_cast<uint4*>(o + c) =
+            c < a.d ? *reinterpret_cast<const uint4*>(x + c) : make_uint4(0, 0, 0, 0);
+    } else {
+      for (int c = lane; c < a.d_pad; c += 32) o[c] = c < a.d ? x[c] : __nv_bfloat16(0.f);
+    }
+  } else {
+    const float* x = static_cast<const float*>(a.hidden) + (size_t)src * a.ld;
+    for (int c = lane; c < a.d_pad; c += 32) {
+      __nv_bfloat16 p0, p1, p2;
+      split3(c < a.d ? x[c] : 0.f, p0, p1, p2);
+      o[c] = p0;
+      o[plane + c] = p1;
+      o[2 * plane + c] = p2;
+    }
+  }
+}
+
+// List the rows that take part, in order, and copy them together.  Every CTA reads all targets
+// (from L2) to know how many listed rows precede its own and whether all rows are listed; a
+// device-wide scan would take a second launch.
+__global__ void __launch_bounds__(256) head_rows_kernel(RowsArgs a) {
+  griddep_launch();
+  griddep_wait();
+  __shared__ int red[2][8];
+  __shared__ int s_before, s_total;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int r0 = blockIdx.x * a.per, r1 = min(a.rows, r0 + a.per);
+  int before = 0, total = 0;
+  for (int r = tid; r < a.rows; r += 256) {
+    const int t = a.target[r];
+    const int on = t >= 0 && t < a.vocab;
+    total += on;
+    if (r < r0) before += on;
+  }
+  for (int o = 16; o > 0; o >>= 1) {
+    before += __shfl_xor_sync(0xffffffffu, before, o);
+    total += __shfl_xor_sync(0xffffffffu, total, o);
+  }
+  if (lane == 0) { red[0][warp] = before; red[1][warp] = total; }
+  __syncthreads();
+  if (tid == 0) {
+    int b = 0, t = 0;
+    for (int w = 0; w < 8; ++w) { b += red[0][w]; t += red[1][w]; }
+    s_before = b;
+    s_total = t;
+    if (blockIdx.x == 0) {
+      a.meta->n = t;
+      a.meta->dense = (a.in_place && t == a.rows) ? 1 : 0;
+    }
+  }
+  __syncthreads();
+  const int n = s_total;
+  const bool dense = a.in_place && n == a.rows;
+  int at = s_before;
+  // 32 rows at a time: every warp works out the same listed positions, then takes every 8th row
+  for (int b = r0; b < r1; b += 32) {
+    const int r = b + lane;
+    const int t = r < r1 ? a.target[r] : -1;
+    const bool on = t >= 0 && t < a.vocab;
+    if (t >= a.vocab && warp == 0 && a.status) atomicOr(a.status, kStatusBounds);
+    const uint32_t mask = __ballot_sync(0xffffffffu, on);
+    const int pos = at + __popc(mask & ((1u << lane) - 1u));
+    at += __popc(mask);
+    if (warp == 0 && r < r1) {
+      if (on) {
+        a.row_idx[pos] = r;
+      } else if (a.nll) {
+        a.nll[r] = 0.f;
+        a.lse[r] = 0.f;
+      }
+    }
+    for (int i = warp; i < min(32, r1 - b); i += 8) {
+      const int p = __shfl_sync(0xffffffffu, pos, i);
+      if ((mask >> i) & 1u) {
+        if (!dense) copy_row(a, b + i, p, lane);
+      } else if (a.grad_hidden) {
+        const size_t es = a.f32 ? 4 : 2;
+        uint8_t* g = static_cast<uint8_t*>(a.grad_hidden) + (size_t)(b + i) * a.d * es;
+        if (a.gvec) {
+          for (size_t c = lane * 16; c < a.d * es; c += 512)
+            *reinterpret_cast<uint4*>(g + c) = make_uint4(0, 0, 0, 0);
+        } else if (a.f32) {
+          for (int c = lane; c < a.d; c += 32) reinterpret_cast<float*>(g)[c] = 0.f;
+        } else {
+          for (int c = lane; c < a.d; c += 32)
+            reinterpret_cast<__nv_bfloat16*>(g)[c] = __nv_bfloat16(0.f);
+        }
+      }
+    }
+  }
+  // the rows up to the next multiple of 64 are summed over by dW: zeros
+  if (blockIdx.x == gridDim.x - 1 && !dense) {
+    const int end = min(a.r_pad, (n + 63) & ~63);
+    const size_t plane = (size_t)a.r_pad * a.d_pad;
+    for (int r = n + warp; r < end; r += 8)
+      for (int p = 0; p < (a.f32 ? 3 : 1); ++p)
+        for (int c = lane * 8; c < a.d_pad; c += 256)
+          *reinterpret_cast<uint4*>(a.out + p * plane + (size_t)r * a.d_pad + c) =
+              make_uint4(0, 0, 0, 0);
+  }
+}
+
+// The weight rows of one piece that TMA cannot read in place: fp32 ones, split into three bf16
+// parts, or bf16 ones whose rows do not start on 16-byte boundaries.
+template <bool F32>
+__global__ void __launch_bounds__(256)
+    head_weights_kernel(const void* w, long long ld, int d, int d_pad, int vc, int vc_pad,
+                        __nv_bfloat16* out) {
+  griddep_launch();
+  griddep_wait();
+  const int lane = threadIdx.x & 31;
+  const size_t plane = (size_t)vc_pad * d_pad;
+  for (int v = blockIdx.x * 8 + (threadIdx.x >> 5); v < vc_pad; v += gridDim.x * 8) {
+    __nv_bfloat16* o = out + (size_t)v * d_pad;
+    for (int c = lane; c < d_pad; c += 32) {
+      const bool in = v < vc && c < d;
+      if constexpr (F32) {
+        __nv_bfloat16 p0, p1, p2;
+        split3(in ? static_cast<const float*>(w)[(size_t)v * ld + c] : 0.f, p0, p1, p2);
+        o[c] = p0;
+        o[plane + c] = p1;
+        o[2 * plane + c] = p2;
+      } else {
+        o[c] = in ? static_cast<const __nv_bfloat16*>(w)[(size_t)v * ld + c] : __nv_bfloat16(0.f);
+      }
+    }
+  }
+}
+
+// nll and lse of the listed rows from the column groups' (maximum, sum) pairs.  32 rows per CTA,
+// 8 threads per row over the groups (neighbouring lanes on neighbouring rows).
+__global__ void __launch_bounds__(256)
+    head_finish_kernel(const HeadMeta* meta, const int* row_idx, const float2* part, int n_part,
+                       int r_pad, const float* tlogit, float* nll, float* lse) {
+  griddep_launch();
+  griddep_wait();
+  __shared__ float2 sh[8][32];
+  const int lane = threadIdx.x & 31, g = threadIdx.x >> 5;
+  const int n = meta->n;
+  for (int b = blockIdx.x * 32; b < n; b += gridDim.x * 32) {
+    const int row = b + lane;
+    float m = -INFINITY, s = 0.f;
+    if (row < n) {
+#pragma unroll 4
+      for (int i = g; i < n_part; i += 8) {
+        const float2 p = part[(size_t)i * r_pad + row];
+        if (p.y == 0.f) continue;           // a group past the vocabulary's end
+        const float mn = fmaxf(m, p.x);
+        s = s * ex2((m - mn) * kLog2e) + p.y * ex2((p.x - mn) * kLog2e);
+        m = mn;
+      }
+    }
+    sh[g][lane] = make_float2(m, s);
+    __syncthreads();
+    if (g == 0 && row < n) {
+      for (int i = 1; i < 8; ++i) m = fmaxf(m, sh[i][lane].x);
+      float t = 0.f;
+      for (int i = 0; i < 8; ++i)
+        if (sh[i][lane].y != 0.f) t += sh[i][lane].y * ex2((sh[i][lane].x - m) * kLog2e);
+      const float l = logf(t);
+      const int r = row_idx[row];
+      lse[r] = m + l;
+      nll[r] = (m - tlogit[row]) + l;
+    }
+    __syncthreads();
+  }
+}
+
+// dH from its fp32 sums: the K ranges in order, rounded once, at the caller's rows.
+template <bool F32>
+__global__ void __launch_bounds__(256)
+    head_sum_kernel(const HeadMeta* meta, const int* row_idx, const float* acc, int splits,
+                    int r_pad, int d, int d_pad, void* out) {
+  griddep_launch();
+  griddep_wait();
+  const int n = meta->n;
+  const size_t plane = (size_t)r_pad * d_pad;
+  const int d4 = d_pad >> 2;
+  const long long total = (long long)n * d4;
+  for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < total;
+       i += (long long)gridDim.x * 256) {
+    const int r = (int)(i / d4), c = (int)(i % d4) * 4;
+    if (c >= d) continue;
+    const float* p = acc + (size_t)r * d_pad + c;
+    float4 s = *reinterpret_cast<const float4*>(p);
+    for (int k = 1; k < splits; ++k) {
+      const float4 t = *reinterpret_cast<const float4*>(p + k * plane);
+      s.x += t.x; s.y += t.y; s.z += t.z; s.w += t.w;
+    }
+    const float v[4] = {s.x, s.y, s.z, s.w};
+    const size_t o = (size_t)row_idx[r] * d + c;
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (c + k < d) {
+        if constexpr (F32) static_cast<float*>(out)[o + k] = v[k];
+        else static_cast<__nv_bfloat16*>(out)[o + k] = __float2bfloat16_rn(v[k]);
+      }
+  }
+}
+
+// ------------------------------------------------------------------------------------------
+// Host side
+// ------------------------------------------------------------------------------------------
+size_t up(size_t x, size_t a) { return (x + a - 1) / a * a; }
+
+int sm_count() {
+  int dev = 0, n = 148;
+  if (cudaGetDevice(&dev) == cudaSuccess)
+    cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
+  return n;
+}
+
+struct Plan {
+  int parts, terms, r_pad, d_pad;
+  bool staged;        // weights go through a bf16 copy of each piece
+  int piece, n_pieces;
+  size_t meta, row_idx, hid, part, tlogit, wst, dlog, acc, total;
+  int cfg, cfg_g;     // tile configuration of the logits' product and of the gradients'
+  int splits, n_part;
+};
+
+// Tile configurations: {CTAs per tile, columns}.
+constexpr int kCfgCG[4] = {1, 1, 1, 2};
+constexpr int kCfgBN[4] = {64, 128, 256, 256};
+
+bool weight_in_place(int d, long long ld, bool f32) { return !f32 && d % 8 == 0 && ld % 8 == 0; }
+
+// Time of the product in SM clocks: rounds of tiles times a K chunk's time, the longer of its
+// MMAs and its bytes at 64 per clock.
+double tile_cost(int cfg, long long m, long long n, int sms) {
+  const int cg = kCfgCG[cfg], bn = kCfgBN[cfg];
+  const long long tiles = ((m + 128 * cg - 1) / (128 * cg)) * ((n + bn - 1) / bn);
+  const long long slots = sms / cg;
+  const double mma = bn * 2.0, bytes = (kABytes * std::min<long long>(m, 128) / 128.0 +
+                                        bn / cg * 128.0) / 64.0;
+  return (double)((tiles + slots - 1) / slots) * std::max(mma, bytes);
+}
+
+int pick_cfg(long long m, long long n, int sms) {
+  int best = 0;
+  double bc = 0;
+  for (int c = 0; c < 4; ++c) {
+    const double t = tile_cost(c, m, n, sms);
+    if (c == 0 || t <= bc) { bc = t; best = c; }
+  }
+  return best;
+}
+
+Plan make_plan(int rows, int d, int vocab, long long ld_head, bool f32, bool grad) {
+  Plan p{};
+  const int sms = sm_count();
+  p.parts = f32 ? 3 : 1;
+  p.terms = f32 ? 6 : 1;
+  p.r_pad = (int)up(rows, 256);
+  p.d_pad = (int)up(d, 64);
+  p.staged = !weight_in_place(d, ld_head, f32);
+  // widest piece whose D (gradient) and weight copy (when made) stay below kPieceBytes
+  size_t per_col = 0;
+  if (grad) per_col = (size_t)p.parts * p.r_pad * 2;
+  if (p.staged) per_col = std::max(per_col, (size_t)p.parts * p.d_pad * 2);
+  const int v_pad = (int)up(vocab, 256);
+  p.piece = v_pad;
+  if (per_col) p.piece = (int)std::min<size_t>(v_pad, std::max<size_t>(256, kPieceBytes / per_col / 256 * 256));
+  p.n_pieces = (vocab + p.piece - 1) / p.piece;
+  // pieces of equal width
+  p.piece = (int)up((vocab + p.n_pieces - 1) / p.n_pieces, 256);
+  p.n_pieces = (vocab + p.piece - 1) / p.piece;
+  p.cfg = pick_cfg(rows, p.piece, sms);
+  const int bn = kCfgBN[p.cfg];
+  p.n_part = 2 * ((p.piece + bn - 1) / bn) * p.n_pieces;
+  p.splits = 1;
+  if (grad) {
+    const double c3 = tile_cost(3, p.piece, d, sms) * p.r_pad + tile_cost(3, rows, d, sms) * p.piece;
+    const double c1 = tile_cost(1, p.piece, d, sms) * p.r_pad + tile_cost(1, rows, d, sms) * p.piece;
+    p.cfg_g = c3 <= c1 ? 3 : 1;
+    // K ranges of dH: a unit takes no more than a slot's share of all the work
+    const int cg = kCfgCG[p.cfg_g], gbn = kCfgBN[p.cfg_g];
+    const long long kh = p.piece / 64, kw = (rows + 63) / 64;
+    const long long nh = (long long)((rows + 128 * cg - 1) / (128 * cg)) * ((d + gbn - 1) / gbn);
+    const long long nw = (long long)((p.piece + 128 * cg - 1) / (128 * cg)) * ((d + gbn - 1) / gbn);
+    const long long share = std::max<long long>(8, (nh * kh + nw * (kw + 6)) / (sms / cg));
+    p.splits = (int)std::min<long long>(32, std::max<long long>(1, kh / share));
+  }
+  size_t off = 0;
+  auto take = [&](size_t b) {
+    const size_t o = off;
+    off = up(off + b, 1024);
+    return o;
+  };
+  p.meta = take(256);
+  p.row_idx = take((size_t)p.r_pad * 4);
+  p.hid = take((size_t)p.parts * p.r_pad * p.d_pad * 2);
+  if (!grad) {
+    p.part = take((size_t)p.n_part * p.r_pad * 8);
+    p.tlogit = take((size_t)p.r_pad * 4);
+  }
+  if (p.staged) p.wst = take((size_t)p.parts * p.piece * p.d_pad * 2);
+  if (grad) {
+    p.dlog = take((size_t)p.parts * p.r_pad * p.piece * 2);
+    if (p.splits > 1 || p.n_pieces > 1) p.acc = take((size_t)p.splits * p.r_pad * p.d_pad * 4);
+  }
+  p.total = off;
+  return p;
+}
+
+bool encode_bf16(CUtensorMap* m, const void* base, uint64_t inner, uint64_t outer, uint64_t ld,
+                 uint32_t box_inner, uint32_t box_outer) {
+  EncodeTiledFn fn = get_encode_fn();
+  if (!fn) return false;
+  cuuint64_t dims[2] = {inner, outer};
+  cuuint64_t strides[1] = {ld * 2};
+  cuuint32_t box[2] = {box_inner, box_outer};
+  cuuint32_t estr[2] = {1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box,
+            estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+struct Maps {
+  CUtensorMap h, hc, w, dk, dm;
+};
+
+// Clusters of the pair kernels that fit the device at once (some SM groups are odd).
+template <typename K>
+int max_pairs(K kern, int smem) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(2);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  int n = 0;
+  if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess) {
+    cudaGetLastError();
+    n = 0;
+  }
+  return n;
+}
+
+template <int kMode, int CG, int BN, bool F32>
+cudaError_t launch_one(const Maps& m, HeadDev a, long long units, int sms, cudaStream_t st) {
+  constexpr int kStage = kABytes + BN / CG * 128;
+  const int budget = kSmemLimit - 1024 - kStagingBytes - 512;
+  a.nstages = std::min(kMaxStages, budget / kStage);
+  a.staging_off = a.nstages * kStage;
+  a.bar_off = a.staging_off + kStagingBytes;
+  const int smem = a.bar_off + 512 + 1024;
+  auto kern = head_gemm_kernel<kMode, CG, BN, F32>;
+  // per device: the shared-memory opt-in and the number of pairs that fit
+  static int ready[64];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  if (!ready[dev]) {
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit);
+    if (e != cudaSuccess) return e;
+    int n = sms;
+    if (CG == 2) {
+      n = max_pairs(kern, smem);
+      if (n <= 0) n = sms / 2;
+    }
+    ready[dev] = n;
+  }
+  long long slots = std::min<long long>(ready[dev], units);
+  if (slots < 1) slots = 1;
+  return launch_pdl(kern, dim3((unsigned)(slots * CG)), dim3(kThreads), (size_t)smem, st, CG, m.h,
+                    m.hc, m.w, m.dk, m.dm, a);
+}
+
+template <int kMode, bool F32>
+cudaError_t launch_cfg(int cfg, const Maps& m, const HeadDev& a, long long units, int sms,
+                       cudaStream_t st) {
+  switch (cfg) {
+    case 0:
+      if constexpr (kMode != kGrad) return launch_one<kMode, 1, 64, F32>(m, a, units, sms, st);
+      break;
+    case 1: return launch_one<kMode, 1, 128, F32>(m, a, units, sms, st);
+    case 2:
+      if constexpr (kMode != kGrad) return launch_one<kMode, 1, 256, F32>(m, a, units, sms, st);
+      break;
+    case 3: return launch_one<kMode, 2, 256, F32>(m, a, units, sms, st);
+  }
+  return cudaErrorInvalidValue;
+}
+
+template <int kMode>
+cudaError_t launch_mode(bool f32, int cfg, const Maps& m, const HeadDev& a, long long units,
+                        int sms, cudaStream_t st) {
+  return f32 ? launch_cfg<kMode, true>(cfg, m, a, units, sms, st)
+             : launch_cfg<kMode, false>(cfg, m, a, units, sms, st);
+}
+
+#define TRY(x)                        \
+  do {                                \
+    cudaError_t e_ = (x);             \
+    if (e_ != cudaSuccess) return e_; \
+  } while (0)
+
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+
+struct Call {
+  const HeadArgs& h;
+  Plan p;
+  int sms;
+  uint8_t* ws;
+  bool in_place;    // the caller's hidden can be read by TMA
+  template <typename T> T* at(size_t off) const { return reinterpret_cast<T*>(ws + off); }
+
+  Call(const HeadArgs& a, bool grad)
+      : h(a), p(make_plan(a.rows, a.d, a.vocab, a.ld_head, a.f32, grad)), sms(sm_count()),
+        ws(static_cast<uint8_t*>(a.ws)) {
+    in_place = !a.f32 && a.d % 8 == 0 && a.ld_hidden % 8 == 0 && aligned16(a.hidden);
+  }
+
+  cudaError_t rows(cudaStream_t st) const {
+    RowsArgs r{};
+    r.rows = h.rows;
+    r.d = h.d;
+    r.d_pad = p.d_pad;
+    r.vocab = h.vocab;
+    r.r_pad = p.r_pad;
+    r.per = std::max(8, (h.rows + 1023) / 1024);
+    r.f32 = h.f32;
+    r.in_place = in_place;
+    r.vec = in_place;
+    r.ld = h.ld_hidden;
+    r.hidden = h.hidden;
+    r.target = h.target;
+    r.meta = at<HeadMeta>(p.meta);
+    r.row_idx = at<int>(p.row_idx);
+    r.out = at<__nv_bfloat16>(p.hid);
+    r.nll = h.nll;
+    r.lse = h.lse_out;
+    r.grad_hidden = h.grad_hidden;
+    r.gvec = aligned16(h.grad_hidden) && (size_t)h.d * (h.f32 ? 4 : 2) % 16 == 0;
+    r.status = h.status;
+    return launch_pdl(head_rows_kernel, dim3((h.rows + r.per - 1) / r.per), dim3(256), 0, st, 1, r);
+  }
+
+  // The weights of a piece: in place, or copied into the workspace.  box: {64, box_rows}.
+  cudaError_t weights(int v0, int vc, cudaStream_t st) const {
+    if (!p.staged) return cudaSuccess;
+    const size_t es = h.f32 ? 4 : 2;
+    const void* src = static_cast<const uint8_t*>(h.head) + (size_t)v0 * h.ld_head * es;
+    const int vp = (int)up(vc, 256);
+    const int grid = std::min((vp + 7) / 8, sms * 8);
+    auto k = h.f32 ? head_weights_kernel<true> : head_weights_kernel<false>;
+    return launch_pdl(k, dim3(grid), dim3(256), 0, st, 1, src, h.ld_head, h.d, p.d_pad, vc, vp,
+                      at<__nv_bfloat16>(p.wst));
+  }
+  bool weight_map(CUtensorMap* m, int vc, uint32_t box_rows) const {
+    if (p.staged)
+      return encode_bf16(m, at<uint8_t>(p.wst), p.d_pad, (uint64_t)p.parts * up(vc, 256), p.d_pad,
+                         64, box_rows);
+    return encode_bf16(m, h.head, h.d, h.vocab, h.ld_head, 64, box_rows);
+  }
+  bool hidden_maps(CUtensorMap* in, CUtensorMap* listed, uint32_t box_rows) const {
+    bool ok = encode_bf16(listed, at<uint8_t>(p.hid), p.d_pad, (uint64_t)p.parts * p.r_pad,
+                          p.d_pad, 64, box_rows);
+    if (in_place) ok &= encode_bf16(in, h.hidden, h.d, h.rows, h.ld_hidden, 64, box_rows);
+    else *in = *listed;
+    return ok;
+  }
+  HeadDev dev(int v0, int vc) const {
+    HeadDev a{};
+    a.meta = at<HeadMeta>(p.meta);
+    a.row_idx = at<int>(p.row_idx);
+    a.target = h.target;
+    a.d = h.d;
+    a.v0 = v0;
+    a.vc = vc;
+    a.w_row0 = p.staged ? 0 : v0;
+    a.terms = p.terms;
+    a.h_plane = p.r_pad;
+    a.w_plane = p.staged ? (int)up(vc, 256) : 0;
+    a.d_plane = p.r_pad;
+    a.r_pad = p.r_pad;
+    a.d_pad = p.d_pad;
+    a.status = h.status;
+    return a;
+  }
+  // rows of A that one box brings: no more than there are (a multiple of 8)
+  int a_box() const { return (int)std::min<size_t>(128, up(h.rows, 8)); }
+};
+
+}  // namespace
+
+size_t head_workspace_bytes(int rows, int d, int vocab, bool f32, bool grad) {
+  // the layout that copies the weights is the larger one; it serves every row stride
+  return std::max(make_plan(rows, d, vocab, 0, f32, grad).total,
+                  make_plan(rows, d, vocab, 1, f32, grad).total);
+}
+
+bool head_needs_aligned_weight(int d, long long ld_head, bool f32) {
+  return weight_in_place(d, ld_head, f32);
+}
+
+int head_loss_launches(const HeadArgs& a) {
+  const Plan p = make_plan(a.rows, a.d, a.vocab, a.ld_head, a.f32, false);
+  return 2 + p.n_pieces * (p.staged ? 2 : 1);
+}
+
+int head_grad_launches(const HeadArgs& a) {
+  const Plan p = make_plan(a.rows, a.d, a.vocab, a.ld_head, a.f32, true);
+  const bool sums = p.splits > 1 || p.n_pieces > 1;
+  return 1 + p.n_pieces * (p.staged ? 3 : 2) + (sums && a.grad_hidden ? 1 : 0);
+}
+
+cudaError_t launch_head_loss(const HeadArgs& h, cudaStream_t st) {
+  const Call c(h, false);
+  const Plan& p = c.p;
+  TRY(c.rows(st));
+  const int cg = kCfgCG[p.cfg], bn = kCfgBN[p.cfg];
+  for (int i = 0; i < p.n_pieces; ++i) {
+    const int v0 = i * p.piece, vc = std::min(p.piece, h.vocab - v0);
+    TRY(c.weights(v0, vc, st));
+    Maps m;
+    HeadDev a = c.dev(v0, vc);
+    a.a_box = c.a_box();
+    if (!c.hidden_maps(&m.h, &m.hc, a.a_box) || !c.weight_map(&m.w, vc, bn / cg))
+      return cudaErrorInvalidValue;
+    m.dk = m.dm = m.hc;
+    a.part = c.at<float2>(p.part);
+    a.part0 = 2 * (p.piece / bn) * i;
+    a.tlogit = c.at<float>(p.tlogit);
+    const long long units = (long long)((h.rows + 128 * cg - 1) / (128 * cg)) * ((vc + bn - 1) / bn);
+    TRY(launch_mode<kLoss>(h.f32, p.cfg, m, a, units, c.sms, st));
+  }
+  const int last = h.vocab - (p.n_pieces - 1) * p.piece;
+  const int n_part = 2 * (p.piece / bn) * (p.n_pieces - 1) + 2 * ((last + bn - 1) / bn);
+  return launch_pdl(head_finish_kernel, dim3(std::min((h.rows + 31) / 32, c.sms * 4)), dim3(256),
+                    0, st, 1, c.at<HeadMeta>(p.meta), c.at<int>(p.row_idx), c.at<float2>(p.part),
+                    n_part, p.r_pad, c.at<float>(p.tlogit), h.nll, h.lse_out);
+}
+
+cudaError_t launch_head_grad(const HeadArgs& h, cudaStream_t st) {
+  const Call c(h, true);
+  const Plan& p = c.p;
+  TRY(c.rows(st));
+  const int cg = kCfgCG[p.cfg], bn = kCfgBN[p.cfg];
+  const int gcg = kCfgCG[p.cfg_g], gbn = kCfgBN[p.cfg_g];
+  const size_t es = h.f32 ? 4 : 2;
+  const bool sums = p.splits > 1 || p.n_pieces > 1;
+  for (int i = 0; i < p.n_pieces; ++i) {
+    const int v0 = i * p.piece, vc = std::min(p.piece, h.vocab - v0);
+    TRY(c.weights(v0, vc, st));
+    Maps m;
+    HeadDev a = c.dev(v0, vc);
+    a.a_box = c.a_box();
+    if (!c.hidden_maps(&m.h, &m.hc, a.a_box) || !c.weight_map(&m.w, vc, bn / cg))
+      return cudaErrorInvalidValue;
+    m.dk = m.dm = m.hc;
+    a.lse = h.lse;
+    a.grad_nll = h.grad_nll;
+    a.dlog = c.at<__nv_bfloat16>(p.dlog);
+    a.ld_dlog = p.piece;
+    const long long units = (long long)((h.rows + 128 * cg - 1) / (128 * cg)) * ((vc + bn - 1) / bn);
+    TRY(launch_mode<kDlog>(h.f32, p.cfg, m, a, units, c.sms, st));
+    // both products of D: 64-row boxes for the MN-major operands
+    if (!c.hidden_maps(&m.h, &m.hc, 64) || !c.weight_map(&m.w, vc, 64) ||
+        !encode_bf16(&m.dk, a.dlog, p.piece, (uint64_t)p.parts * p.r_pad, p.piece, 64, 128) ||
+        !encode_bf16(&m.dm, a.dlog, p.piece, (uint64_t)p.parts * p.r_pad, p.piece, 64, 64))
+      return cudaErrorInvalidValue;
+    a.do_h = h.grad_hidden != nullptr;
+    a.do_w = h.grad_head != nullptr;
+    a.splits = p.splits;
+    a.acc = sums ? c.at<float>(p.acc) : nullptr;
+    a.acc_add = i > 0;
+    a.out_h = h.grad_hidden;
+    a.out_w = h.grad_head ? static_cast<uint8_t*>(h.grad_head) + (size_t)v0 * h.d * es : nullptr;
+    a.vec_ok = (size_t)h.d * es % 16 == 0 && (!h.grad_hidden || aligned16(h.grad_hidden)) &&
+               (!h.grad_head || aligned16(h.grad_head));
+    const long long nt = (h.d + gbn - 1) / gbn;
+    const long long gu = (a.do_h ? nt * ((h.rows + 128 * gcg - 1) / (128 * gcg)) * p.splits : 0) +
+                         (a.do_w ? nt * ((vc + 128 * gcg - 1) / (128 * gcg)) : 0);
+    TRY(launch_mode<kGrad>(h.f32, p.cfg_g, m, a, gu, c.sms, st));
+  }
+  if (sums && h.grad_hidden) {
+    const long long n4 = (long long)h.rows * (p.d_pad / 4);
+    const int grid = (int)std::min<long long>((n4 + 255) / 256, (long long)c.sms * 16);
+    auto k = h.f32 ? head_sum_kernel<true> : head_sum_kernel<false>;
+    TRY(launch_pdl(k, dim3(grid), dim3(256), 0, st, 1, c.at<HeadMeta>(p.meta),
+                   c.at<int>(p.row_idx), c.at<float>(p.acc), p.splits, p.r_pad, h.d, p.d_pad,
+                   h.grad_hidden));
+  }
+  return cudaSuccess;
+}
+
+}  // namespace smdm
