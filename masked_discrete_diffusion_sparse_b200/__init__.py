@@ -447,7 +447,7 @@ def _typed(t: torch.Tensor, dt: torch.dtype, name: str):
 
 
 def _shape(t: torch.Tensor, shape: tuple, name: str):
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
 
 
@@ -457,50 +457,70 @@ def _bytes(n: int) -> int:
     return n
 
 
+def _adr(t: Optional[torch.Tensor], name: str):
+    """Address of a contiguous CUDA tensor (None stays None)."""
+    if t is None:
+        return None
+    if not t.is_cuda:
+        raise ValueError(f"{name}: expected a CUDA tensor")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous tensor")
+    return t.data_ptr()
+
+
 def _rows(t: torch.Tensor, name: str):
-    """Pointer and row stride of a 2-D tensor whose rows are contiguous."""
+    """Address and row stride of a 2-D CUDA tensor whose rows are contiguous."""
     if t.dim() != 2:
         raise ValueError(f"{name}: expected a 2-D tensor")
     n, d = t.shape
-    ld = t.stride(0) if n > 1 else d
-    if d > 1 and t.stride(1) != 1:
+    ld, step = t.stride()
+    if d > 1 and step != 1:
         raise ValueError(f"{name}: the elements of a row must be contiguous")
+    if n < 2:
+        ld = d
     if ld < d:
         raise ValueError(f"{name}: rows overlap")
     if not t.is_cuda:
-        raise ValueError("expected a CUDA tensor")
-    return (ctypes.c_void_p(t.data_ptr()) if t.numel() else None), ld
+        raise ValueError(f"{name}: expected a CUDA tensor")
+    return t.data_ptr(), ld
 
 
 def _call(fn: str, stream, tensors, *args):
     """Run one entry point on the tensors' device and the given (or that device's current)
     stream; a tensor used on another stream than the current one is recorded there, so that the
     allocator does not hand its memory out while the kernels run."""
-    ts = [t for t in tensors if t is not None]
-    dev = ts[0].device
-    if any(t.device != dev for t in ts):
-        raise ValueError("all tensors must be on one device")
-    if stream is not None and stream.device != dev:
-        raise ValueError(f"the stream is on {stream.device}, the tensors on {dev}")
-    with torch.cuda.device(dev):
-        cur = torch.cuda.current_stream(dev)
-        s = cur if stream is None else stream
-        if s != cur:
-            for t in ts:
-                t.record_stream(s)
-        r = getattr(lib(), fn)(*args, ctypes.c_void_p(s.cuda_stream))
+    dev = tensors[0].get_device()
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            raise ValueError("all tensors must be on one device")
+    f = getattr(lib(), fn)
+    if stream is None and dev == torch.cuda.current_device():
+        r = f(*args, torch._C._cuda_getCurrentRawStream(dev))
+    else:
+        if stream is not None and stream.device.index != dev:
+            raise ValueError(f"the stream is on {stream.device}, the tensors on cuda:{dev}")
+        with torch.cuda.device(dev):
+            cur = torch.cuda.current_stream(dev)
+            s = cur if stream is None else stream
+            if s != cur:
+                for t in tensors:
+                    if t is not None:
+                        t.record_stream(s)
+            r = f(*args, s.cuda_stream)
     if r != SMDM_OK:
         raise SmdmError(r, f"{fn} failed")
 
 
 def _status(t: Optional[torch.Tensor]):
-    if t is not None and (t.numel() < 1 or t.element_size() != 4):
+    if t is None:
+        return None
+    if t.numel() < 1 or t.element_size() != 4:
         raise ValueError("status: expected a 32-bit integer tensor of one element")
-    return _ptr(t)
+    return _adr(t, "status")
 
 
 def _ws(t: torch.Tensor):
-    return _ptr(t), t.numel() * t.element_size()
+    return _adr(t, "workspace"), t.nbytes
 
 
 def _head_shape(hidden, lm_head, target):
@@ -509,7 +529,8 @@ def _head_shape(hidden, lm_head, target):
     h, ld_h = _rows(hidden, "hidden")
     w, ld_w = _rows(lm_head, "lm_head")
     n, d = hidden.shape
-    _shape(lm_head, (lm_head.shape[0], d), "lm_head")
+    if lm_head.shape[1] != d:
+        raise ValueError("hidden and lm_head must share their width")
     _shape(target, (n,), "target")
     s = smdm_head_shape(n, d, lm_head.shape[0], _dtype(hidden), ld_h, ld_w)
     return s, h, w
@@ -532,7 +553,7 @@ def smdm_head_loss(hidden, lm_head, target, nll, lse, workspace, status=None, st
         _typed(t, torch.float32, name)
     ws, nb = _ws(workspace)
     _call("smdm_head_loss", stream, (hidden, lm_head, target, nll, lse, workspace, status),
-          ctypes.byref(s), h, w, _ptr(_i32(target)), _ptr(nll), _ptr(lse), ws, nb,
+          ctypes.byref(s), h, w, _adr(_i32(target), "target"), _adr(nll, "nll"), _adr(lse, "lse"), ws, nb,
           _status(status))
 
 
@@ -552,8 +573,8 @@ def smdm_head_loss_grad(hidden, lm_head, target, lse, grad_nll, grad_hidden, gra
     ws, nb = _ws(workspace)
     _call("smdm_head_loss_grad", stream,
           (hidden, lm_head, target, lse, grad_nll, grad_hidden, grad_lm_head, workspace, status),
-          ctypes.byref(s), h, w, _ptr(_i32(target)), _ptr(lse), _ptr(grad_nll),
-          _ptr(grad_hidden), _ptr(grad_lm_head), ws, nb, _status(status))
+          ctypes.byref(s), h, w, _adr(_i32(target), "target"), _adr(lse, "lse"), _adr(grad_nll, "grad_nll"),
+          _adr(grad_hidden, "grad_hidden"), _adr(grad_lm_head, "grad_lm_head"), ws, nb, _status(status))
 
 
 def smdm_rmsnorm(x, gain, y, rstd=None, eps: float = 1e-6, stream=None):
@@ -568,8 +589,8 @@ def smdm_rmsnorm(x, gain, y, rstd=None, eps: float = 1e-6, stream=None):
         _shape(rstd, (x.shape[0],), "rstd")
         _typed(rstd, torch.float32, "rstd")
     s = smdm_rmsnorm_shape(x.shape[0], x.shape[1], _dtype(x), _dtype(y), ld_x, ld_y, eps)
-    _call("smdm_rmsnorm", stream, (x, gain, y, rstd), ctypes.byref(s), px, _ptr(gain), py,
-          _ptr(rstd))
+    _call("smdm_rmsnorm", stream, (x, gain, y, rstd), ctypes.byref(s), px, _adr(gain, "gain"), py,
+          _adr(rstd, "rstd"))
 
 
 def smdm_rmsnorm_grad_workspace_bytes(rows: int, d_model: int) -> int:
@@ -596,7 +617,7 @@ def smdm_rmsnorm_grad(x, gain, rstd, grad_y, grad_x, grad_gain, workspace, grad_
     ws, nb = _ws(workspace)
     _call("smdm_rmsnorm_grad", stream,
           (x, gain, rstd, grad_y, grad_x, grad_gain, workspace, grad_add), ctypes.byref(s), px,
-          _ptr(gain), _ptr(rstd), pg, _ptr(grad_add), _ptr(grad_x), _ptr(grad_gain), ws, nb)
+          _adr(gain, "gain"), _adr(rstd, "rstd"), pg, _adr(grad_add, "grad_add"), _adr(grad_x, "grad_x"), _adr(grad_gain, "grad_gain"), ws, nb)
 
 
 def smdm_embed(ids, table, out, scale: float = 1.0, status=None, stream=None):
@@ -606,8 +627,8 @@ def smdm_embed(ids, table, out, scale: float = 1.0, status=None, stream=None):
     _shape(out, (out.shape[0], table.shape[1]), "out")
     s = smdm_embed_shape(ids.numel(), table.shape[1], table.shape[0], _dtype(table), _dtype(out),
                          ld, scale)
-    _call("smdm_embed", stream, (ids, table, out, status), ctypes.byref(s), _ptr(_i32(ids)), pt,
-          _ptr(out), _status(status))
+    _call("smdm_embed", stream, (ids, table, out, status), ctypes.byref(s), _adr(_i32(ids), "ids"), pt,
+          _adr(out, "out"), _status(status))
 
 
 def smdm_embed_grad_workspace_bytes(rows: int, d_model: int, n_emb: int) -> int:
@@ -625,7 +646,7 @@ def smdm_embed_grad(ids, grad_out, grad_table, workspace, scale: float = 1.0, st
                          _dtype(grad_out), ld, scale)
     ws, nb = _ws(workspace)
     _call("smdm_embed_grad", stream, (ids, grad_out, grad_table, workspace, status),
-          ctypes.byref(s), _ptr(_i32(ids)), pg, _ptr(grad_table), ws, nb, _status(status))
+          ctypes.byref(s), _adr(_i32(ids), "ids"), pg, _adr(grad_table, "grad_table"), ws, nb, _status(status))
 
 
 def make_config(n_layers, d_model, n_heads, d_head, d_ffn, vocab, n_reg=64, dtype=SMDM_BF16,

@@ -39,6 +39,40 @@ SMDM_DEV void store_v(T* p, const float* v) {
   else *p = from_f<T>(v[0]);
 }
 
+// N elements in as few instructions as their bytes allow (16 each).
+template <int N>
+SMDM_DEV void load_n(const float* p, float* v) {
+#pragma unroll
+  for (int k = 0; k < N; k += 4) load4(p + k, v + k);
+}
+template <int N>
+SMDM_DEV void load_n(const __nv_bfloat16* p, float* v) {
+  if constexpr (N == 8) {
+    const uint4 u = *reinterpret_cast<const uint4*>(p);
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      v[2 * k] = __uint_as_float(w[k] << 16);
+      v[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
+    }
+  } else {
+    load4(p, v);
+  }
+}
+template <int N>
+SMDM_DEV void store_n(float* p, const float* v) {
+#pragma unroll
+  for (int k = 0; k < N; k += 4) store4(p + k, v + k);
+}
+template <int N>
+SMDM_DEV void store_n(__nv_bfloat16* p, const float* v) {
+  if constexpr (N == 8)
+    *reinterpret_cast<uint4*>(p) = make_uint4(bf2(v[0], v[1]), bf2(v[2], v[3]), bf2(v[4], v[5]),
+                                              bf2(v[6], v[7]));
+  else
+    store4(p, v);
+}
+
 int device_sms() {
   int dev = 0, n = 148;
   if (cudaGetDevice(&dev) == cudaSuccess)
@@ -204,6 +238,116 @@ __global__ void __launch_bounds__(kNormThreads) train_rms_grad_kernel(RmsArgs a)
   }
 }
 
+// The gradient for wide rows on 16-byte boundaries: the same sums, with the rows' loads taken off
+// the threads.  Bulk copies bring x, grad_y and add of the CTA's next rows into a ring of shared
+// memory stages while the threads work on the current one, so that HBM stays busy through the
+// row's reduction and its stores.  One row per turn and CTA of TH threads.
+struct RmsRing {
+  int stages, stage_bytes, gy_off, add_off;   // offsets within a stage
+};
+
+template <typename X, typename T, int TH>
+__global__ void __launch_bounds__(TH, 512 / TH) train_rms_grad_ring_kernel(RmsArgs a, RmsRing q) {
+  extern __shared__ __align__(128) uint8_t ring[];
+  __shared__ float red[32];
+  __shared__ __align__(8) uint64_t full[8];
+  __shared__ int s_abort;
+  constexpr int NU = 4;
+  const int tid = threadIdx.x;
+  const int units = a.d >> 2;
+  if (tid == 0) {
+    for (int i = 0; i < q.stages; ++i) mbar_init(&full[i], 1);
+    s_abort = 0;
+    fence_mbar_init();
+  }
+  __syncthreads();
+  griddep_launch();
+  griddep_wait();
+  volatile int* abort_flag = &s_abort;
+  const uint32_t xb = a.d * sizeof(X), gb = a.d * sizeof(T);
+  auto fetch = [&](int row, int st) {
+    uint8_t* p = ring + (size_t)st * q.stage_bytes;
+    mbar_arrive_expect_tx(&full[st], xb + gb + (a.add ? xb : 0u));
+    bulk_load(p, static_cast<const X*>(a.x) + (size_t)row * a.ld_x, xb, &full[st]);
+    bulk_load(p + q.gy_off, static_cast<const T*>(a.grad_y) + (size_t)row * a.ld_y, gb, &full[st]);
+    if (a.add)
+      bulk_load(p + q.add_off, static_cast<const X*>(a.add) + (size_t)row * a.d, xb, &full[st]);
+  };
+  if (tid == 0)
+    for (int i = 0; i < q.stages; ++i) {
+      const long long row = blockIdx.x + (long long)i * gridDim.x;
+      if (row < a.rows) fetch((int)row, i);
+    }
+  float gain[NU * 4], acc[NU * 4];
+#pragma unroll
+  for (int u = 0; u < NU; ++u) {
+    const int i = tid + u * TH;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) gain[u * 4 + k] = acc[u * 4 + k] = 0.f;
+    if (i < units) load4(static_cast<const T*>(a.gain) + (size_t)i * 4, gain + u * 4);
+  }
+  int st = 0, turn = 0;
+  uint32_t phase = 0;
+  for (int row = blockIdx.x; row < a.rows; row += gridDim.x, ++turn) {
+    const float r = a.rstd[row];
+    mbar_wait(&full[st], phase, abort_flag, nullptr);
+    const uint8_t* p = ring + (size_t)st * q.stage_bytes;
+    const X* x = reinterpret_cast<const X*>(p);
+    const T* gy = reinterpret_cast<const T*>(p + q.gy_off);
+    const X* ad = reinterpret_cast<const X*>(p + q.add_off);
+    float v[NU * 4], g[NU * 4], w[NU * 4];
+    float dot = 0.f;
+#pragma unroll
+    for (int u = 0; u < NU; ++u) {
+      const int i = tid + u * TH;
+      if (i < units) {
+        load4(x + i * 4, v + u * 4);
+        load4(gy + i * 4, g + u * 4);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) w[u * 4 + k] = 0.f;
+        if (a.add) load4(ad + i * 4, w + u * 4);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int e = u * 4 + k;
+          acc[e] += g[e] * (v[e] * r);
+          g[e] *= gain[e];
+          dot += g[e] * v[e];
+        }
+      }
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
+    // two sets of partial sums in turn: the next row's do not overwrite the ones being read
+    float* rd = red + (turn & 1) * 16;
+    if ((tid & 31) == 0) rd[tid >> 5] = dot;
+    __syncthreads();                        // the stage has been read, too
+    const long long next = row + (long long)q.stages * gridDim.x;
+    if (tid == 0 && next < a.rows) fetch((int)next, st);
+    dot = 0.f;
+#pragma unroll
+    for (int i = 0; i < TH / 32; ++i) dot += rd[i];
+    const float c = dot / (float)a.d * r * r;
+    X* gx = static_cast<X*>(a.grad_x) + (size_t)row * a.d;
+#pragma unroll
+    for (int u = 0; u < NU; ++u) {
+      const int i = tid + u * TH;
+      if (i < units) {
+        float o[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) o[k] = r * (g[u * 4 + k] - v[u * 4 + k] * c) + w[u * 4 + k];
+        store4(gx + (size_t)i * 4, o);
+      }
+    }
+    if (++st == q.stages) { st = 0; phase ^= 1; }
+  }
+  float* ws = a.ws + (size_t)blockIdx.x * a.d;
+#pragma unroll
+  for (int u = 0; u < NU; ++u) {
+    const int i = tid + u * TH;
+    if (i < units) store4(ws + (size_t)i * 4, acc + u * 4);
+  }
+}
+
 // Columns of ws[parts][d] added up: 32 columns and 32 part groups per CTA.
 template <typename T>
 __global__ void __launch_bounds__(1024) rms_gain_kernel(const float* ws, int parts, int d, T* out) {
@@ -228,7 +372,9 @@ __global__ void __launch_bounds__(1024) rms_gain_kernel(const float* ws, int par
 // ------------------------------------------------------------------------------------------
 // Embedding
 // ------------------------------------------------------------------------------------------
-// One warp per row; 8 elements per lane and turn.  A negative id gives a row of zeros.
+// One warp per row.  A lane takes as many elements as fill 16 bytes of the wider of the two types,
+// so that every store instruction of a warp writes whole 32-byte sectors in a row.  A negative id
+// gives a row of zeros.
 template <typename T, typename O, bool VECT>
 __global__ void __launch_bounds__(256) embed_kernel(EmbedArgs a) {
   griddep_launch();
@@ -242,19 +388,16 @@ __global__ void __launch_bounds__(256) embed_kernel(EmbedArgs a) {
   const T* t = static_cast<const T*>(a.table) + (size_t)(on ? id : 0) * a.ld_table;
   O* o = static_cast<O*>(a.out) + (size_t)row * a.d;
   if constexpr (VECT) {
-#pragma unroll 4
-    for (int c = lane * 8; c < a.d; c += 256) {
-      float v[8];
+    constexpr int N = sizeof(T) == 4 || sizeof(O) == 4 ? 4 : 8;
+#pragma unroll 8
+    for (int c = lane * N; c < a.d; c += 32 * N) {
+      float v[N];
 #pragma unroll
-      for (int k = 0; k < 8; ++k) v[k] = 0.f;
-      if (on) {
-        load4(t + c, v);
-        load4(t + c + 4, v + 4);
-      }
+      for (int k = 0; k < N; ++k) v[k] = 0.f;
+      if (on) load_n<N>(t + c, v);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) v[k] *= a.scale;
-      store4(o + c, v);
-      store4(o + c + 4, v + 4);
+      for (int k = 0; k < N; ++k) v[k] *= a.scale;
+      store_n<N>(o + c, v);
     }
   } else {
     for (int c = lane; c < a.d; c += 32) o[c] = from_f<O>(on ? to_f<T>(t[c]) * a.scale : 0.f);
@@ -265,15 +408,17 @@ __global__ void __launch_bounds__(256) embed_kernel(EmbedArgs a) {
 // and the sums below always add a token's rows in the same order.
 constexpr int kChunk = 2048, kWays = 8;
 
-// Each CTA sorts one chunk of kChunk words in shared memory (bitonic network).
+// Each CTA sorts one chunk of kChunk words: a bitonic network, two words per thread.  Exchanges over
+// distances below 64 stay within a warp (shuffles; the last one within a thread), 51 of the 66
+// steps; only the other 15 go through shared memory.  Thread t of a step holds words 2t and 2t + 1.
 __global__ void __launch_bounds__(1024) embed_sort_kernel(const int* ids, int n, int n_emb,
                                                           unsigned long long* out,
                                                           uint32_t* status) {
   griddep_launch();
   griddep_wait();
-  __shared__ unsigned long long s[kChunk];
-  const int base = blockIdx.x * kChunk;
-  for (int i = threadIdx.x; i < kChunk; i += 1024) {
+  __shared__ __align__(16) unsigned long long s[kChunk];
+  const int base = blockIdx.x * kChunk, t = threadIdx.x;
+  auto word = [&](int i) {
     const int r = base + i;
     unsigned key = 0xffffffffu;            // behind every id
     if (r < n) {
@@ -284,22 +429,47 @@ __global__ void __launch_bounds__(1024) embed_sort_kernel(const int* ids, int n,
         if (id >= n_emb && status) atomicOr(status, kStatusBounds);
       }
     }
-    s[i] = ((unsigned long long)key << 32) | (unsigned)r;
-  }
-  __syncthreads();
-  for (int k = 2; k <= kChunk; k <<= 1)
-    for (int j = k >> 1; j > 0; j >>= 1) {
-      const int t = threadIdx.x;
-      const int i = ((t & ~(j - 1)) << 1) | (t & (j - 1)), l = i | j;
-      const unsigned long long x = s[i], y = s[l];
-      if ((x > y) == ((i & k) == 0)) {
-        s[i] = y;
-        s[l] = x;
+    return ((unsigned long long)key << 32) | (unsigned)r;
+  };
+  auto order = [](unsigned long long& x, unsigned long long& y, bool up) {
+    if ((x > y) == up) {
+      const unsigned long long z = x;
+      x = y;
+      y = z;
+    }
+  };
+  unsigned long long x = word(2 * t), y = word(2 * t + 1);
+  for (int k = 2; k <= kChunk; k <<= 1) {
+    const bool up = ((2 * t) & k) == 0;
+    if (k >= 128) {
+      // distances 64 and more: word pairs of the whole chunk in shared memory
+      s[2 * t] = x;
+      s[2 * t + 1] = y;
+      __syncthreads();
+      for (int j = k >> 1; j >= 64; j >>= 1) {
+        const int i = ((t & ~(j - 1)) << 1) | (t & (j - 1)), l = i | j;
+        unsigned long long p = s[i], q = s[l];
+        order(p, q, (i & k) == 0);
+        s[i] = p;
+        s[l] = q;
+        __syncthreads();
       }
+      x = s[2 * t];
+      y = s[2 * t + 1];
       __syncthreads();
     }
-  for (int i = threadIdx.x; i < kChunk; i += 1024)
-    if (base + i < n) out[base + i] = s[i];
+    for (int j = min(k >> 1, 32); j >= 2; j >>= 1) {
+      // partner thread t ^ (j / 2): the lower one keeps the smaller word of an ascending pair
+      const bool keep_min = ((t & (j >> 1)) == 0) == up;
+      const unsigned long long px = __shfl_xor_sync(0xffffffffu, x, j >> 1);
+      const unsigned long long py = __shfl_xor_sync(0xffffffffu, y, j >> 1);
+      x = (px < x) == keep_min ? px : x;
+      y = (py < y) == keep_min ? py : y;
+    }
+    order(x, y, up);
+  }
+  if (base + 2 * t < n) out[base + 2 * t] = x;
+  if (base + 2 * t + 1 < n) out[base + 2 * t + 1] = y;
 }
 
 // Merge groups of kWays sorted runs of `run` words: a word's place is its place in its own run
@@ -380,8 +550,9 @@ __global__ void __launch_bounds__(256) embed_sum_kernel(EmbedGradArgs a) {
       if (v0 + i >= a.e.n_emb || ((present >> i) & 1u)) continue;
       T* o = table + (size_t)(v0 + i) * d;
       if constexpr (VECT) {
-        const float z[4] = {0.f, 0.f, 0.f, 0.f};
-        for (int c = lane * 4; c < d; c += 128) store4(o + c, z);
+        constexpr int N = 16 / (int)sizeof(T);
+        const float z[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+        for (int c = lane * N; c < d; c += 32 * N) store_n<N>(o + c, z);
       } else {
         for (int c = lane; c < d; c += 32) o[c] = from_f<T>(0.f);
       }
@@ -392,8 +563,10 @@ __global__ void __launch_bounds__(256) embed_sum_kernel(EmbedGradArgs a) {
   const int piece = job / a.slabs, slab = job % a.slabs;
   if (piece >= a.pieces) return;
   const int i0 = piece * a.per, i1 = min(n, i0 + a.per);
-  // this lane's columns: 8 in a row, or 8 that lie 32 apart
-  auto col = [&](int j) { return VECT ? slab * 256 + lane * 8 + j : slab * 256 + j * 32 + lane; };
+  // this lane's columns: 8 in a row (bf16 rows), 4 and 4 that lie 128 apart (fp32), or 8 that
+  // lie 32 apart (rows off their 16-byte boundaries)
+  constexpr int N = !VECT ? 1 : sizeof(O) == 2 ? 8 : 4;
+  auto col = [&](int j) { return slab * 256 + (j / N) * 32 * N + lane * N + j % N; };
   float acc[8];
 #pragma unroll
   for (int j = 0; j < 8; ++j) acc[j] = 0.f;
@@ -403,60 +576,57 @@ __global__ void __launch_bounds__(256) embed_sum_kernel(EmbedGradArgs a) {
   int run_first = 1;       // the current run is the piece's first
   constexpr int kAhead = 8;
   for (int b = i0; b < i1; b += 32) {
-    const unsigned long long mine = b + lane < i1 ? a.list[b + lane] : 0;
+    const unsigned long long mine = b + lane < i1 ? a.list[b + lane] : ~0ull;
+    const int my_key = key_of(mine), my_row = (int)(unsigned)mine;
     const int cnt = min(32, i1 - b);
-    // the key that follows this batch of entries
-    const int after = b + 32 < i1 ? key_of(a.list[b + 32]) : next_key;
+    // the key behind each entry of the batch
+    int my_next = __shfl_down_sync(0xffffffffu, my_key, 1);
+    if (lane == cnt - 1) my_next = b + 32 < i1 ? key_of(a.list[b + 32]) : next_key;
     for (int h = 0; h < cnt; h += kAhead) {
       float v[kAhead][8];
 #pragma unroll
       for (int k = 0; k < kAhead; ++k) {
-        const unsigned long long w = __shfl_sync(0xffffffffu, mine, (h + k) & 31);
-        if (h + k < cnt && key_of(w) < a.e.n_emb) {
-          const O* r = g + (size_t)(unsigned)w * a.e.ld_grad;
-          if constexpr (VECT) {
-            if (col(0) < d) {
-              load4(r + col(0), v[k]);
-              load4(r + col(0) + 4, v[k] + 4);
-            }
-          } else {
+        const int key = __shfl_sync(0xffffffffu, my_key, h + k);
+        const int row = __shfl_sync(0xffffffffu, my_row, h + k);
+        if (h + k < cnt && key < a.e.n_emb) {
+          const O* r = g + (size_t)row * a.e.ld_grad;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) v[k][j] = col(j) < d ? to_f<O>(r[col(j)]) : 0.f;
-          }
+          for (int j = 0; j < 8; j += N)
+            if (col(j) < d) {
+              if constexpr (VECT) load_n<N>(r + col(j), v[k] + j);
+              else v[k][j] = to_f<O>(r[col(j)]);
+            }
         }
       }
 #pragma unroll
       for (int k = 0; k < kAhead; ++k) {
-        const int key = key_of(__shfl_sync(0xffffffffu, mine, (h + k) & 31));
-        const int nk = key_of(__shfl_sync(0xffffffffu, mine, (h + k + 1) & 31));
+        const int key = __shfl_sync(0xffffffffu, my_key, h + k);
+        const int following = __shfl_sync(0xffffffffu, my_next, h + k);
         if (h + k >= cnt || key >= a.e.n_emb) continue;      // uniform over the warp
 #pragma unroll
         for (int j = 0; j < 8; ++j) acc[j] += v[k][j];
-        const bool last = h + k + 1 >= cnt;
-        const int following = last ? after : nk;
-        const bool piece_end = last && b + 32 >= i1;
+        const bool piece_end = b + h + k + 1 >= i1;
         if (following == key && !piece_end) continue;        // the run goes on
         const bool from_before = run_first && key == prev_key;
         const bool goes_on = piece_end && following == key;
         if (from_before || goes_on) {
           float* p = a.part + ((size_t)piece * 2 + (from_before ? 0 : 1)) * d;
 #pragma unroll
-          for (int j = 0; j < 8; ++j)
-            if (col(j) < d) p[col(j)] = acc[j];
+          for (int j = 0; j < 8; j += N)
+            if (col(j) < d) {
+              if constexpr (VECT) store_n<N>(p + col(j), acc + j);
+              else p[col(j)] = acc[j];
+            }
         } else {
           T* o = table + (size_t)key * d;
 #pragma unroll
           for (int j = 0; j < 8; ++j) acc[j] *= a.e.scale;
-          if constexpr (VECT) {
-            if (col(0) < d) {
-              store4(o + col(0), acc);
-              store4(o + col(0) + 4, acc + 4);
-            }
-          } else {
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-              if (col(j) < d) o[col(j)] = from_f<T>(acc[j]);
-          }
+          for (int j = 0; j < 8; j += N)
+            if (col(j) < d) {
+              if constexpr (VECT) store_n<N>(o + col(j), acc + j);
+              else o[col(j)] = from_f<T>(acc[j]);
+            }
         }
         run_first = 0;
 #pragma unroll
@@ -573,21 +743,48 @@ int norm_tpr(int d) { return d <= 1024 ? 32 : 256; }
 
 int norm_grad_ctas(int rows, int d) {
   const int tpr = norm_tpr(d), rpc = std::max(1, 256 / tpr);
-  return std::min((rows + rpc - 1) / rpc, device_sms() * 2);
+  return std::min((rows + rpc - 1) / rpc, device_sms() * (tpr == 32 ? 4 : 2));
+}
+
+// Wide rows whose every copy starts on 16 bytes: two CTAs of 256 threads per SM, or one of 512
+// above 4096 elements, with as many stages as their share of shared memory holds.
+template <typename X, typename T, int TH>
+cudaError_t rms_ring(const RmsArgs& a, int* ctas, cudaStream_t st) {
+  RmsRing q{};
+  const int xb = (int)up_to(a.d * sizeof(X), 128), gb = (int)up_to(a.d * sizeof(T), 128);
+  q.gy_off = xb;
+  q.add_off = xb + gb;
+  q.stage_bytes = xb + gb + (a.add ? xb : 0);
+  const int budget = (TH == 256 ? 110 : 220) * 1024;
+  q.stages = std::min(8, budget / q.stage_bytes);
+  auto kern = train_rms_grad_ring_kernel<X, T, TH>;
+  static bool ready[64];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  if (!ready[dev]) {
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, budget);
+    if (e != cudaSuccess) return e;
+    ready[dev] = true;
+  }
+  *ctas = std::min(a.rows, device_sms() * (512 / TH));
+  return launch_pdl(kern, dim3(*ctas), dim3(TH), (size_t)q.stages * q.stage_bytes, st, 1, a, q);
 }
 
 template <typename X, typename T, int TPR, int VEC, int NU>
-cudaError_t rms_one(const RmsArgs& a, bool grad, cudaStream_t st) {
+cudaError_t rms_one(const RmsArgs& a, int* grad_ctas, cudaStream_t st) {
   constexpr int B = kNormThreads, RPC = B / TPR;
-  if (!grad)
+  if (!grad_ctas)
     return launch_pdl(train_rms_kernel<X, T, TPR, VEC, NU>, dim3((a.rows + RPC - 1) / RPC),
                       dim3(B), 0, st, 1, a);
-  return launch_pdl(train_rms_grad_kernel<X, T, TPR, VEC, NU>, dim3(norm_grad_ctas(a.rows, a.d)),
-                    dim3(B), RPC > 1 ? (size_t)a.d * 4 : 0, st, 1, a);
+  *grad_ctas = norm_grad_ctas(a.rows, a.d);
+  return launch_pdl(train_rms_grad_kernel<X, T, TPR, VEC, NU>, dim3(*grad_ctas), dim3(B),
+                    RPC > 1 ? (size_t)a.d * 4 : 0, st, 1, a);
 }
 
 template <typename X, typename T>
-cudaError_t rms_types(const RmsArgs& a, bool grad, cudaStream_t st) {
+cudaError_t rms_types(const RmsArgs& a, int* grad, cudaStream_t st) {
   // four elements at a time where every row starts on their alignment
   bool v4 = a.d % 4 == 0 && a.ld_x % 4 == 0 && a.ld_y % 4 == 0 && aligned(a.x, 4 * sizeof(X)) &&
             aligned(a.gain, 4 * sizeof(T));
@@ -597,6 +794,11 @@ cudaError_t rms_types(const RmsArgs& a, bool grad, cudaStream_t st) {
          aligned(a.add, 4 * sizeof(X));
   const int tpr = norm_tpr(a.d);
   if (v4) {
+    const bool ring = grad && tpr > 32 && a.d * sizeof(X) % 16 == 0 && a.d * sizeof(T) % 16 == 0 &&
+                      a.ld_x * sizeof(X) % 16 == 0 && a.ld_y * sizeof(T) % 16 == 0 &&
+                      aligned(a.x, 16) && aligned(a.grad_y, 16) && aligned(a.add, 16);
+    if (ring)
+      return a.d <= 4096 ? rms_ring<X, T, 256>(a, grad, st) : rms_ring<X, T, 512>(a, grad, st);
     if (tpr == 32) {
       return a.d <= 512 ? rms_one<X, T, 32, 4, 4>(a, grad, st) : rms_one<X, T, 32, 4, 8>(a, grad, st);
     }
@@ -607,7 +809,7 @@ cudaError_t rms_types(const RmsArgs& a, bool grad, cudaStream_t st) {
   return rms_one<X, T, 256, 1, 32>(a, grad, st);
 }
 
-cudaError_t rms_any(const RmsArgs& a, bool grad, cudaStream_t st) {
+cudaError_t rms_any(const RmsArgs& a, int* grad, cudaStream_t st) {
   if (a.x_f32) return a.f32 ? rms_types<float, float>(a, grad, st)
                             : rms_types<float, __nv_bfloat16>(a, grad, st);
   return a.f32 ? rms_types<__nv_bfloat16, float>(a, grad, st)
@@ -658,23 +860,23 @@ cudaError_t embed_grad_types(const EmbedGradArgs& g, cudaStream_t st) {
   const cudaError_t e = v ? launch_pdl(embed_sum_kernel<T, O, true>, grid, dim3(256), 0, st, 1, g)
                           : launch_pdl(embed_sum_kernel<T, O, false>, grid, dim3(256), 0, st, 1, g);
   if (e != cudaSuccess || g.pieces < 2) return e;
-  const dim3 jgrid(device_sms() * 2);
+  const dim3 jgrid(device_sms() * 8);
   return a.d % 4 == 0 ? launch_pdl(embed_join_kernel<T, 4>, jgrid, dim3(256), 0, st, 1, g)
                       : launch_pdl(embed_join_kernel<T, 1>, jgrid, dim3(256), 0, st, 1, g);
 }
 
 }  // namespace
 
-cudaError_t launch_train_rmsnorm(const RmsArgs& a, cudaStream_t st) { return rms_any(a, false, st); }
+cudaError_t launch_train_rmsnorm(const RmsArgs& a, cudaStream_t st) { return rms_any(a, nullptr, st); }
 
 size_t rmsnorm_grad_bytes(int rows, int d) {
   return std::max<size_t>(256, up_to((size_t)norm_grad_ctas(rows, d) * d * 4, 256));
 }
 
 cudaError_t launch_train_rmsnorm_grad(const RmsArgs& a, cudaStream_t st) {
-  const cudaError_t e = rms_any(a, true, st);
+  int parts = 0;
+  const cudaError_t e = rms_any(a, &parts, st);
   if (e != cudaSuccess) return e;
-  const int parts = norm_grad_ctas(a.rows, a.d);
   const dim3 grid((a.d + 31) / 32);
   return a.f32 ? launch_pdl(rms_gain_kernel<float>, grid, dim3(1024), 0, st, 1,
                             (const float*)a.ws, parts, a.d, static_cast<float*>(a.grad_gain))

@@ -93,6 +93,15 @@ struct Unit {
 
 constexpr int kTileCost = 6;
 
+// The tensor core cuts its fp32 sums instead of rounding them: measured, a sum over K terms comes
+// out smaller by 2^-30 K of its value (1.0e-6 at K = 1024, 4.0e-6 at 4096).  Where the result is
+// fp32 (the loss, and everything of the fp32 path) the tensor core therefore sums kSegment
+// chunks (512 terms) at a time, and the epilogue threads add the segments in registers, rounded
+// to nearest.  Where it is rounded to bf16 next, the cut does not matter and K is summed whole.
+constexpr int kSegment = 8;
+template <int kMode, bool F32>
+constexpr bool kPromote = F32 || kMode == kLoss;
+
 // The work of one slot (CTA or pair) p of P.  Loss and D: tiles round robin, in groups of 16 row
 // tiles so that a group's rows stay in L2 while the weights pass once.  Gradients: the dH units
 // round robin, then the dW tiles so that every slot ends at about the same number of K chunks
@@ -386,39 +395,43 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = true;
       for (int i = 0; ok && sch.get(a, i, u); ++i) {
         const int total = u.nk * a.terms;
-        if (total == 0) continue;          // nothing to sum: the epilogue writes zeros
-        if (!mbar_wait(&acc_empty[acc], acc_phase ^ 1, abort_flag, a.status)) break;
-        tc_fence_after();
-        const uint32_t d = tbase + acc * BN;
-        const int a_mn = u.kind == 2, b_mn = u.kind != 0;
-        const uint32_t idesc = idesc_bf16(128 * CG, BN, a_mn, b_mn);
         // K-major: the next 16 K values lie 32 bytes on; MN-major: 16 rows of 128 bytes on,
         // with 8192 bytes between 64-element runs along M or N
+        const int a_mn = u.kind == 2, b_mn = u.kind != 0;
+        const uint32_t idesc = idesc_bf16(128 * CG, BN, a_mn, b_mn);
         const uint32_t a_lbo = a_mn ? 8192 : 16, b_lbo = b_mn ? 8192 : 16;
         const uint32_t a_step = a_mn ? 2048 >> 4 : 32 >> 4, b_step = b_mn ? 2048 >> 4 : 32 >> 4;
-        for (int c = 0; c < total; ++c) {
-          if (!mbar_wait(&full[stage], phase, abort_flag, a.status)) { ok = false; break; }
+        // (no chunks at all: nothing to sum, the epilogue writes zeros)
+        for (int c0 = 0; ok && c0 < total;) {
+          const int c1 = kPromote<kMode, F32> ? min(total, c0 + kSegment) : total;
+          if (!mbar_wait(&acc_empty[acc], acc_phase ^ 1, abort_flag, a.status)) { ok = false; break; }
           tc_fence_after();
-          const uint32_t a_addr = smem_u32(smem + stage * kStage);
-          const uint64_t ad = sdesc_sw128(a_addr, a_lbo, 1024);
-          const uint64_t bd = sdesc_sw128(a_addr + kABytes, b_lbo, 1024);
+          const uint32_t d = tbase + acc * BN;
+          for (int c = c0; c < c1; ++c) {
+            if (!mbar_wait(&full[stage], phase, abort_flag, a.status)) { ok = false; break; }
+            tc_fence_after();
+            const uint32_t a_addr = smem_u32(smem + stage * kStage);
+            const uint64_t ad = sdesc_sw128(a_addr, a_lbo, 1024);
+            const uint64_t bd = sdesc_sw128(a_addr + kABytes, b_lbo, 1024);
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk) {
-            const uint32_t accum = (c > 0 || kk > 0) ? 1u : 0u;
-            if constexpr (CG == 2)
-              umma_f16_pair(d, ad + kk * a_step, bd + kk * b_step, idesc, accum);
-            else
-              umma_f16(d, ad + kk * a_step, bd + kk * b_step, idesc, accum);
+            for (int kk = 0; kk < 4; ++kk) {
+              const uint32_t accum = (c > c0 || kk > 0) ? 1u : 0u;
+              if constexpr (CG == 2)
+                umma_f16_pair(d, ad + kk * a_step, bd + kk * b_step, idesc, accum);
+              else
+                umma_f16(d, ad + kk * a_step, bd + kk * b_step, idesc, accum);
+            }
+            if constexpr (CG == 2) umma_commit_pair(&empty[stage]);
+            else umma_commit(&empty[stage]);
+            if (++stage == a.nstages) { stage = 0; phase ^= 1; }
           }
-          if constexpr (CG == 2) umma_commit_pair(&empty[stage]);
-          else umma_commit(&empty[stage]);
-          if (++stage == a.nstages) { stage = 0; phase ^= 1; }
+          if (!ok) break;
+          if constexpr (CG == 2) umma_commit_pair(&acc_full[acc]);
+          else umma_commit(&acc_full[acc]);
+          acc ^= 1;
+          if (acc == 0) acc_phase ^= 1;
+          c0 = c1;
         }
-        if (!ok) break;
-        if constexpr (CG == 2) umma_commit_pair(&acc_full[acc]);
-        else umma_commit(&acc_full[acc]);
-        acc ^= 1;
-        if (acc == 0) acc_phase ^= 1;
       }
     }
   } else {
@@ -433,7 +446,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; sch.get(a, i, u); ++i) {
       const int row = u.m0 + (int)rank * 128 + q * 32 + lane;   // row of the product
       const bool empty_sum = u.nk == 0;
-      const uint32_t tacc = tbase + (uint32_t(q * 32) << 16) + acc * BN + half * HC;
       int my_row = 0, tgt = -1;
       float lse = 0.f, g = 0.f;
       if (kMode != kGrad || u.kind == 1) {
@@ -446,14 +458,51 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
-      if (!empty_sum) {
-        // a wait that gave up only flags the status word; the results are then garbage but the
-        // kernel ends
-        mbar_wait_sleep(&acc_full[acc], acc_phase, abort_flag, a.status);
+      const uint32_t lanes = uint32_t(q * 32) << 16;
+      // a wait that gave up only flags the status word; the results are then garbage but the
+      // kernel ends
+      auto acquire = [&]() {
+        mbar_wait(&acc_full[acc], acc_phase, abort_flag, a.status);
         tc_fence_after();
+      };
+      auto release = [&]() {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          if constexpr (CG == 2) mbar_arrive_cluster(lead_addr(&acc_empty[acc]));
+          else mbar_arrive(&acc_empty[acc]);
+        }
+        acc ^= 1;
+        if (acc == 0) acc_phase ^= 1;
+      };
+      // Promoted sums: this thread's HC columns live in registers once the last segment is in.
+      constexpr bool kRegs = kPromote<kMode, F32>;
+      constexpr int NB = HC / 32;
+      float sum[kRegs ? HC : 1];
+      if constexpr (kRegs) {
+        const int total = u.nk * a.terms;
+#pragma unroll
+        for (int j = 0; j < HC; ++j) sum[j] = 0.f;
+        for (int c0 = 0; c0 < total; c0 += kSegment) {
+          acquire();
+#pragma unroll
+          for (int c = 0; c < NB; ++c) {
+            float v[32];
+            tmem_ld32(tbase + lanes + acc * BN + half * HC + c * 32, v);
+#pragma unroll
+            for (int j = 0; j < 32; ++j) sum[c * 32 + j] += v[j];
+          }
+          release();
+        }
+      } else if (!empty_sum) {
+        acquire();
       }
+      const uint32_t tacc = tbase + lanes + acc * BN + half * HC;
       auto load = [&](int c, float* v) {
-        if (!empty_sum) {
+        if constexpr (kRegs) {
+#pragma unroll
+          for (int j = 0; j < 32; ++j) v[j] = sum[c * 32 + j];
+        } else if (!empty_sum) {
           tmem_ld32(tacc + c * 32, v);
         } else {
 #pragma unroll
@@ -465,8 +514,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         // running maximum and sum of this row over the half's columns
         const int ncol = min(HC, a.vc - ccol);
         float m = -INFINITY, s = 0.f;
-#pragma unroll 1
-        for (int c = 0; c < HC / 32; ++c) {
+#pragma unroll
+        for (int c = 0; c < NB; ++c) {
           if (c * 32 >= ncol) break;
           float v[32];
           load(c, v);
@@ -506,8 +555,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             return a.dlog + ((size_t)plane * a.d_plane + (row - lane + r)) * a.ld_dlog;
           };
         };
-#pragma unroll 1
-        for (int c = 0; c < HC / 32; c += PC) {
+#pragma unroll(kRegs ? NB : 1)
+        for (int c = 0; c < NB; c += PC) {
 #pragma unroll
           for (int s2 = 0; s2 < PC; ++s2) {
             float v[32];
@@ -545,8 +594,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       } else if (u.kind == 1 && a.acc) {
         // fp32 sums of this piece and K range
         float* base = a.acc + (size_t)u.split * a.r_pad * a.d_pad;
-#pragma unroll 1
-        for (int c = 0; c < HC / 32; ++c) {
+#pragma unroll(kRegs ? NB : 1)
+        for (int c = 0; c < NB; ++c) {
           const int col = ccol + c * 32;
           float v[32];
           load(c, v);
@@ -582,8 +631,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         };
         constexpr int PC = (!F32 && HC >= 64) ? 2 : 1;
         constexpr int RB = F32 ? 128 : 64 * PC;
-#pragma unroll 1
-        for (int c = 0; c < HC / 32; c += PC) {
+#pragma unroll(kRegs ? NB : 1)
+        for (int c = 0; c < NB; c += PC) {
 #pragma unroll
           for (int s2 = 0; s2 < PC; ++s2) {
             float v[32];
@@ -594,16 +643,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           flush_rows<T, RB>(st, lane, ccol + c * 32, a.d, a.vec_ok != 0, rp);
         }
       }
-      if (!empty_sum) {
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) {
-          if constexpr (CG == 2) mbar_arrive_cluster(lead_addr(&acc_empty[acc]));
-          else mbar_arrive(&acc_empty[acc]);
-        }
-        acc ^= 1;
-        if (acc == 0) acc_phase ^= 1;
-      }
+      if (!kRegs && !empty_sum) release();
     }
   }
   tc_fence_before();
@@ -771,42 +811,50 @@ __global__ void __launch_bounds__(256)
   }
 }
 
-// nll and lse of the listed rows from the column groups' (maximum, sum) pairs.  32 rows per CTA,
-// 8 threads per row over the groups (neighbouring lanes on neighbouring rows).
-__global__ void __launch_bounds__(256)
+// nll and lse of the listed rows from the column groups' (maximum, sum) pairs.  32 rows per CTA
+// (a lane each), 32 warps over the groups; a warp has eight pairs in flight.
+__global__ void __launch_bounds__(1024)
     head_finish_kernel(const HeadMeta* meta, const int* row_idx, const float2* part, int n_part,
                        int r_pad, const float* tlogit, float* nll, float* lse) {
   griddep_launch();
   griddep_wait();
-  __shared__ float2 sh[8][32];
+  __shared__ float2 sh[32][33];
   const int lane = threadIdx.x & 31, g = threadIdx.x >> 5;
   const int n = meta->n;
-  for (int b = blockIdx.x * 32; b < n; b += gridDim.x * 32) {
-    const int row = b + lane;
-    float m = -INFINITY, s = 0.f;
-    if (row < n) {
-#pragma unroll 4
-      for (int i = g; i < n_part; i += 8) {
-        const float2 p = part[(size_t)i * r_pad + row];
-        if (p.y == 0.f) continue;           // a group past the vocabulary's end
-        const float mn = fmaxf(m, p.x);
-        s = s * ex2((m - mn) * kLog2e) + p.y * ex2((p.x - mn) * kLog2e);
-        m = mn;
-      }
+  const int row = blockIdx.x * 32 + lane;
+  if (blockIdx.x * 32 >= n) return;
+  float m = -INFINITY, s = 0.f;
+  for (int i0 = g; i0 < n_part; i0 += 32 * 8) {
+    float2 p[8];
+    float mn = m;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const int i = i0 + k * 32;
+      p[k] = (row < n && i < n_part) ? part[(size_t)i * r_pad + row] : make_float2(-INFINITY, 0.f);
+      mn = fmaxf(mn, p[k].x);
     }
-    sh[g][lane] = make_float2(m, s);
-    __syncthreads();
-    if (g == 0 && row < n) {
-      for (int i = 1; i < 8; ++i) m = fmaxf(m, sh[i][lane].x);
-      float t = 0.f;
-      for (int i = 0; i < 8; ++i)
-        if (sh[i][lane].y != 0.f) t += sh[i][lane].y * ex2((sh[i][lane].x - m) * kLog2e);
-      const float l = logf(t);
-      const int r = row_idx[row];
-      lse[r] = m + l;
-      nll[r] = (m - tlogit[row]) + l;
-    }
-    __syncthreads();
+    s *= s == 0.f ? 0.f : ex2((m - mn) * kLog2e);
+#pragma unroll
+    for (int k = 0; k < 8; ++k)        // (a group past the vocabulary's end has sum 0)
+      if (p[k].y != 0.f) s += p[k].y * ex2((p[k].x - mn) * kLog2e);
+    m = mn;
+  }
+  sh[g][lane] = make_float2(m, s);
+  __syncthreads();
+  // warp g: row g of the CTA, a lane per group range
+  const float2 p = sh[lane][g];
+  m = p.x;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  s = p.y != 0.f ? p.y * ex2((p.x - m) * kLog2e) : 0.f;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  const int out = blockIdx.x * 32 + g;
+  if (lane == 0 && out < n) {
+    const float l = logf(s);
+    const int r = row_idx[out];
+    lse[r] = m + l;
+    nll[r] = (m - tlogit[out]) + l;
   }
 }
 
@@ -1178,7 +1226,7 @@ cudaError_t launch_head_loss(const HeadArgs& h, cudaStream_t st) {
   }
   const int last = h.vocab - (p.n_pieces - 1) * p.piece;
   const int n_part = 2 * (p.piece / bn) * (p.n_pieces - 1) + 2 * ((last + bn - 1) / bn);
-  return launch_pdl(head_finish_kernel, dim3(std::min((h.rows + 31) / 32, c.sms * 4)), dim3(256),
+  return launch_pdl(head_finish_kernel, dim3((h.rows + 31) / 32), dim3(1024),
                     0, st, 1, c.at<HeadMeta>(p.meta), c.at<int>(p.row_idx), c.at<float2>(p.part),
                     n_part, p.r_pad, c.at<float>(p.tlogit), h.nll, h.lse_out);
 }
