@@ -40,25 +40,43 @@ SMDM_DEV void store_v(T* p, const float* v) {
 }
 
 // N elements in as few instructions as their bytes allow (16 each).
-template <int N>
-SMDM_DEV void load_n(const float* p, float* v) {
+// N elements as loaded, widened when they are used: a conversion next to its load would make the
+// thread wait for each load before it issues the next.
+template <typename T, int N>
+struct Raw {
+  static constexpr int kWords = N * (int)sizeof(T) / 4;
+  uint32_t w[kWords];
+  SMDM_DEV void load(const T* p) {
+    if constexpr (kWords % 4 == 0) {
 #pragma unroll
-  for (int k = 0; k < N; k += 4) load4(p + k, v + k);
-}
-template <int N>
-SMDM_DEV void load_n(const __nv_bfloat16* p, float* v) {
-  if constexpr (N == 8) {
-    const uint4 u = *reinterpret_cast<const uint4*>(p);
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      v[2 * k] = __uint_as_float(w[k] << 16);
-      v[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
+      for (int k = 0; k < kWords; k += 4) {
+        const uint4 u = *reinterpret_cast<const uint4*>(p + k * 4 / (int)sizeof(T));
+        w[k] = u.x; w[k + 1] = u.y; w[k + 2] = u.z; w[k + 3] = u.w;
+      }
+    } else {
+      const uint2 u = *reinterpret_cast<const uint2*>(p);
+      w[0] = u.x; w[1] = u.y;
     }
-  } else {
-    load4(p, v);
   }
-}
+  SMDM_DEV void get(float* v) const {
+#pragma unroll
+    for (int k = 0; k < kWords; ++k) {
+      if constexpr (sizeof(T) == 4) {
+        v[k] = __uint_as_float(w[k]);
+      } else {
+        v[2 * k] = __uint_as_float(w[k] << 16);
+        v[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
+      }
+    }
+  }
+};
+template <typename T>
+struct Raw<T, 1> {
+  T x;
+  SMDM_DEV void load(const T* p) { x = *p; }
+  SMDM_DEV void get(float* v) const { v[0] = to_f<T>(x); }
+};
+
 template <int N>
 SMDM_DEV void store_n(float* p, const float* v) {
 #pragma unroll
@@ -113,13 +131,16 @@ __global__ void __launch_bounds__(kNormThreads) train_rms_kernel(RmsArgs a) {
   if (RPC > 1 && row >= a.rows) return;
   const int units = a.d / VEC;
   const X* x = static_cast<const X*>(a.x) + (size_t)row * a.ld_x;
+  Raw<X, VEC> rx[NU];
+#pragma unroll
+  for (int u = 0; u < NU; ++u)
+    if (tid + u * TPR < units) rx[u].load(x + (size_t)(tid + u * TPR) * VEC);
   float v[NU * VEC];
   float ss = 0.f;
 #pragma unroll
   for (int u = 0; u < NU; ++u) {
-    const int i = tid + u * TPR;
-    if (i < units) {
-      load_v<VEC>(x + (size_t)i * VEC, v + u * VEC);
+    if (tid + u * TPR < units) {
+      rx[u].get(v + u * VEC);
 #pragma unroll
       for (int k = 0; k < VEC; ++k) ss += v[u * VEC + k] * v[u * VEC + k];
     }
@@ -166,19 +187,24 @@ __global__ void __launch_bounds__(kNormThreads) train_rms_grad_kernel(RmsArgs a)
     const T* gy = static_cast<const T*>(a.grad_y) + (size_t)row * a.ld_y;
     const X* ad = a.add ? static_cast<const X*>(a.add) + (size_t)row * a.d : nullptr;
     const float r = a.rstd[row];
-    float v[NU * VEC], g[NU * VEC];
-    float dot = 0.f;
+    Raw<X, VEC> rx[NU], ra[NU];
+    Raw<T, VEC> rg[NU];
 #pragma unroll
     for (int u = 0; u < NU; ++u) {
       const int i = tid + u * TPR;
       if (i < units) {
-        load_v<VEC>(x + (size_t)i * VEC, v + u * VEC);
-        load_v<VEC>(gy + (size_t)i * VEC, g + u * VEC);
+        rx[u].load(x + (size_t)i * VEC);
+        rg[u].load(gy + (size_t)i * VEC);
+        if (ad) ra[u].load(ad + (size_t)i * VEC);
       }
     }
+    float v[NU * VEC], g[NU * VEC];
+    float dot = 0.f;
 #pragma unroll
     for (int u = 0; u < NU; ++u) {
       if (tid + u * TPR < units) {
+        rx[u].get(v + u * VEC);
+        rg[u].get(g + u * VEC);
 #pragma unroll
         for (int k = 0; k < VEC; ++k) {
           const int e = u * VEC + k;
@@ -200,7 +226,7 @@ __global__ void __launch_bounds__(kNormThreads) train_rms_grad_kernel(RmsArgs a)
         for (int k = 0; k < VEC; ++k) o[k] = r * (g[u * VEC + k] - v[u * VEC + k] * c);
         if (ad) {
           float w[VEC];
-          load_v<VEC>(ad + (size_t)i * VEC, w);
+          ra[u].get(w);
 #pragma unroll
           for (int k = 0; k < VEC; ++k) o[k] += w[k];
         }
@@ -389,15 +415,23 @@ __global__ void __launch_bounds__(256) embed_kernel(EmbedArgs a) {
   O* o = static_cast<O*>(a.out) + (size_t)row * a.d;
   if constexpr (VECT) {
     constexpr int N = sizeof(T) == 4 || sizeof(O) == 4 ? 4 : 8;
-#pragma unroll 8
-    for (int c = lane * N; c < a.d; c += 32 * N) {
-      float v[N];
+    constexpr int B = 8;               // loads in flight; stores follow them
+    for (int c0 = lane * N; c0 < a.d; c0 += B * 32 * N) {
+      Raw<T, N> raw[B];
 #pragma unroll
-      for (int k = 0; k < N; ++k) v[k] = 0.f;
-      if (on) load_n<N>(t + c, v);
+      for (int b = 0; b < B; ++b)
+        if (c0 + b * 32 * N < a.d) raw[b].load(t + c0 + b * 32 * N);
 #pragma unroll
-      for (int k = 0; k < N; ++k) v[k] *= a.scale;
-      store_n<N>(o + c, v);
+      for (int b = 0; b < B; ++b) {
+        const int c = c0 + b * 32 * N;
+        if (c < a.d) {
+          float v[N];
+          raw[b].get(v);
+#pragma unroll
+          for (int k = 0; k < N; ++k) v[k] = on ? v[k] * a.scale : 0.f;
+          store_n<N>(o + c, v);
+        }
+      }
     }
   } else {
     for (int c = lane; c < a.d; c += 32) o[c] = from_f<O>(on ? to_f<T>(t[c]) * a.scale : 0.f);
@@ -411,16 +445,19 @@ constexpr int kChunk = 2048, kWays = 8;
 // Each CTA sorts one chunk of kChunk words: a bitonic network, two words per thread.  Exchanges over
 // distances below 64 stay within a warp (shuffles; the last one within a thread), 51 of the 66
 // steps; only the other 15 go through shared memory.  Thread t of a step holds words 2t and 2t + 1.
+// W: 32-bit words (id, place in the chunk) where the ids leave room for the place's 11 bits.
+template <typename W>
 __global__ void __launch_bounds__(1024) embed_sort_kernel(const int* ids, int n, int n_emb,
                                                           unsigned long long* out,
                                                           uint32_t* status) {
   griddep_launch();
   griddep_wait();
-  __shared__ __align__(16) unsigned long long s[kChunk];
+  __shared__ __align__(16) W s[kChunk];
+  constexpr bool k32 = sizeof(W) == 4;
   const int base = blockIdx.x * kChunk, t = threadIdx.x;
   auto word = [&](int i) {
     const int r = base + i;
-    unsigned key = 0xffffffffu;            // behind every id
+    unsigned key = k32 ? (1u << 21) - 1 : 0xffffffffu;   // behind every id
     if (r < n) {
       const int id = ids[r];
       if (id >= 0 && id < n_emb) key = (unsigned)id;
@@ -429,16 +466,16 @@ __global__ void __launch_bounds__(1024) embed_sort_kernel(const int* ids, int n,
         if (id >= n_emb && status) atomicOr(status, kStatusBounds);
       }
     }
-    return ((unsigned long long)key << 32) | (unsigned)r;
+    return k32 ? (W)((key << 11) | (unsigned)i) : (W)(((unsigned long long)key << 32) | (unsigned)r);
   };
-  auto order = [](unsigned long long& x, unsigned long long& y, bool up) {
+  auto order = [](W& x, W& y, bool up) {
     if ((x > y) == up) {
-      const unsigned long long z = x;
+      const W z = x;
       x = y;
       y = z;
     }
   };
-  unsigned long long x = word(2 * t), y = word(2 * t + 1);
+  W x = word(2 * t), y = word(2 * t + 1);
   for (int k = 2; k <= kChunk; k <<= 1) {
     const bool up = ((2 * t) & k) == 0;
     if (k >= 128) {
@@ -448,7 +485,7 @@ __global__ void __launch_bounds__(1024) embed_sort_kernel(const int* ids, int n,
       __syncthreads();
       for (int j = k >> 1; j >= 64; j >>= 1) {
         const int i = ((t & ~(j - 1)) << 1) | (t & (j - 1)), l = i | j;
-        unsigned long long p = s[i], q = s[l];
+        W p = s[i], q = s[l];
         order(p, q, (i & k) == 0);
         s[i] = p;
         s[l] = q;
@@ -461,15 +498,19 @@ __global__ void __launch_bounds__(1024) embed_sort_kernel(const int* ids, int n,
     for (int j = min(k >> 1, 32); j >= 2; j >>= 1) {
       // partner thread t ^ (j / 2): the lower one keeps the smaller word of an ascending pair
       const bool keep_min = ((t & (j >> 1)) == 0) == up;
-      const unsigned long long px = __shfl_xor_sync(0xffffffffu, x, j >> 1);
-      const unsigned long long py = __shfl_xor_sync(0xffffffffu, y, j >> 1);
+      const W px = __shfl_xor_sync(0xffffffffu, x, j >> 1);
+      const W py = __shfl_xor_sync(0xffffffffu, y, j >> 1);
       x = (px < x) == keep_min ? px : x;
       y = (py < y) == keep_min ? py : y;
     }
     order(x, y, up);
   }
-  if (base + 2 * t < n) out[base + 2 * t] = x;
-  if (base + 2 * t + 1 < n) out[base + 2 * t + 1] = y;
+  auto wide = [&](W w) {
+    return k32 ? ((unsigned long long)(w >> 11) << 32) | (unsigned)(base + (int)(w & (kChunk - 1)))
+               : (unsigned long long)w;
+  };
+  if (base + 2 * t < n) out[base + 2 * t] = wide(x);
+  if (base + 2 * t + 1 < n) out[base + 2 * t + 1] = wide(y);
 }
 
 // Merge groups of kWays sorted runs of `run` words: a word's place is its place in its own run
@@ -577,26 +618,20 @@ __global__ void __launch_bounds__(256) embed_sum_kernel(EmbedGradArgs a) {
   constexpr int kAhead = 8;
   for (int b = i0; b < i1; b += 32) {
     const unsigned long long mine = b + lane < i1 ? a.list[b + lane] : ~0ull;
-    const int my_key = key_of(mine), my_row = (int)(unsigned)mine;
+    const int my_key = key_of(mine), my_row = b + lane < i1 ? (int)(unsigned)mine : 0;
     const int cnt = min(32, i1 - b);
     // the key behind each entry of the batch
     int my_next = __shfl_down_sync(0xffffffffu, my_key, 1);
     if (lane == cnt - 1) my_next = b + 32 < i1 ? key_of(a.list[b + 32]) : next_key;
     for (int h = 0; h < cnt; h += kAhead) {
-      float v[kAhead][8];
+      Raw<O, N> v[kAhead][8 / N];
 #pragma unroll
       for (int k = 0; k < kAhead; ++k) {
-        const int key = __shfl_sync(0xffffffffu, my_key, h + k);
+        // (rows that take no part are read and left out; past the piece's end, row 0 is)
         const int row = __shfl_sync(0xffffffffu, my_row, h + k);
-        if (h + k < cnt && key < a.e.n_emb) {
-          const O* r = g + (size_t)row * a.e.ld_grad;
+        const O* r = g + (size_t)row * a.e.ld_grad;
 #pragma unroll
-          for (int j = 0; j < 8; j += N)
-            if (col(j) < d) {
-              if constexpr (VECT) load_n<N>(r + col(j), v[k] + j);
-              else v[k][j] = to_f<O>(r[col(j)]);
-            }
-        }
+        for (int j = 0; j < 8; j += N) v[k][j / N].load(r + min(col(j), d - N));
       }
 #pragma unroll
       for (int k = 0; k < kAhead; ++k) {
@@ -604,7 +639,12 @@ __global__ void __launch_bounds__(256) embed_sum_kernel(EmbedGradArgs a) {
         const int following = __shfl_sync(0xffffffffu, my_next, h + k);
         if (h + k >= cnt || key >= a.e.n_emb) continue;      // uniform over the warp
 #pragma unroll
-        for (int j = 0; j < 8; ++j) acc[j] += v[k][j];
+        for (int j = 0; j < 8; j += N) {
+          float w[N];
+          v[k][j / N].get(w);
+#pragma unroll
+          for (int e = 0; e < N; ++e) acc[j + e] += w[e];
+        }
         const bool piece_end = b + h + k + 1 >= i1;
         if (following == key && !piece_end) continue;        // the run goes on
         const bool from_before = run_first && key == prev_key;
@@ -902,8 +942,11 @@ cudaError_t launch_embed_grad(const EmbedArgs& a, cudaStream_t st) {
   uint8_t* ws = static_cast<uint8_t*>(a.ws);
   unsigned long long* list[2] = {reinterpret_cast<unsigned long long*>(ws + p.list[0]),
                                  reinterpret_cast<unsigned long long*>(ws + p.list[1])};
-  cudaError_t e = launch_pdl(embed_sort_kernel, dim3(p.chunks), dim3(1024), 0, st, 1, a.ids, a.rows,
-                             a.n_emb, list[0], a.status);
+  static_assert(kChunk == 1 << 11, "the 32-bit words hold a place of 11 bits");
+  auto sort = a.n_emb < (1 << 21) - 1 ? embed_sort_kernel<unsigned>
+                                      : embed_sort_kernel<unsigned long long>;
+  cudaError_t e = launch_pdl(sort, dim3(p.chunks), dim3(1024), 0, st, 1, a.ids, a.rows, a.n_emb,
+                             list[0], a.status);
   if (e != cudaSuccess) return e;
   int cur = 0;
   for (long long run = kChunk; run < a.rows; run *= kWays, cur ^= 1) {

@@ -661,6 +661,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 // ------------------------------------------------------------------------------------------
 struct RowsArgs {
   int rows, d, d_pad, vocab, r_pad, per;   // per: rows of one CTA
+  int row_ctas;
   bool f32, in_place, vec;
   long long ld;
   const void* hidden;
@@ -674,37 +675,105 @@ struct RowsArgs {
   uint32_t* status;
 };
 
-// Copy (or split) one row of width d into d_pad bf16 columns, by one warp.
+// Copy (bf16) or split (fp32) one row of d elements into d_pad bf16 columns, zeros behind the
+// row, by one warp; x null: all zeros.  vec: the row starts on a 16-byte boundary and d fills
+// whole 16-byte words.  Four loads per lane are in flight.
+template <typename T>
+SMDM_DEV void put_row(const T* x, int d, int d_pad, bool vec, __nv_bfloat16* o, size_t plane,
+                      int lane) {
+  constexpr int B = 4;
+  if (vec || !x) {
+    constexpr int E = 16 / (int)sizeof(T);
+    for (int c0 = lane * E; c0 < d_pad; c0 += B * 32 * E) {
+      uint4 r[B];
+#pragma unroll
+      for (int b = 0; b < B; ++b) {
+        const int c = c0 + b * 32 * E;
+        r[b] = x && c < d ? *reinterpret_cast<const uint4*>(x + c) : make_uint4(0, 0, 0, 0);
+      }
+#pragma unroll
+      for (int b = 0; b < B; ++b) {
+        const int c = c0 + b * 32 * E;
+        if (c >= d_pad) break;
+        if constexpr (sizeof(T) == 2) {
+          *reinterpret_cast<uint4*>(o + c) = r[b];
+        } else {
+          const uint32_t w[4] = {r[b].x, r[b].y, r[b].z, r[b].w};
+          __nv_bfloat16 p[3][4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) split3(__uint_as_float(w[k]), p[0][k], p[1][k], p[2][k]);
+#pragma unroll
+          for (int k = 0; k < 3; ++k)
+            *reinterpret_cast<uint2*>(o + k * plane + c) = *reinterpret_cast<const uint2*>(p[k]);
+        }
+      }
+    }
+    return;
+  }
+  for (int c0 = lane; c0 < d_pad; c0 += 2 * B * 32) {
+    T r[2 * B];
+#pragma unroll
+    for (int b = 0; b < 2 * B; ++b) r[b] = c0 + b * 32 < d ? x[c0 + b * 32] : T(0.f);
+#pragma unroll
+    for (int b = 0; b < 2 * B; ++b) {
+      const int c = c0 + b * 32;
+      if (c >= d_pad) break;
+      if constexpr (sizeof(T) == 2) {
+        o[c] = r[b];
+      } else {
+        split3(r[b], o[c], o[plane + c], o[2 * plane + c]);
+      }
+    }
+  }
+}
+
 SMDM_DEV void copy_row(const RowsArgs& a, int src, int dst, int lane) {
   const size_t plane = (size_t)a.r_pad * a.d_pad;
   __nv_bfloat16* o = a.out + (size_t)dst * a.d_pad;
-  if (!a.f32) {
-    const __nv_bfloat16* x = static_cast<const __nv_bfloat16*>(a.hidden) + (size_t)src * a.ld;
-    if (a.vec) {   // d % 8 == 0, rows on 16-byte boundaries
-      for (int c = lane * 8; c < a.d_pad; c += 256)
-        *reinterpret_cast<uint4*>(o + c) =
-            c < a.d ? *reinterpret_cast<const uint4*>(x + c) : make_uint4(0, 0, 0, 0);
-    } else {
-      for (int c = lane; c < a.d_pad; c += 32) o[c] = c < a.d ? x[c] : __nv_bfloat16(0.f);
-    }
-  } else {
-    const float* x = static_cast<const float*>(a.hidden) + (size_t)src * a.ld;
-    for (int c = lane; c < a.d_pad; c += 32) {
-      __nv_bfloat16 p0, p1, p2;
-      split3(c < a.d ? x[c] : 0.f, p0, p1, p2);
-      o[c] = p0;
-      o[plane + c] = p1;
-      o[2 * plane + c] = p2;
-    }
+  if (a.f32)
+    put_row(static_cast<const float*>(a.hidden) + (size_t)src * a.ld, a.d, a.d_pad, a.vec, o, plane,
+            lane);
+  else
+    put_row(static_cast<const __nv_bfloat16*>(a.hidden) + (size_t)src * a.ld, a.d, a.d_pad, a.vec,
+            o, plane, lane);
+}
+
+// The weight rows of one piece that TMA cannot read in place: fp32 ones, split into three bf16
+// parts, or bf16 ones whose rows do not start on 16-byte boundaries.
+struct WeightArgs {
+  const void* w;
+  long long ld;
+  int vc, vc_pad;      // rows, and rows to fill (zeros behind)
+  bool vec;
+  __nv_bfloat16* out;  // [parts][vc_pad][d_pad]
+  int ctas;            // 0: nothing to do
+};
+
+SMDM_DEV void put_weights(const RowsArgs& a, const WeightArgs& w, int cta) {
+  const int lane = threadIdx.x & 31;
+  const size_t plane = (size_t)w.vc_pad * a.d_pad;
+  for (int v = cta * 8 + (threadIdx.x >> 5); v < w.vc_pad; v += w.ctas * 8) {
+    __nv_bfloat16* o = w.out + (size_t)v * a.d_pad;
+    if (a.f32)
+      put_row(v < w.vc ? static_cast<const float*>(w.w) + (size_t)v * w.ld : nullptr, a.d, a.d_pad,
+              w.vec, o, plane, lane);
+    else
+      put_row(v < w.vc ? static_cast<const __nv_bfloat16*>(w.w) + (size_t)v * w.ld : nullptr, a.d,
+              a.d_pad, w.vec, o, plane, lane);
   }
 }
 
 // List the rows that take part, in order, and copy them together.  Every CTA reads all targets
 // (from L2) to know how many listed rows precede its own and whether all rows are listed; a
-// device-wide scan would take a second launch.
-__global__ void __launch_bounds__(256) head_rows_kernel(RowsArgs a) {
+// device-wide scan would take a second launch.  The CTAs behind row_ctas lay out the first
+// piece's weights meanwhile, where those cannot be read in place.
+__global__ void __launch_bounds__(256) head_rows_kernel(RowsArgs a, WeightArgs w) {
   griddep_launch();
   griddep_wait();
+  if ((int)blockIdx.x >= a.row_ctas) {
+    put_weights(a, w, blockIdx.x - a.row_ctas);
+    return;
+  }
   __shared__ int red[2][8];
   __shared__ int s_before, s_total;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -773,7 +842,7 @@ __global__ void __launch_bounds__(256) head_rows_kernel(RowsArgs a) {
     }
   }
   // the rows up to the next multiple of 64 are summed over by dW: zeros
-  if (blockIdx.x == gridDim.x - 1 && !dense) {
+  if ((int)blockIdx.x == a.row_ctas - 1 && !dense) {
     const int end = min(a.r_pad, (n + 63) & ~63);
     const size_t plane = (size_t)a.r_pad * a.d_pad;
     for (int r = n + warp; r < end; r += 8)
@@ -784,31 +853,11 @@ __global__ void __launch_bounds__(256) head_rows_kernel(RowsArgs a) {
   }
 }
 
-// The weight rows of one piece that TMA cannot read in place: fp32 ones, split into three bf16
-// parts, or bf16 ones whose rows do not start on 16-byte boundaries.
-template <bool F32>
-__global__ void __launch_bounds__(256)
-    head_weights_kernel(const void* w, long long ld, int d, int d_pad, int vc, int vc_pad,
-                        __nv_bfloat16* out) {
+// The weights of a later piece.
+__global__ void __launch_bounds__(256) head_weights_kernel(RowsArgs a, WeightArgs w) {
   griddep_launch();
   griddep_wait();
-  const int lane = threadIdx.x & 31;
-  const size_t plane = (size_t)vc_pad * d_pad;
-  for (int v = blockIdx.x * 8 + (threadIdx.x >> 5); v < vc_pad; v += gridDim.x * 8) {
-    __nv_bfloat16* o = out + (size_t)v * d_pad;
-    for (int c = lane; c < d_pad; c += 32) {
-      const bool in = v < vc && c < d;
-      if constexpr (F32) {
-        __nv_bfloat16 p0, p1, p2;
-        split3(in ? static_cast<const float*>(w)[(size_t)v * ld + c] : 0.f, p0, p1, p2);
-        o[c] = p0;
-        o[plane + c] = p1;
-        o[2 * plane + c] = p2;
-      } else {
-        o[c] = in ? static_cast<const __nv_bfloat16*>(w)[(size_t)v * ld + c] : __nv_bfloat16(0.f);
-      }
-    }
-  }
+  put_weights(a, w, blockIdx.x);
 }
 
 // nll and lse of the listed rows from the column groups' (maximum, sum) pairs.  32 rows per CTA
@@ -917,15 +966,18 @@ constexpr int kCfgBN[4] = {64, 128, 256, 256};
 
 bool weight_in_place(int d, long long ld, bool f32) { return !f32 && d % 8 == 0 && ld % 8 == 0; }
 
-// Time of the product in SM clocks: rounds of tiles times a K chunk's time, the longer of its
-// MMAs and its bytes at 64 per clock.
+// SM clocks of one K chunk with `m` rows of A: its MMAs, or its bytes at 64 per clock.
+double chunk_clocks(int cfg, long long m) {
+  const int cg = kCfgCG[cfg], bn = kCfgBN[cfg];
+  return std::max(bn * 2.0, (kABytes * std::min<long long>(m, 128) / 128.0 + bn / cg * 128.0) / 64.0);
+}
+
+// Time of the product: rounds of tiles times a K chunk's time.
 double tile_cost(int cfg, long long m, long long n, int sms) {
   const int cg = kCfgCG[cfg], bn = kCfgBN[cfg];
   const long long tiles = ((m + 128 * cg - 1) / (128 * cg)) * ((n + bn - 1) / bn);
   const long long slots = sms / cg;
-  const double mma = bn * 2.0, bytes = (kABytes * std::min<long long>(m, 128) / 128.0 +
-                                        bn / cg * 128.0) / 64.0;
-  return (double)((tiles + slots - 1) / slots) * std::max(mma, bytes);
+  return (double)((tiles + slots - 1) / slots) * chunk_clocks(cfg, m);
 }
 
 int pick_cfg(long long m, long long n, int sms) {
@@ -962,16 +1014,21 @@ Plan make_plan(int rows, int d, int vocab, long long ld_head, bool f32, bool gra
   p.n_part = 2 * ((p.piece + bn - 1) / bn) * p.n_pieces;
   p.splits = 1;
   if (grad) {
-    const double c3 = tile_cost(3, p.piece, d, sms) * p.r_pad + tile_cost(3, rows, d, sms) * p.piece;
-    const double c1 = tile_cost(1, p.piece, d, sms) * p.r_pad + tile_cost(1, rows, d, sms) * p.piece;
-    p.cfg_g = c3 <= c1 ? 3 : 1;
-    // K ranges of dH: a unit takes no more than a slot's share of all the work
-    const int cg = kCfgCG[p.cfg_g], gbn = kCfgBN[p.cfg_g];
+    // The configuration whose slots finish both products first.  K ranges of dH are cut until a
+    // unit takes no more than a slot's share of all the work.
     const long long kh = p.piece / 64, kw = (rows + 63) / 64;
-    const long long nh = (long long)((rows + 128 * cg - 1) / (128 * cg)) * ((d + gbn - 1) / gbn);
-    const long long nw = (long long)((p.piece + 128 * cg - 1) / (128 * cg)) * ((d + gbn - 1) / gbn);
-    const long long share = std::max<long long>(8, (nh * kh + nw * (kw + 6)) / (sms / cg));
-    p.splits = (int)std::min<long long>(32, std::max<long long>(1, kh / share));
+    double best = 0;
+    for (int c : {0, 1, 3}) {
+      const int mt = 128 * kCfgCG[c], bnc = kCfgBN[c], slots = sms / kCfgCG[c];
+      const long long nt = (d + bnc - 1) / bnc;
+      const double ch = chunk_clocks(c, 128), epi = bnc * 8.0 / ch;   // a tile's fixed cost
+      const long long nh = (rows + mt - 1) / mt * nt, nw = (p.piece + mt - 1) / mt * nt;
+      const double uh = (double)kh * p.terms, uw = (double)kw * p.terms + epi;
+      const double share = (nh * (uh + epi) + nw * uw) / slots;
+      const int s = (int)std::min<double>(std::min<long long>(32, kh), std::max(1.0, uh / std::max(share, 8.0)));
+      const double t = ch * std::max(std::max(share, uw), uh / s + epi);
+      if (c == 0 || t <= best) { best = t; p.cfg_g = c; p.splits = s; }
+    }
   }
   size_t off = 0;
   auto take = [&](size_t b) {
@@ -1069,9 +1126,7 @@ template <int kMode, bool F32>
 cudaError_t launch_cfg(int cfg, const Maps& m, const HeadDev& a, long long units, int sms,
                        cudaStream_t st) {
   switch (cfg) {
-    case 0:
-      if constexpr (kMode != kGrad) return launch_one<kMode, 1, 64, F32>(m, a, units, sms, st);
-      break;
+    case 0: return launch_one<kMode, 1, 64, F32>(m, a, units, sms, st);
     case 1: return launch_one<kMode, 1, 128, F32>(m, a, units, sms, st);
     case 2:
       if constexpr (kMode != kGrad) return launch_one<kMode, 1, 256, F32>(m, a, units, sms, st);
@@ -1110,7 +1165,7 @@ struct Call {
     in_place = !a.f32 && a.d % 8 == 0 && a.ld_hidden % 8 == 0 && aligned16(a.hidden);
   }
 
-  cudaError_t rows(cudaStream_t st) const {
+  RowsArgs row_args() const {
     RowsArgs r{};
     r.rows = h.rows;
     r.d = h.d;
@@ -1118,9 +1173,10 @@ struct Call {
     r.vocab = h.vocab;
     r.r_pad = p.r_pad;
     r.per = std::max(8, (h.rows + 1023) / 1024);
+    r.row_ctas = (h.rows + r.per - 1) / r.per;
     r.f32 = h.f32;
     r.in_place = in_place;
-    r.vec = in_place;
+    r.vec = whole_words(h.hidden, h.ld_hidden);
     r.ld = h.ld_hidden;
     r.hidden = h.hidden;
     r.target = h.target;
@@ -1130,21 +1186,39 @@ struct Call {
     r.nll = h.nll;
     r.lse = h.lse_out;
     r.grad_hidden = h.grad_hidden;
-    r.gvec = aligned16(h.grad_hidden) && (size_t)h.d * (h.f32 ? 4 : 2) % 16 == 0;
+    r.gvec = whole_words(h.grad_hidden, h.d);
     r.status = h.status;
-    return launch_pdl(head_rows_kernel, dim3((h.rows + r.per - 1) / r.per), dim3(256), 0, st, 1, r);
+    return r;
   }
-
-  // The weights of a piece: in place, or copied into the workspace.  box: {64, box_rows}.
-  cudaError_t weights(int v0, int vc, cudaStream_t st) const {
-    if (!p.staged) return cudaSuccess;
+  // rows of h.d elements, ld apart, that start on 16-byte boundaries and fill 16-byte words
+  bool whole_words(const void* t, long long ld) const {
+    const int es = h.f32 ? 4 : 2;
+    return aligned16(t) && (long long)h.d * es % 16 == 0 && ld * es % 16 == 0;
+  }
+  WeightArgs weight_args(int v0, int vc) const {
+    WeightArgs w{};
+    if (!p.staged) return w;
     const size_t es = h.f32 ? 4 : 2;
-    const void* src = static_cast<const uint8_t*>(h.head) + (size_t)v0 * h.ld_head * es;
-    const int vp = (int)up(vc, 256);
-    const int grid = std::min((vp + 7) / 8, sms * 8);
-    auto k = h.f32 ? head_weights_kernel<true> : head_weights_kernel<false>;
-    return launch_pdl(k, dim3(grid), dim3(256), 0, st, 1, src, h.ld_head, h.d, p.d_pad, vc, vp,
-                      at<__nv_bfloat16>(p.wst));
+    w.w = static_cast<const uint8_t*>(h.head) + (size_t)v0 * h.ld_head * es;
+    w.ld = h.ld_head;
+    w.vc = vc;
+    w.vc_pad = (int)up(vc, 256);
+    w.vec = whole_words(w.w, h.ld_head);
+    w.out = at<__nv_bfloat16>(p.wst);
+    w.ctas = std::min(w.vc_pad / 8, sms * 8);
+    return w;
+  }
+  // The rows that take part, and the first piece's weights.
+  cudaError_t rows(cudaStream_t st) const {
+    const RowsArgs r = row_args();
+    const WeightArgs w = weight_args(0, std::min(p.piece, h.vocab));
+    return launch_pdl(head_rows_kernel, dim3(r.row_ctas + w.ctas), dim3(256), 0, st, 1, r, w);
+  }
+  // The weights of a later piece: read in place, or copied into the workspace.
+  cudaError_t weights(int v0, int vc, cudaStream_t st) const {
+    if (!p.staged || v0 == 0) return cudaSuccess;
+    const WeightArgs w = weight_args(v0, vc);
+    return launch_pdl(head_weights_kernel, dim3(w.ctas), dim3(256), 0, st, 1, row_args(), w);
   }
   bool weight_map(CUtensorMap* m, int vc, uint32_t box_rows) const {
     if (p.staged)
@@ -1195,13 +1269,13 @@ bool head_needs_aligned_weight(int d, long long ld_head, bool f32) {
 
 int head_loss_launches(const HeadArgs& a) {
   const Plan p = make_plan(a.rows, a.d, a.vocab, a.ld_head, a.f32, false);
-  return 2 + p.n_pieces * (p.staged ? 2 : 1);
+  return 2 + p.n_pieces + (p.staged ? p.n_pieces - 1 : 0);
 }
 
 int head_grad_launches(const HeadArgs& a) {
   const Plan p = make_plan(a.rows, a.d, a.vocab, a.ld_head, a.f32, true);
   const bool sums = p.splits > 1 || p.n_pieces > 1;
-  return 1 + p.n_pieces * (p.staged ? 3 : 2) + (sums && a.grad_hidden ? 1 : 0);
+  return 1 + 2 * p.n_pieces + (p.staged ? p.n_pieces - 1 : 0) + (sums && a.grad_hidden ? 1 : 0);
 }
 
 cudaError_t launch_head_loss(const HeadArgs& h, cudaStream_t st) {
