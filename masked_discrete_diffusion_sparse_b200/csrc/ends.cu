@@ -242,25 +242,20 @@ __global__ void __launch_bounds__(kNormThreads) train_rms_grad_kernel(RmsArgs a)
       if (i < units) store_v<VEC>(ws + (size_t)i * VEC, acc + u * VEC);
     }
   } else {
-    // the warps' shares in order, through shared memory
+    // the warps' shares side by side in shared memory, added in order
     extern __shared__ float sh[];
-    for (int w = 0; w < RPC; ++w) {
-      if (sub == w) {
 #pragma unroll
-        for (int u = 0; u < NU; ++u) {
-          const int i = tid + u * TPR;
-          if (i < units) {
-#pragma unroll
-            for (int k = 0; k < VEC; ++k) {
-              float* s = sh + (size_t)i * VEC + k;
-              *s = (w ? *s : 0.f) + acc[u * VEC + k];
-            }
-          }
-        }
-      }
-      __syncthreads();
+    for (int u = 0; u < NU; ++u) {
+      const int i = tid + u * TPR;
+      if (i < units) store_v<VEC>(sh + (size_t)sub * a.d + (size_t)i * VEC, acc + u * VEC);
     }
-    for (int i = threadIdx.x; i < a.d; i += kNormThreads) ws[i] = sh[i];
+    __syncthreads();
+    for (int i = threadIdx.x; i < a.d; i += kNormThreads) {
+      float t = 0.f;
+#pragma unroll
+      for (int w = 0; w < RPC; ++w) t += sh[(size_t)w * a.d + i];
+      ws[i] = t;
+    }
   }
 }
 
@@ -442,19 +437,36 @@ __global__ void __launch_bounds__(256) embed_kernel(EmbedArgs a) {
 // and the sums below always add a token's rows in the same order.
 constexpr int kChunk = 2048, kWays = 8;
 
-// Each CTA sorts one chunk of kChunk words: a bitonic network, two words per thread.  Exchanges over
-// distances below 64 stay within a warp (shuffles; the last one within a thread), 51 of the 66
-// steps; only the other 15 go through shared memory.  Thread t of a step holds words 2t and 2t + 1.
+// Each of the first `chunks` CTAs sorts one chunk of `size` words (a power of two, up to kChunk): a
+// bitonic network, two words per thread.  Exchanges over distances below 64 stay within a warp
+// (shuffles; the last one within a thread), 51 of the 66 steps of 2048 words; only the other 15
+// go through shared memory.  Thread t holds words 2t and 2t + 1.
+// The other CTAs clear the table's gradient meanwhile.  The sort keeps few SMs busy, so the rows
+// of tokens that do occur cost nothing visible although they are written again (looking every
+// row up in the sorted list instead, in the next kernel: 24.2 -> XX us for 512 rows of 32066).
 // W: 32-bit words (id, place in the chunk) where the ids leave room for the place's 11 bits.
 template <typename W>
-__global__ void __launch_bounds__(1024) embed_sort_kernel(const int* ids, int n, int n_emb,
-                                                          unsigned long long* out,
+__global__ void __launch_bounds__(1024) embed_sort_kernel(const int* ids, int n, int n_emb, int size,
+                                                          int chunks, unsigned long long* out,
+                                                          uint8_t* table, size_t table_bytes,
                                                           uint32_t* status) {
   griddep_launch();
   griddep_wait();
+  if ((int)blockIdx.x >= chunks) {
+    // bytes before the first 16-byte boundary, whole 16-byte words, bytes behind the last
+    const size_t head = min(table_bytes, (size_t)(-reinterpret_cast<uintptr_t>(table) & 15));
+    const size_t words = (table_bytes - head) / 16;
+    uint4* w = reinterpret_cast<uint4*>(table + head);
+    const size_t step = (size_t)(gridDim.x - chunks) * blockDim.x;
+    const size_t at = (size_t)(blockIdx.x - chunks) * blockDim.x + threadIdx.x;
+    for (size_t i = at; i < words; i += step) w[i] = make_uint4(0, 0, 0, 0);
+    if (at < head) table[at] = 0;
+    if (at < table_bytes - head - words * 16) table[head + words * 16 + at] = 0;
+    return;
+  }
   __shared__ __align__(16) W s[kChunk];
   constexpr bool k32 = sizeof(W) == 4;
-  const int base = blockIdx.x * kChunk, t = threadIdx.x;
+  const int base = blockIdx.x * size, t = threadIdx.x;
   auto word = [&](int i) {
     const int r = base + i;
     unsigned key = k32 ? (1u << 21) - 1 : 0xffffffffu;   // behind every id
@@ -476,7 +488,7 @@ __global__ void __launch_bounds__(1024) embed_sort_kernel(const int* ids, int n,
     }
   };
   W x = word(2 * t), y = word(2 * t + 1);
-  for (int k = 2; k <= kChunk; k <<= 1) {
+  for (int k = 2; k <= size; k <<= 1) {
     const bool up = ((2 * t) & k) == 0;
     if (k >= 128) {
       // distances 64 and more: word pairs of the whole chunk in shared memory
@@ -551,18 +563,14 @@ struct EmbedGradArgs {
   const unsigned long long* list;   // sorted (id, row); id n_emb: takes no part
   float* part;                      // [pieces][2][d]
   int per, pieces, slabs;           // list entries per piece; 256-column slabs
-  int sum_ctas;                     // CTAs that sum; the others clear rows without tokens
 };
-
-constexpr int kZeroIds = 32;        // table rows that one clearing CTA looks at
 
 SMDM_DEV int key_of(unsigned long long w) { return (int)(w >> 32); }
 
 // Sum the rows of every token.  One warp takes `per` sorted entries and 256 columns; a run of
 // one token that lies within the piece is written at once, rounded from its fp32 sum; one that
 // goes on in the next piece leaves its part in slot 1 of the piece where it starts and in slot 0
-// of every later one (embed_join_kernel adds them up in order).  The remaining CTAs clear the
-// rows of tokens that do not occur.
+// of every later one (embed_join_kernel adds them up in order).
 template <typename T, typename O, bool VECT>
 __global__ void __launch_bounds__(256) embed_sum_kernel(EmbedGradArgs a) {
   griddep_launch();
@@ -570,36 +578,6 @@ __global__ void __launch_bounds__(256) embed_sum_kernel(EmbedGradArgs a) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int n = a.e.rows, d = a.e.d;
   T* table = static_cast<T*>(a.e.grad_table);
-  if ((int)blockIdx.x >= a.sum_ctas) {
-    __shared__ unsigned s_present;
-    const int v0 = (blockIdx.x - a.sum_ctas) * kZeroIds;
-    if (warp == 0) {
-      const unsigned long long x = (unsigned long long)(unsigned)(v0 + lane) << 32;
-      int lo = 0, hi = n;
-      while (lo < hi) {
-        const int mid = (lo + hi) >> 1;
-        if (a.list[mid] < x) lo = mid + 1;
-        else hi = mid;
-      }
-      const bool here = lo < n && key_of(a.list[lo]) == v0 + lane;
-      const unsigned m = __ballot_sync(0xffffffffu, here);
-      if (lane == 0) s_present = m;
-    }
-    __syncthreads();
-    const unsigned present = s_present;
-    for (int i = warp; i < kZeroIds; i += 8) {
-      if (v0 + i >= a.e.n_emb || ((present >> i) & 1u)) continue;
-      T* o = table + (size_t)(v0 + i) * d;
-      if constexpr (VECT) {
-        constexpr int N = 16 / (int)sizeof(T);
-        const float z[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-        for (int c = lane * N; c < d; c += 32 * N) store_n<N>(o + c, z);
-      } else {
-        for (int c = lane; c < d; c += 32) o[c] = from_f<T>(0.f);
-      }
-    }
-    return;
-  }
   const int job = blockIdx.x * 8 + warp;
   const int piece = job / a.slabs, slab = job % a.slabs;
   if (piece >= a.pieces) return;
@@ -720,24 +698,27 @@ __global__ void __launch_bounds__(256) embed_join_kernel(EmbedGradArgs a) {
       const int first = s_run[j / blocks];
       const int c = (int)(j % blocks) * kCols + lane * VEC;
       const int key = key_of(a.list[(size_t)(first + 1) * a.per]);
-      int cnt = 0;                         // later pieces that begin with this token
-      while (true) {
-        const int q = first + 1 + cnt + threadIdx.x;
-        const int k = __syncthreads_count(q < a.pieces && key_of(a.list[(size_t)q * a.per]) == key);
-        cnt += k;
-        if (k < 256) break;
-      }
-      // part 0: slot 1 of the first piece; part k: slot 0 of the k-th piece after it
+      // part 0: slot 1 of the first piece; part k: slot 0 of the k-th piece after it, as long as
+      // that piece begins with this token (its list entry is read along with the part)
       float s[VEC];
 #pragma unroll
       for (int k = 0; k < VEC; ++k) s[k] = 0.f;
-      if (c < d) {
-#pragma unroll 4
-        for (int k = grp; k <= cnt; k += 8) {
-          float v[VEC];
-          load_v<VEC>(a.part + ((size_t)(first + k) * 2 + (k == 0 ? 1 : 0)) * d + c, v);
+      bool more = true;
+      for (int k0 = grp; more && first + k0 < a.pieces; k0 += 8 * 4) {
+        float v[4][VEC];
+        bool in[4];
 #pragma unroll
-          for (int e = 0; e < VEC; ++e) s[e] += v[e];
+        for (int u = 0; u < 4; ++u) {
+          const int k = k0 + 8 * u, q = min(first + k, a.pieces - 1);
+          in[u] = first + k < a.pieces && (k == 0 || key_of(a.list[(size_t)q * a.per]) == key);
+          load_v<VEC>(a.part + ((size_t)q * 2 + (k == 0 ? 1 : 0)) * d + min(c, d - VEC), v[u]);
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          more = more && in[u];
+          if (more)
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) s[e] += v[u][e];
         }
       }
 #pragma unroll
@@ -820,7 +801,7 @@ cudaError_t rms_one(const RmsArgs& a, int* grad_ctas, cudaStream_t st) {
                       dim3(B), 0, st, 1, a);
   *grad_ctas = norm_grad_ctas(a.rows, a.d);
   return launch_pdl(train_rms_grad_kernel<X, T, TPR, VEC, NU>, dim3(*grad_ctas), dim3(B),
-                    RPC > 1 ? (size_t)a.d * 4 : 0, st, 1, a);
+                    RPC > 1 ? (size_t)a.d * RPC * 4 : 0, st, 1, a);
 }
 
 template <typename X, typename T>
@@ -845,7 +826,8 @@ cudaError_t rms_types(const RmsArgs& a, int* grad, cudaStream_t st) {
     return a.d <= 4096 ? rms_one<X, T, 256, 4, 4>(a, grad, st)
                        : rms_one<X, T, 256, 4, 8>(a, grad, st);
   }
-  if (tpr == 32) return rms_one<X, T, 32, 1, 32>(a, grad, st);
+  if (tpr == 32)
+    return a.d <= 256 ? rms_one<X, T, 32, 1, 8>(a, grad, st) : rms_one<X, T, 32, 1, 32>(a, grad, st);
   return rms_one<X, T, 256, 1, 32>(a, grad, st);
 }
 
@@ -896,7 +878,7 @@ cudaError_t embed_grad_types(const EmbedGradArgs& g, cudaStream_t st) {
   const EmbedArgs& a = g.e;
   const bool v = a.d % 8 == 0 && a.ld_grad % 8 == 0 && aligned(a.grad_out, 16) &&
                  aligned(a.grad_table, 16);
-  const dim3 grid(g.sum_ctas + (a.n_emb + kZeroIds - 1) / kZeroIds);
+  const dim3 grid((unsigned)(((long long)g.pieces * g.slabs + 7) / 8));
   const cudaError_t e = v ? launch_pdl(embed_sum_kernel<T, O, true>, grid, dim3(256), 0, st, 1, g)
                           : launch_pdl(embed_sum_kernel<T, O, false>, grid, dim3(256), 0, st, 1, g);
   if (e != cudaSuccess || g.pieces < 2) return e;
@@ -945,13 +927,20 @@ cudaError_t launch_embed_grad(const EmbedArgs& a, cudaStream_t st) {
   static_assert(kChunk == 1 << 11, "the 32-bit words hold a place of 11 bits");
   auto sort = a.n_emb < (1 << 21) - 1 ? embed_sort_kernel<unsigned>
                                       : embed_sort_kernel<unsigned long long>;
-  cudaError_t e = launch_pdl(sort, dim3(p.chunks), dim3(1024), 0, st, 1, a.ids, a.rows, a.n_emb,
-                             list[0], a.status);
+  int size = 256;
+  while (size < kChunk && size < a.rows) size *= 2;
+  const size_t bytes = (size_t)a.n_emb * a.d * (a.f32 ? 4 : 2);
+  const int threads = size / 2;
+  const int clear = (int)std::min<size_t>((size_t)device_sms() * (2048 / threads),
+                                          (bytes + 16 * threads - 1) / (16 * threads));
+  cudaError_t e = launch_pdl(sort, dim3(p.chunks + clear), dim3(threads), 0, st, 1, a.ids, a.rows,
+                             a.n_emb, size, p.chunks, list[0], static_cast<uint8_t*>(a.grad_table),
+                             bytes, a.status);
   if (e != cudaSuccess) return e;
   int cur = 0;
   for (long long run = kChunk; run < a.rows; run *= kWays, cur ^= 1) {
-    const long long threads = (long long)a.rows * kWays;
-    e = launch_pdl(embed_merge_kernel, dim3((unsigned)((threads + 255) / 256)), dim3(256), 0, st, 1,
+    const long long searches = (long long)a.rows * kWays;
+    e = launch_pdl(embed_merge_kernel, dim3((unsigned)((searches + 255) / 256)), dim3(256), 0, st, 1,
                    (const unsigned long long*)list[cur], a.rows, (int)run, list[cur ^ 1]);
     if (e != cudaSuccess) return e;
   }
@@ -962,7 +951,6 @@ cudaError_t launch_embed_grad(const EmbedArgs& a, cudaStream_t st) {
   g.per = p.per;
   g.pieces = p.pieces;
   g.slabs = p.slabs;
-  g.sum_ctas = (int)(((long long)p.pieces * p.slabs + 7) / 8);
   if (a.f32) return a.out_f32 ? embed_grad_types<float, float>(g, st)
                               : embed_grad_types<float, __nv_bfloat16>(g, st);
   return a.out_f32 ? embed_grad_types<__nv_bfloat16, float>(g, st)

@@ -143,7 +143,12 @@ struct Schedule {
         if ((long long)n_rem * qa + (long long)(P - n_rem) * qb >= nw) break;
         T += 0.25f * cw + T * 1e-6f;
       }
-      my_w = p < n_rem ? qa : qb;
+      // this slot's dW tiles below nw (see get(): its t-th tile's number grows with t)
+      my_w = min(qa, p < nw ? (nw - 1 - p) / P + 1 : 0);
+      if (p >= n_rem && my_w == qa) {
+        const int rest = nw - qa * P - (p - n_rem);
+        if (rest > 0) my_w += min(qb - qa, (rest - 1) / (P - n_rem) + 1);
+      }
     }
   }
 
@@ -164,6 +169,10 @@ struct Schedule {
       u.split = 0;
       return true;
     } else {
+      // odd slots take their dW tiles first: dH reads the weights, dW writes their gradient, and
+      // the two halves of the traffic overlap
+      if (i >= my_h + my_w) return false;
+      if (p & 1) i = i < my_w ? i + my_h : i - my_w;
       if (i < my_h) {
         const int t = p + i * P;
         const int tile = t / a.splits;
@@ -176,10 +185,8 @@ struct Schedule {
         return true;
       }
       const int t = i - my_h;
-      if (t >= my_w) return false;
       // rounds in which every slot has a tile, then those of the slots with fewer dH units
       const int q = t < qa ? t * P + p : qa * P + (t - qa) * (P - n_rem) + (p - n_rem);
-      if (q >= nw) return false;
       u.kind = 2;
       u.split = 0;
       u.m0 = (q / nt_d) * MT;
@@ -225,7 +232,8 @@ SMDM_DEV uint8_t* stage_at(uint8_t* st, int row, int chunk) {
 
 // Write the staged rows to global memory: RB bytes of every row, at column `col` (elements) of
 // the row that `row_ptr(row)` gives (null: skip), of which `cols` columns exist.
-template <typename T, int RB, typename RowPtr>
+// kLast: nothing reads the data again soon (a gradient), so it need not stay in L2.
+template <typename T, int RB, bool kLast, typename RowPtr>
 SMDM_DEV void flush_rows(uint8_t* st, int lane, int col, int cols, bool vec, RowPtr row_ptr) {
   constexpr int C = RB / 16, E = 16 / (int)sizeof(T), RPI = 32 / C;
   __syncwarp();
@@ -237,7 +245,8 @@ SMDM_DEV void flush_rows(uint8_t* st, int lane, int col, int cols, bool vec, Row
     if (dst && c0 < cols) {
       const uint4 v = *reinterpret_cast<const uint4*>(stage_at<RB>(st, row, chunk));
       if (vec && c0 + E <= cols) {
-        *reinterpret_cast<uint4*>(dst + c0) = v;
+        if constexpr (kLast) __stcs(reinterpret_cast<uint4*>(dst + c0), v);
+        else *reinterpret_cast<uint4*>(dst + c0) = v;
       } else {
         const T* e = reinterpret_cast<const T*>(&v);
 #pragma unroll
@@ -584,12 +593,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                   w[j] = __bfloat162float(pl == 0 ? p0 : pl == 1 ? p1 : p2);
                 }
                 stage_bf16<RB>(st, lane, 0, w);
-                flush_rows<__nv_bfloat16, RB>(st, lane, col, a.ld_dlog, true, rp(pl));
+                flush_rows<__nv_bfloat16, RB, false>(st, lane, col, a.ld_dlog, true, rp(pl));
               }
             }
           }
           if constexpr (!F32)
-            flush_rows<__nv_bfloat16, RB>(st, lane, ccol + c * 32, a.ld_dlog, true, rp(0));
+            flush_rows<__nv_bfloat16, RB, false>(st, lane, ccol + c * 32, a.ld_dlog, true, rp(0));
         }
       } else if (u.kind == 1 && a.acc) {
         // fp32 sums of this piece and K range
@@ -615,7 +624,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
             }
           }
-          flush_rows<float, 128>(st, lane, col, a.d_pad, true, [&](int r) -> float* {
+          flush_rows<float, 128, false>(st, lane, col, a.d_pad, true, [&](int r) -> float* {
             return row - lane + r < n ? base + (size_t)(row - lane + r) * a.d_pad : nullptr;
           });
         }
@@ -640,7 +649,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if constexpr (F32) stage_f32(st, lane, v);
             else stage_bf16<RB>(st, lane, s2 * 4, v);
           }
-          flush_rows<T, RB>(st, lane, ccol + c * 32, a.d, a.vec_ok != 0, rp);
+          flush_rows<T, RB, true>(st, lane, ccol + c * 32, a.d, a.vec_ok != 0, rp);
         }
       }
       if (!kRegs && !empty_sum) release();
