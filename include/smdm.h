@@ -369,7 +369,8 @@ size_t smdm_head_loss_workspace_bytes(const smdm_head_shape* shape, int grad);
  * into d_nll and d_lse, fp32 [rows].  A row with a negative target takes no part: nll = lse = 0,
  * and nothing that its hidden row holds (NaN included) reaches any output.  bf16 lm_head rows
  * that lie on 16-byte boundaries (d_model and ld_head multiples of 8) are read in place; the
- * tensor must then start on one too (SMDM_EINVAL). */
+ * tensor must then start on one too (SMDM_EINVAL).  Rows that take part and the weights are taken
+ * to be finite. */
 smdm_status smdm_head_loss(const smdm_head_shape* shape, const void* d_hidden,
                            const void* d_lm_head, const int32_t* d_target, float* d_nll,
                            float* d_lse, void* d_workspace, size_t bytes, uint32_t* d_status,

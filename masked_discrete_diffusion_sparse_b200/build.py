@@ -19,7 +19,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libsmdm.so")
-SOURCES = ["api.cu", "gemm.cu", "attn.cu", "misc.cu", "head.cu", "ends.cu", "training.cu"]
+SOURCES = ["api.cu", "gemm.cu", "attn.cu", "misc.cu", "head.cu", "head_few.cu", "ends.cu", "training.cu"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
 

@@ -49,12 +49,14 @@ struct HeadMeta {
 };
 
 struct HeadDev {
-  const HeadMeta* meta;
+  const HeadMeta* meta;     // null: row i is the caller's row i
   const int* row_idx;       // row that takes part -> row of the caller's tensors
   const int* target;
+  int rows;
   int d, v0, vc;            // width; first column and columns of this piece
   int w_row0;               // row of the weight map that holds column v0
-  int terms;                // 1 (bf16) or 6 (fp32 as three bf16 parts)
+  int terms;                // products of parts: 1 (bf16), 2 (D in two parts) or 6 (three each)
+  int d_parts;              // bf16 parts of D
   int h_plane, w_plane, d_plane;   // rows between the parts of H, W, D in their maps
   int a_box;                // rows of A that one box brings (K-major H)
   int nstages, staging_off, bar_off;
@@ -99,6 +101,12 @@ constexpr int kTileCost = 6;
 // chunks (512 terms) at a time, and the epilogue threads add the segments in registers, rounded
 // to nearest.  Where it is rounded to bf16 next, the cut does not matter and K is summed whole.
 constexpr int kSegment = 8;
+
+// Rounding D to one bf16 part adds an error as large as the gradients' own rounding (together
+// 2.4e-3 of their norm against 1.7e-3).  Up to this many rows the products are bound by the
+// weights' traffic, and a second part (the rounding's remainder) costs XX; above it would cost
+// another pair of products (XX).
+constexpr int kTwoPartRows = 256;
 template <int kMode, bool F32>
 constexpr bool kPromote = F32 || kMode == kLoss;
 
@@ -199,8 +207,10 @@ struct Schedule {
 };
 
 // The two parts' planes of term t, smallest products first.
-SMDM_DEV int term_a(int terms, int t) { return terms == 1 ? 0 : (0x021010 >> (4 * (5 - t))) & 15; }
-SMDM_DEV int term_b(int terms, int t) { return terms == 1 ? 0 : (0x201100 >> (4 * (5 - t))) & 15; }
+SMDM_DEV int term_a(int terms, int t) {
+  return terms == 6 ? (0x021010 >> (4 * (5 - t))) & 15 : terms - 1 - t;
+}
+SMDM_DEV int term_b(int terms, int t) { return terms == 6 ? (0x201100 >> (4 * (5 - t))) & 15 : 0; }
 
 // x = p0 + p1 + p2 with bf16 parts; an infinity or NaN stays in the first part alone.
 SMDM_DEV void split3(float x, __nv_bfloat16& p0, __nv_bfloat16& p1, __nv_bfloat16& p2) {
@@ -335,8 +345,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   griddep_launch();
   griddep_wait();
 
-  const int n = a.meta->n;
-  const bool dense = a.meta->dense != 0;
+  // (no meta: every row of the caller's hidden, listed or not)
+  const int n = a.meta ? a.meta->n : a.rows;
+  const bool dense = a.meta ? a.meta->dense != 0 : true;
   const Schedule<kMode, CG, BN> sch(a, n, blockIdx.x / CG, gridDim.x / CG);
   auto lead_addr = [&](uint64_t* bar) -> uint32_t {
     return CG == 2 ? mapa_shared(smem_u32(bar), 0) : smem_u32(bar);
@@ -459,7 +470,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       float lse = 0.f, g = 0.f;
       if (kMode != kGrad || u.kind == 1) {
         if (row < n) {
-          my_row = a.row_idx[row];
+          my_row = a.meta ? a.row_idx[row] : row;
           if constexpr (kMode != kGrad) tgt = a.target[my_row] - a.v0 - u.n0 - half * HC;
           if constexpr (kMode == kDlog) {
             lse = a.lse[my_row];
@@ -548,9 +559,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (mine) a.tlogit[row] = tv;
           }
           float y[4] = {0.f, 0.f, 0.f, 0.f};
+          const float ref = mn == -INFINITY ? 0.f : mn;   // (no column above -inf so far)
 #pragma unroll
-          for (int j = 0; j < 32; ++j) y[j & 3] += ex2((v[j] - mn) * kLog2e);
-          s = s * ex2((m - mn) * kLog2e) + ((y[0] + y[1]) + (y[2] + y[3]));
+          for (int j = 0; j < 32; ++j) y[j & 3] += ex2((v[j] - ref) * kLog2e);
+          s = s * ex2((m - ref) * kLog2e) + ((y[0] + y[1]) + (y[2] + y[3]));
           m = mn;
         }
         if (row < n)
@@ -582,7 +594,23 @@ __global__ void __launch_bounds__(kThreads, 1)
               v[j] = j < lim ? p * g : 0.f;
             }
             if constexpr (!F32) {
-              stage_bf16<RB>(st, lane, s2 * 4, v);
+              if (a.d_parts == 2) {
+                // the rounding's remainder, as the second part
+                float w[32];
+#pragma unroll
+                for (int j = 0; j < 32; ++j) {
+                  const float hi = __bfloat162float(__float2bfloat16_rn(v[j]));
+                  w[j] = fabsf(hi) <= 3.3895314e38f ? v[j] - hi : 0.f;
+                }
+                stage_bf16<RB>(st, lane, 0, w);
+                flush_rows<__nv_bfloat16, RB, false>(st, lane, col, min(a.ld_dlog, col + 32), true,
+                                                     rp(1));
+                stage_bf16<RB>(st, lane, 0, v);
+                flush_rows<__nv_bfloat16, RB, false>(st, lane, col, min(a.ld_dlog, col + 32), true,
+                                                     rp(0));
+              } else {
+                stage_bf16<RB>(st, lane, s2 * 4, v);
+              }
             } else {
               for (int pl = 0; pl < planes; ++pl) {
                 float w[32];
@@ -598,7 +626,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
           if constexpr (!F32)
-            flush_rows<__nv_bfloat16, RB, false>(st, lane, ccol + c * 32, a.ld_dlog, true, rp(0));
+            if (a.d_parts == 1)
+              flush_rows<__nv_bfloat16, RB, false>(st, lane, ccol + c * 32, a.ld_dlog, true, rp(0));
         }
       } else if (u.kind == 1 && a.acc) {
         // fp32 sums of this piece and K range
@@ -872,13 +901,14 @@ __global__ void __launch_bounds__(256) head_weights_kernel(RowsArgs a, WeightArg
 // nll and lse of the listed rows from the column groups' (maximum, sum) pairs.  32 rows per CTA
 // (a lane each), 32 warps over the groups; a warp has eight pairs in flight.
 __global__ void __launch_bounds__(1024)
-    head_finish_kernel(const HeadMeta* meta, const int* row_idx, const float2* part, int n_part,
-                       int r_pad, const float* tlogit, float* nll, float* lse) {
+    head_finish_kernel(const HeadMeta* meta, const int* row_idx, const int* target, int rows,
+                       int vocab, const float2* part, int n_part, int r_pad, const float* tlogit,
+                       float* nll, float* lse, uint32_t* status) {
   griddep_launch();
   griddep_wait();
   __shared__ float2 sh[32][33];
   const int lane = threadIdx.x & 31, g = threadIdx.x >> 5;
-  const int n = meta->n;
+  const int n = meta ? meta->n : rows;
   const int row = blockIdx.x * 32 + lane;
   if (blockIdx.x * 32 >= n) return;
   float m = -INFINITY, s = 0.f;
@@ -910,9 +940,12 @@ __global__ void __launch_bounds__(1024)
   const int out = blockIdx.x * 32 + g;
   if (lane == 0 && out < n) {
     const float l = logf(s);
-    const int r = row_idx[out];
-    lse[r] = m + l;
-    nll[r] = (m - tlogit[out]) + l;
+    const int r = meta ? row_idx[out] : out;
+    const int t = target[r];
+    const bool on = t >= 0 && t < vocab;      // (without the list: also rows that take no part)
+    if (t >= vocab && status) atomicOr(status, kStatusBounds);
+    lse[r] = on ? m + l : 0.f;
+    nll[r] = on ? (m - tlogit[out]) + l : 0.f;
   }
 }
 
@@ -954,14 +987,19 @@ __global__ void __launch_bounds__(256)
 size_t up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
 int sm_count() {
+  static int cached[64];
   int dev = 0, n = 148;
-  if (cudaGetDevice(&dev) == cudaSuccess)
-    cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
-  return n;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return n;
+  if (!cached[dev] &&
+      cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess)
+    cached[dev] = n;
+  return cached[dev] ? cached[dev] : n;
 }
 
 struct Plan {
+  bool few;           // head_few.cu takes the call
   int parts, terms, r_pad, d_pad;
+  int d_parts, g_terms;   // bf16 parts of D; products summed by the gradients
   bool staged;        // weights go through a bf16 copy of each piece
   int piece, n_pieces;
   size_t meta, row_idx, hid, part, tlogit, wst, dlog, acc, total;
@@ -1007,9 +1045,16 @@ Plan make_plan(int rows, int d, int vocab, long long ld_head, bool f32, bool gra
   p.r_pad = (int)up(rows, 256);
   p.d_pad = (int)up(d, 64);
   p.staged = !weight_in_place(d, ld_head, f32);
+  p.few = head_few_fits(rows, d) && (grad || p.staged);
+  if (p.few) {
+    p.total = head_few_bytes(rows, d, vocab, sms);
+    return p;
+  }
+  p.d_parts = f32 ? 3 : rows <= kTwoPartRows ? 2 : 1;
+  p.g_terms = f32 ? 6 : p.d_parts;
   // widest piece whose D (gradient) and weight copy (when made) stay below kPieceBytes
   size_t per_col = 0;
-  if (grad) per_col = (size_t)p.parts * p.r_pad * 2;
+  if (grad) per_col = (size_t)p.d_parts * p.r_pad * 2;
   if (p.staged) per_col = std::max(per_col, (size_t)p.parts * p.d_pad * 2);
   const int v_pad = (int)up(vocab, 256);
   p.piece = v_pad;
@@ -1032,7 +1077,7 @@ Plan make_plan(int rows, int d, int vocab, long long ld_head, bool f32, bool gra
       const long long nt = (d + bnc - 1) / bnc;
       const double ch = chunk_clocks(c, 128), epi = bnc * 8.0 / ch;   // a tile's fixed cost
       const long long nh = (rows + mt - 1) / mt * nt, nw = (p.piece + mt - 1) / mt * nt;
-      const double uh = (double)kh * p.terms, uw = (double)kw * p.terms + epi;
+      const double uh = (double)kh * p.g_terms, uw = (double)kw * p.g_terms + epi;
       const double share = (nh * (uh + epi) + nw * uw) / slots;
       const int s = (int)std::min<double>(std::min<long long>(32, kh), std::max(1.0, uh / std::max(share, 8.0)));
       const double t = ch * std::max(std::max(share, uw), uh / s + epi);
@@ -1054,7 +1099,7 @@ Plan make_plan(int rows, int d, int vocab, long long ld_head, bool f32, bool gra
   }
   if (p.staged) p.wst = take((size_t)p.parts * p.piece * p.d_pad * 2);
   if (grad) {
-    p.dlog = take((size_t)p.parts * p.r_pad * p.piece * 2);
+    p.dlog = take((size_t)p.d_parts * p.r_pad * p.piece * 2);
     if (p.splits > 1 || p.n_pieces > 1) p.acc = take((size_t)p.splits * p.r_pad * p.d_pad * 4);
   }
   p.total = off;
@@ -1166,11 +1211,12 @@ struct Call {
   int sms;
   uint8_t* ws;
   bool in_place;    // the caller's hidden can be read by TMA
+  bool loss;
   template <typename T> T* at(size_t off) const { return reinterpret_cast<T*>(ws + off); }
 
   Call(const HeadArgs& a, bool grad)
       : h(a), p(make_plan(a.rows, a.d, a.vocab, a.ld_head, a.f32, grad)), sms(sm_count()),
-        ws(static_cast<uint8_t*>(a.ws)) {
+        ws(static_cast<uint8_t*>(a.ws)), loss(!grad) {
     in_place = !a.f32 && a.d % 8 == 0 && a.ld_hidden % 8 == 0 && aligned16(a.hidden);
   }
 
@@ -1217,8 +1263,14 @@ struct Call {
     w.ctas = std::min(w.vc_pad / 8, sms * 8);
     return w;
   }
+  // The loss of at most 128 rows that lie on 16-byte boundaries skips the list: they fill one
+  // row of tiles either way, and a row of the product that takes no part touches no other.  (Not
+  // the gradient: dW sums over the rows.)
+  bool listed() const { return !(loss && in_place && !p.staged && h.rows <= 128); }
+  HeadMeta* meta() const { return listed() ? at<HeadMeta>(p.meta) : nullptr; }
   // The rows that take part, and the first piece's weights.
   cudaError_t rows(cudaStream_t st) const {
+    if (!listed()) return cudaSuccess;
     const RowsArgs r = row_args();
     const WeightArgs w = weight_args(0, std::min(p.piece, h.vocab));
     return launch_pdl(head_rows_kernel, dim3(r.row_ctas + w.ctas), dim3(256), 0, st, 1, r, w);
@@ -1244,7 +1296,8 @@ struct Call {
   }
   HeadDev dev(int v0, int vc) const {
     HeadDev a{};
-    a.meta = at<HeadMeta>(p.meta);
+    a.meta = meta();
+    a.rows = h.rows;
     a.row_idx = at<int>(p.row_idx);
     a.target = h.target;
     a.d = h.d;
@@ -1277,12 +1330,15 @@ bool head_needs_aligned_weight(int d, long long ld_head, bool f32) {
 }
 
 int head_loss_launches(const HeadArgs& a) {
-  const Plan p = make_plan(a.rows, a.d, a.vocab, a.ld_head, a.f32, false);
-  return 2 + p.n_pieces + (p.staged ? p.n_pieces - 1 : 0);
+  const Call c(a, false);
+  const Plan& p = c.p;
+  if (p.few) return 2;
+  return 1 + (c.listed() ? 1 : 0) + p.n_pieces + (p.staged ? p.n_pieces - 1 : 0);
 }
 
 int head_grad_launches(const HeadArgs& a) {
   const Plan p = make_plan(a.rows, a.d, a.vocab, a.ld_head, a.f32, true);
+  if (p.few) return a.grad_hidden ? 3 : 2;
   const bool sums = p.splits > 1 || p.n_pieces > 1;
   return 1 + 2 * p.n_pieces + (p.staged ? p.n_pieces - 1 : 0) + (sums && a.grad_hidden ? 1 : 0);
 }
@@ -1290,6 +1346,7 @@ int head_grad_launches(const HeadArgs& a) {
 cudaError_t launch_head_loss(const HeadArgs& h, cudaStream_t st) {
   const Call c(h, false);
   const Plan& p = c.p;
+  if (p.few) return launch_head_few_loss(h, c.sms, st);
   TRY(c.rows(st));
   const int cg = kCfgCG[p.cfg], bn = kCfgBN[p.cfg];
   for (int i = 0; i < p.n_pieces; ++i) {
@@ -1310,13 +1367,15 @@ cudaError_t launch_head_loss(const HeadArgs& h, cudaStream_t st) {
   const int last = h.vocab - (p.n_pieces - 1) * p.piece;
   const int n_part = 2 * (p.piece / bn) * (p.n_pieces - 1) + 2 * ((last + bn - 1) / bn);
   return launch_pdl(head_finish_kernel, dim3((h.rows + 31) / 32), dim3(1024),
-                    0, st, 1, c.at<HeadMeta>(p.meta), c.at<int>(p.row_idx), c.at<float2>(p.part),
-                    n_part, p.r_pad, c.at<float>(p.tlogit), h.nll, h.lse_out);
+                    0, st, 1, c.meta(), c.at<int>(p.row_idx), h.target, h.rows, h.vocab,
+                    c.at<float2>(p.part), n_part, p.r_pad, c.at<float>(p.tlogit), h.nll, h.lse_out,
+                    h.status);
 }
 
 cudaError_t launch_head_grad(const HeadArgs& h, cudaStream_t st) {
   const Call c(h, true);
   const Plan& p = c.p;
+  if (p.few) return launch_head_few_grad(h, c.sms, st);
   TRY(c.rows(st));
   const int cg = kCfgCG[p.cfg], bn = kCfgBN[p.cfg];
   const int gcg = kCfgCG[p.cfg_g], gbn = kCfgBN[p.cfg_g];
@@ -1331,6 +1390,7 @@ cudaError_t launch_head_grad(const HeadArgs& h, cudaStream_t st) {
     if (!c.hidden_maps(&m.h, &m.hc, a.a_box) || !c.weight_map(&m.w, vc, bn / cg))
       return cudaErrorInvalidValue;
     m.dk = m.dm = m.hc;
+    a.d_parts = p.d_parts;
     a.lse = h.lse;
     a.grad_nll = h.grad_nll;
     a.dlog = c.at<__nv_bfloat16>(p.dlog);
@@ -1339,9 +1399,10 @@ cudaError_t launch_head_grad(const HeadArgs& h, cudaStream_t st) {
     TRY(launch_mode<kDlog>(h.f32, p.cfg, m, a, units, c.sms, st));
     // both products of D: 64-row boxes for the MN-major operands
     if (!c.hidden_maps(&m.h, &m.hc, 64) || !c.weight_map(&m.w, vc, 64) ||
-        !encode_bf16(&m.dk, a.dlog, p.piece, (uint64_t)p.parts * p.r_pad, p.piece, 64, 128) ||
-        !encode_bf16(&m.dm, a.dlog, p.piece, (uint64_t)p.parts * p.r_pad, p.piece, 64, 64))
+        !encode_bf16(&m.dk, a.dlog, p.piece, (uint64_t)p.d_parts * p.r_pad, p.piece, 64, 128) ||
+        !encode_bf16(&m.dm, a.dlog, p.piece, (uint64_t)p.d_parts * p.r_pad, p.piece, 64, 64))
       return cudaErrorInvalidValue;
+    a.terms = p.g_terms;
     a.do_h = h.grad_hidden != nullptr;
     a.do_w = h.grad_head != nullptr;
     a.splits = p.splits;

@@ -31,4 +31,12 @@ int head_grad_launches(const HeadArgs& a);
 cudaError_t launch_head_loss(const HeadArgs& a, cudaStream_t st);
 cudaError_t launch_head_grad(const HeadArgs& a, cudaStream_t st);
 
+// The same for a handful of rows (head_few.cu); `sms`: SMs of the device.
+constexpr int kFewRows = 16;
+constexpr int kFewSmem = 200 * 1024;     // all hidden rows in fp32
+bool head_few_fits(int rows, int d);
+size_t head_few_bytes(int rows, int d, int vocab, int sms);
+cudaError_t launch_head_few_loss(const HeadArgs& a, int sms, cudaStream_t st);
+cudaError_t launch_head_few_grad(const HeadArgs& a, int sms, cudaStream_t st);
+
 }  // namespace smdm

@@ -141,16 +141,17 @@ class Head:
         D = p.clone()
         D.scatter_add_(1, t, torch.full_like(g, -1.0))
         D *= g
-        # errors of D: the logit's and exp's (systematic), its rounding (independent)
+        # errors of D: the logit's and exp's (systematic), its rounding (independent; with 256 rows
+        # or fewer D keeps two bf16 parts: 2^-16)
         sys_d = g.abs() * p * (dz[:, None] + 2.0 ** -20)
-        u = 2.0 ** -8 if self.dt == BF16 else 2.0 ** -23
+        u = (2.0 ** -8 if self.rows > 256 else 2.0 ** -16) if self.dt == BF16 else 2.0 ** -23
         out = u_of(self.dt)
         for what, got, ref, s, q, mag, k in (
                 ("grad_hidden", gh, D @ w, sys_d @ w.abs(), (D * D) @ (w * w), D.abs() @ w.abs(),
                  self.vocab),
                 ("grad_lm_head", gw, D.T @ h, sys_d.T @ h.abs(), (D * D).T @ (h * h),
                  D.abs().T @ h.abs(), self.rows)):
-            terms = 6 if self.dt == F32 else 1
+            terms = 6 if self.dt == F32 else 2
             acc = (terms * k / 16 + 17) * 2.0 ** -23 + (2.0 ** -23 if self.dt == F32 else 0)
             bound = s + 6 * u * (q / 3).sqrt() + acc * mag
             within(got, ref, bound + out * (ref.abs() + bound) + 1e-37, what)
@@ -177,6 +178,13 @@ HEAD_CASES = [
     (331, 256, 1001, F32, 0.3, 5, 1),
     (1024, 256, 1024, F32, 0.5, 0, 0),
     (640, 130, 2111, F32, 0, 0, 0),
+    # a handful of rows
+    (16, 589, 3001, F32, 0, 0, 0), (16, 120, 1030, BF16, 0.4, 1, 3), (3, 589, 1999, BF16, 0, 0, 0),
+    (7, 4096, 700, F32, 0.2, 4, 0), (13, 4096, 515, F32, 0, 0, 0), (9, 8, 2, BF16, 0, 0, 0),
+    (4, 1000, 5003, F32, 0, 0, 0), (12, 2048, 4099, BF16, 0.3, 0, 0), (2, 1, 70, F32, 0, 0, 0),
+    (17, 256, 900, F32, 0, 0, 0),
+    # one row of tiles
+    (128, 320, 1500, BF16, 0.3, 0, 0), (100, 1024, 8200, BF16, 0, 8, 0),
 ]
 
 
@@ -196,12 +204,14 @@ def test_head_gradient_in_several_pieces(dt, rows, vocab):
     x.check_grad(lse)
 
 
-def test_head_rows_without_a_target_reach_nothing():
-    x = Head(200, 128, 700, BF16, 0.4, seed=5)
+@pytest.mark.parametrize("rows,d,dt", [(200, 128, BF16), (100, 64, BF16), (14, 128, BF16),
+                                       (14, 30, F32), (150, 30, F32)])
+def test_head_rows_without_a_target_reach_nothing(rows, d, dt):
+    x = Head(rows, d, 700, dt, 0.4, seed=5)
     nll, lse = x.loss()
     a = x.grad(lse)
     off = x.target < 0
-    for bad in (float("nan"), float("inf"), torch.finfo(BF16).min):
+    for bad in (float("nan"), float("inf"), torch.finfo(dt).min):
         x.h[off] = bad
         lse2 = lse.clone()
         lse2[off] = float("nan")
@@ -214,8 +224,9 @@ def test_head_rows_without_a_target_reach_nothing():
 
 
 @pytest.mark.parametrize("dt", [BF16, F32])
-def test_head_no_row_takes_part(dt):
-    x = Head(70, 96, 300, dt, seed=6)
+@pytest.mark.parametrize("rows", [70, 5, 300])
+def test_head_no_row_takes_part(dt, rows):
+    x = Head(rows, 96, 300, dt, seed=6)
     x.target.fill_(-7)
     nll, lse = x.loss()
     gh, gw = x.grad(lse)
@@ -227,8 +238,9 @@ def test_head_no_row_takes_part(dt):
     assert (gw == 0).all()
 
 
-def test_head_target_beyond_the_vocabulary_sets_the_status():
-    x = Head(50, 64, 100, BF16, seed=7)
+@pytest.mark.parametrize("rows,dt", [(50, BF16), (10, BF16), (10, F32), (150, F32)])
+def test_head_target_beyond_the_vocabulary_sets_the_status(rows, dt):
+    x = Head(rows, 64, 100, dt, seed=7)
     x.target[3] = 100
     x.target[9] = 2 ** 31 - 1
     nll, lse = x.loss()
@@ -240,8 +252,9 @@ def test_head_target_beyond_the_vocabulary_sets_the_status():
     assert (gh[3] == 0).all() and (gh[9] == 0).all() and (gh[4] != 0).any()
 
 
-def test_head_one_gradient_alone():
-    x = Head(300, 136, 900, BF16, 0.3, seed=8)
+@pytest.mark.parametrize("rows", [300, 11])
+def test_head_one_gradient_alone(rows):
+    x = Head(rows, 136, 900, BF16, 0.3, seed=8)
     _, lse = x.loss()
     gh, gw = x.grad(lse)
     assert torch.equal(x.grad(lse, want=(True, False))[0], gh)
@@ -256,8 +269,9 @@ def test_head_large_logits_and_a_certain_target():
     assert nll.max() > 20
 
 
-def test_head_same_bits_every_time():
-    x = Head(900, 320, 3001, BF16, 0.2, seed=10)
+@pytest.mark.parametrize("rows", [900, 12])
+def test_head_same_bits_every_time(rows):
+    x = Head(rows, 320, 3001, BF16, 0.2, seed=10)
     nll, lse = x.loss()
     a = x.grad(lse)
     for _ in range(3):
