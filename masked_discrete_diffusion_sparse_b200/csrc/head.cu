@@ -227,6 +227,22 @@ SMDM_DEV float ex2(float x) {
   return y;
 }
 
+// One lane of a converged warp.  The producer and MMA warps run their loops as whole warps, so
+// that loop counters, addresses and descriptors are warp-uniform, and only the instructions
+// that one thread must issue are under this predicate.  With the loops inside `if (lane == 0)`
+// instead an MMA took 65 clocks to issue whatever its size, and a 64-wide chunk about 500.
+SMDM_DEV bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}\n"
+      : "=r"(p));
+  return p != 0;
+}
+// mbar_wait by a whole warp.
+SMDM_DEV bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort, uint32_t* status) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort, status));
+}
+
 SMDM_DEV uint32_t pack_bf16(float a, float b) {
   const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
   return *reinterpret_cast<const uint32_t*>(&v);
@@ -311,7 +327,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(acc_empty + 2);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const uint32_t rank = CG == 2 ? cluster_ctarank() : 0u;
   const bool leader = rank == 0;
   if (threadIdx.x == 0) {
@@ -354,7 +370,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   };
 
   if (warp == 0) {
-    if (lane == 0) {
+    {
       const uint64_t pol = policy_evict_normal();
       int stage = 0;
       uint32_t phase = 0;
@@ -368,9 +384,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int t = 0; ok && t < a.terms; ++t) {
           const int pa = term_a(a.terms, t), pb = term_b(a.terms, t);
           for (int k = u.k0; k < u.k0 + u.nk; ++k) {
-            if (!mbar_wait(&empty[stage], phase ^ 1, abort_flag, a.status)) { ok = false; break; }
+            if (!warp_wait(&empty[stage], phase ^ 1, abort_flag, a.status)) { ok = false; break; }
             uint8_t* A = smem + stage * kStage;
             uint8_t* B = A + kABytes;
+            if (elect_one()) {
             const int ab = u.kind == 0 ? a.a_box * 128 : kABytes;
             if (leader) mbar_arrive_expect_tx(&full[stage], CG * (ab + kBRows * 128));
             const uint32_t fb = lead_addr(&full[stage]);
@@ -394,6 +411,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               for (int j = 0; j < kBRows / 64; ++j)
                 load(B + j * 8192, th, n0 + j * 64, pb * h_plane + k * 64);
             }
+            }
+            __syncwarp();
             if (++stage == a.nstages) { stage = 0; phase ^= 1; }
           }
         }
@@ -402,13 +421,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         // The pair's MMA completions arrive on these barriers from the first CTA: wait until
         // every stage is released so that no arrival lands after this CTA has exited.
         for (int s = 0; ok && s < a.nstages; ++s) {
-          if (!mbar_wait(&empty[stage], phase ^ 1, abort_flag, a.status)) break;
+          if (!warp_wait(&empty[stage], phase ^ 1, abort_flag, a.status)) break;
           if (++stage == a.nstages) { stage = 0; phase ^= 1; }
         }
       }
     }
   } else if (warp == 1) {
-    if (lane == 0 && leader) {
+    if (leader) {
       int stage = 0, acc = 0;
       uint32_t phase = 0, acc_phase = 0;
       Unit u;
@@ -424,15 +443,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         // (no chunks at all: nothing to sum, the epilogue writes zeros)
         for (int c0 = 0; ok && c0 < total;) {
           const int c1 = kPromote<kMode, F32> ? min(total, c0 + kSegment) : total;
-          if (!mbar_wait(&acc_empty[acc], acc_phase ^ 1, abort_flag, a.status)) { ok = false; break; }
+          if (!warp_wait(&acc_empty[acc], acc_phase ^ 1, abort_flag, a.status)) { ok = false; break; }
           tc_fence_after();
           const uint32_t d = tbase + acc * BN;
           for (int c = c0; c < c1; ++c) {
-            if (!mbar_wait(&full[stage], phase, abort_flag, a.status)) { ok = false; break; }
+            if (!warp_wait(&full[stage], phase, abort_flag, a.status)) { ok = false; break; }
             tc_fence_after();
             const uint32_t a_addr = smem_u32(smem + stage * kStage);
             const uint64_t ad = sdesc_sw128(a_addr, a_lbo, 1024);
             const uint64_t bd = sdesc_sw128(a_addr + kABytes, b_lbo, 1024);
+            if (elect_one()) {
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk) {
               const uint32_t accum = (c > c0 || kk > 0) ? 1u : 0u;
@@ -443,11 +463,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if constexpr (CG == 2) umma_commit_pair(&empty[stage]);
             else umma_commit(&empty[stage]);
+            }
+            __syncwarp();
             if (++stage == a.nstages) { stage = 0; phase ^= 1; }
           }
           if (!ok) break;
-          if constexpr (CG == 2) umma_commit_pair(&acc_full[acc]);
-          else umma_commit(&acc_full[acc]);
+          if (elect_one()) {
+            if constexpr (CG == 2) umma_commit_pair(&acc_full[acc]);
+            else umma_commit(&acc_full[acc]);
+          }
+          __syncwarp();
           acc ^= 1;
           if (acc == 0) acc_phase ^= 1;
           c0 = c1;
