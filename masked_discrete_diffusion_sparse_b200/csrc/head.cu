@@ -55,7 +55,7 @@ struct HeadDev {
   int rows;
   int d, v0, vc;            // width; first column and columns of this piece
   int w_row0;               // row of the weight map that holds column v0
-  int terms;                // products of parts: 1 (bf16), 2 (D in two parts) or 6 (three each)
+  int terms;                // products of parts per chunk (the schedule's weight of a chunk)
   int d_parts;              // bf16 parts of D
   int h_plane, w_plane, d_plane;   // rows between the parts of H, W, D in their maps
   int a_box;                // rows of A that one box brings (K-major H)
@@ -95,21 +95,35 @@ struct Unit {
 
 constexpr int kTileCost = 6;
 
-// The tensor core cuts its fp32 sums instead of rounding them: measured, a sum over K terms comes
-// out smaller by 2^-30 K of its value (1.0e-6 at K = 1024, 4.0e-6 at 4096).  Where the result is
-// fp32 (the loss, and everything of the fp32 path) the tensor core therefore sums kSegment
-// chunks (512 terms) at a time, and the epilogue threads add the segments in registers, rounded
-// to nearest.  Where it is rounded to bf16 next, the cut does not matter and K is summed whole.
-constexpr int kSegment = 8;
+// Operands in parts.  P = 1: bf16 operands.  P = 2 (gradients of few rows): D in two bf16 parts.
+// P = 3 (fp32): both operands in three.  A pipeline stage holds a 64-wide K chunk of all parts,
+// and the products of parts that count are summed from it, smallest first.
+template <int P> constexpr int kAParts = P;
+template <int P> constexpr int kBParts = P == 3 ? 3 : 1;
+template <int P> constexpr int kProducts = P == 3 ? 6 : P;
+// parts of A and B in product t (t = 0 the smallest)
+template <int P> __host__ __device__ constexpr int part_a(int t) {
+  return P == 3 ? (0x021010 >> (4 * (5 - t))) & 15 : P - 1 - t;
+}
+template <int P> __host__ __device__ constexpr int part_b(int t) {
+  return P == 3 ? (0x201100 >> (4 * (5 - t))) & 15 : 0;
+}
+
+// The tensor core cuts its fp32 sums instead of rounding them: measured, every 16-term step takes
+// 2^-26 of the sum's value off (1.0e-6 at K = 1024, 4.0e-6 at 4096).  Where the result is fp32
+// (the loss, and everything of the fp32 path) the tensor core therefore sums kSegment chunks at a
+// time, 24 to 32 steps, and the epilogue threads add the segments in registers, rounded to
+// nearest.  Where the result is rounded to bf16 next, the cut does not matter and K is summed
+// whole.
+template <int P> constexpr int kSegment = P == 3 ? 1 : 8;
+template <int kMode, int P>
+constexpr bool kPromote = P == 3 || kMode == kLoss;
 
 // Rounding D to one bf16 part adds an error as large as the gradients' own rounding (together
 // 2.4e-3 of their norm against 1.7e-3).  Up to this many rows the products are bound by the
 // weights' traffic, and a second part (the rounding's remainder) costs XX; above it would cost
 // another pair of products (XX).
 constexpr int kTwoPartRows = 256;
-template <int kMode, bool F32>
-constexpr bool kPromote = F32 || kMode == kLoss;
-
 // The work of one slot (CTA or pair) p of P.  Loss and D: tiles round robin, in groups of 16 row
 // tiles so that a group's rows stay in L2 while the weights pass once.  Gradients: the dH units
 // round robin, then the dW tiles so that every slot ends at about the same number of K chunks
@@ -206,12 +220,6 @@ struct Schedule {
   }
 };
 
-// The two parts' planes of term t, smallest products first.
-SMDM_DEV int term_a(int terms, int t) {
-  return terms == 6 ? (0x021010 >> (4 * (5 - t))) & 15 : terms - 1 - t;
-}
-SMDM_DEV int term_b(int terms, int t) { return terms == 6 ? (0x201100 >> (4 * (5 - t))) & 15 : 0; }
-
 // x = p0 + p1 + p2 with bf16 parts; an infinity or NaN stays in the first part alone.
 SMDM_DEV void split3(float x, __nv_bfloat16& p0, __nv_bfloat16& p1, __nv_bfloat16& p2) {
   p0 = __float2bfloat16_rn(x);
@@ -305,8 +313,8 @@ SMDM_DEV void stage_f32(uint8_t* st, int lane, const float* v) {
 }
 
 // kMode: what is computed.  CG: CTAs per tile (2: a pair on two SMs, M = 256).  BN: tile
-// columns.  F32: the outputs (and D's parts) are the fp32 path's.
-template <int kMode, int CG, int BN, bool F32>
+// columns.  P: operand parts; 3 is the fp32 path.
+template <int kMode, int CG, int BN, int P>
 __global__ void __launch_bounds__(kThreads, 1)
     head_gemm_kernel(const __grid_constant__ CUtensorMap tm_h,    // caller's hidden (K-major box)
                      const __grid_constant__ CUtensorMap tm_hc,   // listed rows, or same box
@@ -318,7 +326,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
   constexpr int kBRows = BN / CG;                    // rows (columns of the product) of B here
-  constexpr int kStage = kABytes + kBRows * 128;
+  constexpr bool F32 = P == 3;
+  constexpr int kBPart = kBRows * 128;
+  constexpr int kStage = kAParts<P> * kABytes + kBParts<P> * kBPart;
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + a.bar_off);
   uint64_t* full = bars;
   uint64_t* empty = bars + kMaxStages;
@@ -381,40 +391,46 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int i = 0; ok && sch.get(a, i, u); ++i) {
         const int m0 = u.m0 + (int)rank * 128;
         const int n0 = u.n0 + (int)rank * kBRows;
-        for (int t = 0; ok && t < a.terms; ++t) {
-          const int pa = term_a(a.terms, t), pb = term_b(a.terms, t);
-          for (int k = u.k0; k < u.k0 + u.nk; ++k) {
-            if (!warp_wait(&empty[stage], phase ^ 1, abort_flag, a.status)) { ok = false; break; }
-            uint8_t* A = smem + stage * kStage;
-            uint8_t* B = A + kABytes;
-            if (elect_one()) {
+        for (int k = u.k0; k < u.k0 + u.nk; ++k) {
+          if (!warp_wait(&empty[stage], phase ^ 1, abort_flag, a.status)) { ok = false; break; }
+          uint8_t* A = smem + stage * kStage;
+          uint8_t* B = A + kAParts<P> * kABytes;
+          if (elect_one()) {
             const int ab = u.kind == 0 ? a.a_box * 128 : kABytes;
-            if (leader) mbar_arrive_expect_tx(&full[stage], CG * (ab + kBRows * 128));
+            if (leader)
+              mbar_arrive_expect_tx(&full[stage], CG * (kAParts<P> * ab + kBParts<P> * kBPart));
             const uint32_t fb = lead_addr(&full[stage]);
             auto load = [&](uint8_t* dst, const CUtensorMap* m, int x, int y) {
               if constexpr (CG == 2) tma_load_2d_pair(dst, m, fb, x, y, pol);
               else tma_load_2d(dst, m, &full[stage], x, y, pol);
             };
-            if constexpr (kMode != kGrad) {
-              load(A, th, k * 64, pa * h_plane + m0);
-              load(B, &tm_w, k * 64, a.w_row0 + pb * a.w_plane + n0);
-            } else if (u.kind == 1) {   // dH: D (K = columns, contiguous), W (N contiguous)
-              load(A, &tm_dk, k * 64, pa * a.d_plane + m0);
 #pragma unroll
-              for (int j = 0; j < kBRows / 64; ++j)
-                load(B + j * 8192, &tm_w, n0 + j * 64, a.w_row0 + pb * a.w_plane + k * 64);
-            } else {                    // dW: D (M contiguous), H (N contiguous)
+            for (int p = 0; p < kAParts<P>; ++p) {
+              if constexpr (kMode != kGrad) {
+                load(A + p * kABytes, th, k * 64, p * h_plane + m0);
+              } else if (u.kind == 1) {   // dH: D (K = columns, contiguous)
+                load(A + p * kABytes, &tm_dk, k * 64, p * a.d_plane + m0);
+              } else {                    // dW: D (M contiguous)
 #pragma unroll
-              for (int j = 0; j < 2; ++j)
-                load(A + j * 8192, &tm_dm, m0 + j * 64, pa * a.d_plane + k * 64);
-#pragma unroll
-              for (int j = 0; j < kBRows / 64; ++j)
-                load(B + j * 8192, th, n0 + j * 64, pb * h_plane + k * 64);
+                for (int j = 0; j < 2; ++j)
+                  load(A + p * kABytes + j * 8192, &tm_dm, m0 + j * 64, p * a.d_plane + k * 64);
+              }
             }
+#pragma unroll
+            for (int p = 0; p < kBParts<P>; ++p) {
+              if constexpr (kMode != kGrad) {
+                load(B + p * kBPart, &tm_w, k * 64, a.w_row0 + p * a.w_plane + n0);
+              } else {                    // dH: W, dW: H (N contiguous)
+                const CUtensorMap* tb = u.kind == 1 ? &tm_w : th;
+                const int y = (u.kind == 1 ? a.w_row0 + p * a.w_plane : p * h_plane) + k * 64;
+#pragma unroll
+                for (int j = 0; j < kBRows / 64; ++j)
+                  load(B + p * kBPart + j * 8192, tb, n0 + j * 64, y);
+              }
             }
-            __syncwarp();
-            if (++stage == a.nstages) { stage = 0; phase ^= 1; }
           }
+          __syncwarp();
+          if (++stage == a.nstages) { stage = 0; phase ^= 1; }
         }
       }
       if constexpr (CG == 2) {
@@ -433,7 +449,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       Unit u;
       bool ok = true;
       for (int i = 0; ok && sch.get(a, i, u); ++i) {
-        const int total = u.nk * a.terms;
+        const int total = u.nk;
         // K-major: the next 16 K values lie 32 bytes on; MN-major: 16 rows of 128 bytes on,
         // with 8192 bytes between 64-element runs along M or N
         const int a_mn = u.kind == 2, b_mn = u.kind != 0;
@@ -442,7 +458,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t a_step = a_mn ? 2048 >> 4 : 32 >> 4, b_step = b_mn ? 2048 >> 4 : 32 >> 4;
         // (no chunks at all: nothing to sum, the epilogue writes zeros)
         for (int c0 = 0; ok && c0 < total;) {
-          const int c1 = kPromote<kMode, F32> ? min(total, c0 + kSegment) : total;
+          const int c1 = kPromote<kMode, P> ? min(total, c0 + kSegment<P>) : total;
           if (!warp_wait(&acc_empty[acc], acc_phase ^ 1, abort_flag, a.status)) { ok = false; break; }
           tc_fence_after();
           const uint32_t d = tbase + acc * BN;
@@ -451,18 +467,21 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc_fence_after();
             const uint32_t a_addr = smem_u32(smem + stage * kStage);
             const uint64_t ad = sdesc_sw128(a_addr, a_lbo, 1024);
-            const uint64_t bd = sdesc_sw128(a_addr + kABytes, b_lbo, 1024);
+            const uint64_t bd = sdesc_sw128(a_addr + kAParts<P> * kABytes, b_lbo, 1024);
             if (elect_one()) {
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk) {
-              const uint32_t accum = (c > c0 || kk > 0) ? 1u : 0u;
-              if constexpr (CG == 2)
-                umma_f16_pair(d, ad + kk * a_step, bd + kk * b_step, idesc, accum);
-              else
-                umma_f16(d, ad + kk * a_step, bd + kk * b_step, idesc, accum);
-            }
-            if constexpr (CG == 2) umma_commit_pair(&empty[stage]);
-            else umma_commit(&empty[stage]);
+              for (int t = 0; t < kProducts<P>; ++t) {
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk) {
+                  const uint32_t accum = (c > c0 || t > 0 || kk > 0) ? 1u : 0u;
+                  const uint64_t da = ad + (part_a<P>(t) * kABytes >> 4) + kk * a_step;
+                  const uint64_t db = bd + (part_b<P>(t) * kBPart >> 4) + kk * b_step;
+                  if constexpr (CG == 2) umma_f16_pair(d, da, db, idesc, accum);
+                  else umma_f16(d, da, db, idesc, accum);
+                }
+              }
+              if constexpr (CG == 2) umma_commit_pair(&empty[stage]);
+              else umma_commit(&empty[stage]);
             }
             __syncwarp();
             if (++stage == a.nstages) { stage = 0; phase ^= 1; }
@@ -521,14 +540,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (acc == 0) acc_phase ^= 1;
       };
       // Promoted sums: this thread's HC columns live in registers once the last segment is in.
-      constexpr bool kRegs = kPromote<kMode, F32>;
+      constexpr bool kRegs = kPromote<kMode, P>;
       constexpr int NB = HC / 32;
       float sum[kRegs ? HC : 1];
       if constexpr (kRegs) {
-        const int total = u.nk * a.terms;
 #pragma unroll
         for (int j = 0; j < HC; ++j) sum[j] = 0.f;
-        for (int c0 = 0; c0 < total; c0 += kSegment) {
+        for (int c0 = 0; c0 < u.nk; c0 += kSegment<P>) {
           acquire();
 #pragma unroll
           for (int c = 0; c < NB; ++c) {
@@ -595,7 +613,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       } else if constexpr (kMode == kDlog) {
         constexpr int PC = (!F32 && HC >= 64) ? 2 : 1;   // 32-column blocks per staged pass
         constexpr int RB = 64 * PC;
-        const int planes = F32 ? 3 : 1;
         auto rp = [&](int plane) {
           return [&, plane](int r) {
             return a.dlog + ((size_t)plane * a.d_plane + (row - lane + r)) * a.ld_dlog;
@@ -603,56 +620,33 @@ __global__ void __launch_bounds__(kThreads, 1)
         };
 #pragma unroll(kRegs ? NB : 1)
         for (int c = 0; c < NB; c += PC) {
+          const int col = ccol + c * 32;
+          // rows past the last one and columns past the vocabulary become zeros: the products
+          // that follow read them
+          const int lim = row < n ? a.vc - col : 0;
+          const int rel = tgt - c * 32;
+          float v[32 * PC];
 #pragma unroll
-          for (int s2 = 0; s2 < PC; ++s2) {
-            float v[32];
-            load(c + s2, v);
-            const int col = ccol + (c + s2) * 32;
-            // rows past the last one and columns past the vocabulary become zeros: the products
-            // that follow read them
-            const int lim = row < n ? a.vc - col : 0;
-            const int rel = tgt - (c + s2) * 32;
+          for (int s2 = 0; s2 < PC; ++s2) load(c + s2, v + 32 * s2);
 #pragma unroll
-            for (int j = 0; j < 32; ++j) {
-              float p = ex2((v[j] - lse) * kLog2e);
-              if (j == rel) p -= 1.f;
-              v[j] = j < lim ? p * g : 0.f;
-            }
-            if constexpr (!F32) {
-              if (a.d_parts == 2) {
-                // the rounding's remainder, as the second part
-                float w[32];
+          for (int j = 0; j < 32 * PC; ++j) {
+            float p = ex2((v[j] - lse) * kLog2e);
+            if (j == rel) p -= 1.f;
+            v[j] = j < lim ? p * g : 0.f;
+          }
+          // the parts one after the other, each the rounding of what the ones before leave
+          for (int pl = 0; pl < a.d_parts; ++pl) {
 #pragma unroll
-                for (int j = 0; j < 32; ++j) {
-                  const float hi = __bfloat162float(__float2bfloat16_rn(v[j]));
-                  w[j] = fabsf(hi) <= 3.3895314e38f ? v[j] - hi : 0.f;
-                }
-                stage_bf16<RB>(st, lane, 0, w);
-                flush_rows<__nv_bfloat16, RB, false>(st, lane, col, min(a.ld_dlog, col + 32), true,
-                                                     rp(1));
-                stage_bf16<RB>(st, lane, 0, v);
-                flush_rows<__nv_bfloat16, RB, false>(st, lane, col, min(a.ld_dlog, col + 32), true,
-                                                     rp(0));
-              } else {
-                stage_bf16<RB>(st, lane, s2 * 4, v);
-              }
-            } else {
-              for (int pl = 0; pl < planes; ++pl) {
-                float w[32];
+            for (int s2 = 0; s2 < PC; ++s2) stage_bf16<RB>(st, lane, s2 * 4, v + 32 * s2);
+            flush_rows<__nv_bfloat16, RB, false>(st, lane, col, a.ld_dlog, true, rp(pl));
+            if (pl + 1 < a.d_parts) {
 #pragma unroll
-                for (int j = 0; j < 32; ++j) {
-                  __nv_bfloat16 p0, p1, p2;
-                  split3(v[j], p0, p1, p2);
-                  w[j] = __bfloat162float(pl == 0 ? p0 : pl == 1 ? p1 : p2);
-                }
-                stage_bf16<RB>(st, lane, 0, w);
-                flush_rows<__nv_bfloat16, RB, false>(st, lane, col, a.ld_dlog, true, rp(pl));
+              for (int j = 0; j < 32 * PC; ++j) {
+                const float hi = __bfloat162float(__float2bfloat16_rn(v[j]));
+                v[j] = fabsf(hi) <= 3.3895314e38f ? v[j] - hi : 0.f;
               }
             }
           }
-          if constexpr (!F32)
-            if (a.d_parts == 1)
-              flush_rows<__nv_bfloat16, RB, false>(st, lane, ccol + c * 32, a.ld_dlog, true, rp(0));
         }
       } else if (u.kind == 1 && a.acc) {
         // fp32 sums of this piece and K range
@@ -1038,25 +1032,30 @@ constexpr int kCfgBN[4] = {64, 128, 256, 256};
 
 bool weight_in_place(int d, long long ld, bool f32) { return !f32 && d % 8 == 0 && ld % 8 == 0; }
 
-// SM clocks of one K chunk with `m` rows of A: its MMAs, or its bytes at 64 per clock.
-double chunk_clocks(int cfg, long long m) {
+// SM clocks of one K chunk with `m` rows of A and operands in `parts`: its MMAs, its bytes at 64
+// per clock, or the threads that issue it.
+double chunk_clocks(int cfg, long long m, int parts) {
   const int cg = kCfgCG[cfg], bn = kCfgBN[cfg];
-  return std::max(bn * 2.0, (kABytes * std::min<long long>(m, 128) / 128.0 + bn / cg * 128.0) / 64.0);
+  const int prod = parts == 3 ? 6 : parts, bp = parts == 3 ? 3 : 1;
+  const double mma = prod * std::max(bn * 2.0, 200.0);
+  const double bytes = (parts * kABytes * std::min<long long>(m, 128) / 128.0 + bp * bn / cg * 128.0) / 64.0;
+  return std::max(mma + 150.0, bytes);
 }
 
 // Time of the product: rounds of tiles times a K chunk's time.
-double tile_cost(int cfg, long long m, long long n, int sms) {
+double tile_cost(int cfg, long long m, long long n, int sms, int parts) {
   const int cg = kCfgCG[cfg], bn = kCfgBN[cfg];
   const long long tiles = ((m + 128 * cg - 1) / (128 * cg)) * ((n + bn - 1) / bn);
   const long long slots = sms / cg;
-  return (double)((tiles + slots - 1) / slots) * chunk_clocks(cfg, m);
+  return (double)((tiles + slots - 1) / slots) * chunk_clocks(cfg, m, parts);
 }
 
-int pick_cfg(long long m, long long n, int sms) {
+int pick_cfg(long long m, long long n, int sms, int parts) {
   int best = 0;
   double bc = 0;
   for (int c = 0; c < 4; ++c) {
-    const double t = tile_cost(c, m, n, sms);
+    if (c == 2 && parts != 1) continue;
+    const double t = tile_cost(c, m, n, sms, parts);
     if (c == 0 || t <= bc) { bc = t; best = c; }
   }
   return best;
@@ -1088,7 +1087,7 @@ Plan make_plan(int rows, int d, int vocab, long long ld_head, bool f32, bool gra
   // pieces of equal width
   p.piece = (int)up((vocab + p.n_pieces - 1) / p.n_pieces, 256);
   p.n_pieces = (vocab + p.piece - 1) / p.piece;
-  p.cfg = pick_cfg(rows, p.piece, sms);
+  p.cfg = pick_cfg(rows, std::min(p.piece, vocab), sms, p.parts);
   const int bn = kCfgBN[p.cfg];
   p.n_part = 2 * ((p.piece + bn - 1) / bn) * p.n_pieces;
   p.splits = 1;
@@ -1100,9 +1099,9 @@ Plan make_plan(int rows, int d, int vocab, long long ld_head, bool f32, bool gra
     for (int c : {0, 1, 3}) {
       const int mt = 128 * kCfgCG[c], bnc = kCfgBN[c], slots = sms / kCfgCG[c];
       const long long nt = (d + bnc - 1) / bnc;
-      const double ch = chunk_clocks(c, 128), epi = bnc * 8.0 / ch;   // a tile's fixed cost
+      const double ch = chunk_clocks(c, 128, p.d_parts), epi = bnc * 8.0 / ch;   // (a tile's fixed cost)
       const long long nh = (rows + mt - 1) / mt * nt, nw = (p.piece + mt - 1) / mt * nt;
-      const double uh = (double)kh * p.g_terms, uw = (double)kw * p.g_terms + epi;
+      const double uh = (double)kh, uw = (double)kw + epi;
       const double share = (nh * (uh + epi) + nw * uw) / slots;
       const int s = (int)std::min<double>(std::min<long long>(32, kh), std::max(1.0, uh / std::max(share, 8.0)));
       const double t = ch * std::max(std::max(share, uw), uh / s + epi);
@@ -1170,15 +1169,15 @@ int max_pairs(K kern, int smem) {
   return n;
 }
 
-template <int kMode, int CG, int BN, bool F32>
+template <int kMode, int CG, int BN, int P>
 cudaError_t launch_one(const Maps& m, HeadDev a, long long units, int sms, cudaStream_t st) {
-  constexpr int kStage = kABytes + BN / CG * 128;
+  constexpr int kStage = kAParts<P> * kABytes + kBParts<P> * (BN / CG * 128);
   const int budget = kSmemLimit - 1024 - kStagingBytes - 512;
   a.nstages = std::min(kMaxStages, budget / kStage);
   a.staging_off = a.nstages * kStage;
   a.bar_off = a.staging_off + kStagingBytes;
   const int smem = a.bar_off + 512 + 1024;
-  auto kern = head_gemm_kernel<kMode, CG, BN, F32>;
+  auto kern = head_gemm_kernel<kMode, CG, BN, P>;
   // per device: the shared-memory opt-in and the number of pairs that fit
   static int ready[64];
   int dev = 0;
@@ -1201,25 +1200,27 @@ cudaError_t launch_one(const Maps& m, HeadDev a, long long units, int sms, cudaS
                     m.hc, m.w, m.dk, m.dm, a);
 }
 
-template <int kMode, bool F32>
+template <int kMode, int P>
 cudaError_t launch_cfg(int cfg, const Maps& m, const HeadDev& a, long long units, int sms,
                        cudaStream_t st) {
   switch (cfg) {
-    case 0: return launch_one<kMode, 1, 64, F32>(m, a, units, sms, st);
-    case 1: return launch_one<kMode, 1, 128, F32>(m, a, units, sms, st);
+    case 0: return launch_one<kMode, 1, 64, P>(m, a, units, sms, st);
+    case 1: return launch_one<kMode, 1, 128, P>(m, a, units, sms, st);
     case 2:
-      if constexpr (kMode != kGrad) return launch_one<kMode, 1, 256, F32>(m, a, units, sms, st);
+      if constexpr (kMode != kGrad && P == 1) return launch_one<kMode, 1, 256, P>(m, a, units, sms, st);
       break;
-    case 3: return launch_one<kMode, 2, 256, F32>(m, a, units, sms, st);
+    case 3: return launch_one<kMode, 2, 256, P>(m, a, units, sms, st);
   }
   return cudaErrorInvalidValue;
 }
 
 template <int kMode>
-cudaError_t launch_mode(bool f32, int cfg, const Maps& m, const HeadDev& a, long long units,
+cudaError_t launch_mode(int parts, int cfg, const Maps& m, const HeadDev& a, long long units,
                         int sms, cudaStream_t st) {
-  return f32 ? launch_cfg<kMode, true>(cfg, m, a, units, sms, st)
-             : launch_cfg<kMode, false>(cfg, m, a, units, sms, st);
+  if (parts == 3) return launch_cfg<kMode, 3>(cfg, m, a, units, sms, st);
+  if constexpr (kMode == kGrad)
+    if (parts == 2) return launch_cfg<kMode, 2>(cfg, m, a, units, sms, st);
+  return launch_cfg<kMode, 1>(cfg, m, a, units, sms, st);
 }
 
 #define TRY(x)                        \
@@ -1387,7 +1388,7 @@ cudaError_t launch_head_loss(const HeadArgs& h, cudaStream_t st) {
     a.part0 = 2 * (p.piece / bn) * i;
     a.tlogit = c.at<float>(p.tlogit);
     const long long units = (long long)((h.rows + 128 * cg - 1) / (128 * cg)) * ((vc + bn - 1) / bn);
-    TRY(launch_mode<kLoss>(h.f32, p.cfg, m, a, units, c.sms, st));
+    TRY(launch_mode<kLoss>(p.parts, p.cfg, m, a, units, c.sms, st));
   }
   const int last = h.vocab - (p.n_pieces - 1) * p.piece;
   const int n_part = 2 * (p.piece / bn) * (p.n_pieces - 1) + 2 * ((last + bn - 1) / bn);
@@ -1421,7 +1422,7 @@ cudaError_t launch_head_grad(const HeadArgs& h, cudaStream_t st) {
     a.dlog = c.at<__nv_bfloat16>(p.dlog);
     a.ld_dlog = p.piece;
     const long long units = (long long)((h.rows + 128 * cg - 1) / (128 * cg)) * ((vc + bn - 1) / bn);
-    TRY(launch_mode<kDlog>(h.f32, p.cfg, m, a, units, c.sms, st));
+    TRY(launch_mode<kDlog>(p.parts, p.cfg, m, a, units, c.sms, st));
     // both products of D: 64-row boxes for the MN-major operands
     if (!c.hidden_maps(&m.h, &m.hc, 64) || !c.weight_map(&m.w, vc, 64) ||
         !encode_bf16(&m.dk, a.dlog, p.piece, (uint64_t)p.d_parts * p.r_pad, p.piece, 64, 128) ||
@@ -1440,7 +1441,7 @@ cudaError_t launch_head_grad(const HeadArgs& h, cudaStream_t st) {
     const long long nt = (h.d + gbn - 1) / gbn;
     const long long gu = (a.do_h ? nt * ((h.rows + 128 * gcg - 1) / (128 * gcg)) * p.splits : 0) +
                          (a.do_w ? nt * ((vc + 128 * gcg - 1) / (128 * gcg)) : 0);
-    TRY(launch_mode<kGrad>(h.f32, p.cfg_g, m, a, gu, c.sms, st));
+    TRY(launch_mode<kGrad>(p.d_parts, p.cfg_g, m, a, gu, c.sms, st));
   }
   if (sums && h.grad_hidden) {
     const long long n4 = (long long)h.rows * (p.d_pad / 4);
