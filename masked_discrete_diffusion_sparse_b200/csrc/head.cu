@@ -24,6 +24,7 @@
 #include "head.h"
 
 #include <algorithm>
+#include <type_traits>
 
 #include "tensormap.h"
 
@@ -70,6 +71,7 @@ struct HeadDev {
   const float* grad_nll;
   __nv_bfloat16* dlog;      // [parts][r_pad][ld_dlog]
   int ld_dlog;
+  int d_rows;               // rows of D that are read (one row tile: 16, 64 or 128)
   // gradients
   int do_h, do_w, splits;
   float* acc;               // [splits][r_pad][d_pad] or null: dH is written directly
@@ -118,6 +120,11 @@ template <int P> __host__ __device__ constexpr int part_b(int t) {
 template <int P> constexpr int kSegment = P == 3 ? 1 : 8;
 template <int kMode, int P>
 constexpr bool kPromote = P == 3 || kMode == kLoss;
+
+// 64-wide K chunks per pipeline stage.  Waiting for a stage and releasing it takes the issuing
+// warp about 300 clocks, as much as the MMAs of a narrow tile, so those take two at a time.
+template <int kMode, int CG, int BN, int P>
+constexpr int kChunks = kMode != kGrad && P == 1 && CG == 1 && BN <= 128 ? 2 : 1;
 
 // Rounding D to one bf16 part adds an error as large as the gradients' own rounding (together
 // 2.4e-3 of their norm against 1.7e-3).  Up to this many rows the products are bound by the
@@ -271,18 +278,21 @@ template <typename T, int RB, bool kLast, typename RowPtr>
 SMDM_DEV void flush_rows(uint8_t* st, int lane, int col, int cols, bool vec, RowPtr row_ptr) {
   constexpr int C = RB / 16, E = 16 / (int)sizeof(T), RPI = 32 / C;
   __syncwarp();
+  // all reads first: a read behind a store would wait for its turn each time (1600 -> XX clocks)
+  uint4 v[C];
+#pragma unroll
+  for (int it = 0; it < C; ++it)
+    v[it] = *reinterpret_cast<const uint4*>(stage_at<RB>(st, it * RPI + lane / C, lane % C));
+  const int c0 = col + lane % C * E;
 #pragma unroll
   for (int it = 0; it < C; ++it) {
-    const int row = it * RPI + lane / C, chunk = lane % C;
-    const int c0 = col + chunk * E;
-    T* dst = row_ptr(row);
+    T* dst = row_ptr(it * RPI + lane / C);
     if (dst && c0 < cols) {
-      const uint4 v = *reinterpret_cast<const uint4*>(stage_at<RB>(st, row, chunk));
       if (vec && c0 + E <= cols) {
-        if constexpr (kLast) __stcs(reinterpret_cast<uint4*>(dst + c0), v);
-        else *reinterpret_cast<uint4*>(dst + c0) = v;
+        if constexpr (kLast) __stcs(reinterpret_cast<uint4*>(dst + c0), v[it]);
+        else *reinterpret_cast<uint4*>(dst + c0) = v[it];
       } else {
-        const T* e = reinterpret_cast<const T*>(&v);
+        const T* e = reinterpret_cast<const T*>(&v[it]);
 #pragma unroll
         for (int k = 0; k < E; ++k)
           if (c0 + k < cols) dst[c0 + k] = e[k];
@@ -328,7 +338,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   constexpr int kBRows = BN / CG;                    // rows (columns of the product) of B here
   constexpr bool F32 = P == 3;
   constexpr int kBPart = kBRows * 128;
-  constexpr int kStage = kAParts<P> * kABytes + kBParts<P> * kBPart;
+  constexpr int KS = kChunks<kMode, CG, BN, P>;
+  constexpr int kStage = KS * (kAParts<P> * kABytes + kBParts<P> * kBPart);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + a.bar_off);
   uint64_t* full = bars;
   uint64_t* empty = bars + kMaxStages;
@@ -391,14 +402,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int i = 0; ok && sch.get(a, i, u); ++i) {
         const int m0 = u.m0 + (int)rank * 128;
         const int n0 = u.n0 + (int)rank * kBRows;
-        for (int k = u.k0; k < u.k0 + u.nk; ++k) {
+        for (int k = u.k0; k < u.k0 + u.nk; k += KS) {
           if (!warp_wait(&empty[stage], phase ^ 1, abort_flag, a.status)) { ok = false; break; }
           uint8_t* A = smem + stage * kStage;
-          uint8_t* B = A + kAParts<P> * kABytes;
+          uint8_t* B = A + KS * kAParts<P> * kABytes;
           if (elect_one()) {
             const int ab = u.kind == 0 ? a.a_box * 128 : kABytes;
             if (leader)
-              mbar_arrive_expect_tx(&full[stage], CG * (kAParts<P> * ab + kBParts<P> * kBPart));
+              mbar_arrive_expect_tx(&full[stage],
+                                    CG * KS * (kAParts<P> * ab + kBParts<P> * kBPart));
             const uint32_t fb = lead_addr(&full[stage]);
             auto load = [&](uint8_t* dst, const CUtensorMap* m, int x, int y) {
               if constexpr (CG == 2) tma_load_2d_pair(dst, m, fb, x, y, pol);
@@ -407,7 +419,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int p = 0; p < kAParts<P>; ++p) {
               if constexpr (kMode != kGrad) {
-                load(A + p * kABytes, th, k * 64, p * h_plane + m0);
+                // (a chunk past the row's end arrives as zeros)
+#pragma unroll
+                for (int s = 0; s < KS; ++s)
+                  load(A + (s * kAParts<P> + p) * kABytes, th, (k + s) * 64, p * h_plane + m0);
               } else if (u.kind == 1) {   // dH: D (K = columns, contiguous)
                 load(A + p * kABytes, &tm_dk, k * 64, p * a.d_plane + m0);
               } else {                    // dW: D (M contiguous)
@@ -419,7 +434,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int p = 0; p < kBParts<P>; ++p) {
               if constexpr (kMode != kGrad) {
-                load(B + p * kBPart, &tm_w, k * 64, a.w_row0 + p * a.w_plane + n0);
+#pragma unroll
+                for (int s = 0; s < KS; ++s)
+                  load(B + (s * kBParts<P> + p) * kBPart, &tm_w, (k + s) * 64,
+                       a.w_row0 + p * a.w_plane + n0);
               } else {                    // dH: W, dW: H (N contiguous)
                 const CUtensorMap* tb = u.kind == 1 ? &tm_w : th;
                 const int y = (u.kind == 1 ? a.w_row0 + p * a.w_plane : p * h_plane) + k * 64;
@@ -449,7 +467,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       Unit u;
       bool ok = true;
       for (int i = 0; ok && sch.get(a, i, u); ++i) {
-        const int total = u.nk;
+        const int total = (u.nk + KS - 1) / KS;      // stages
         // K-major: the next 16 K values lie 32 bytes on; MN-major: 16 rows of 128 bytes on,
         // with 8192 bytes between 64-element runs along M or N
         const int a_mn = u.kind == 2, b_mn = u.kind != 0;
@@ -458,7 +476,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t a_step = a_mn ? 2048 >> 4 : 32 >> 4, b_step = b_mn ? 2048 >> 4 : 32 >> 4;
         // (no chunks at all: nothing to sum, the epilogue writes zeros)
         for (int c0 = 0; ok && c0 < total;) {
-          const int c1 = kPromote<kMode, P> ? min(total, c0 + kSegment<P>) : total;
+          const int c1 = kPromote<kMode, P> ? min(total, c0 + kSegment<P> / KS) : total;
           if (!warp_wait(&acc_empty[acc], acc_phase ^ 1, abort_flag, a.status)) { ok = false; break; }
           tc_fence_after();
           const uint32_t d = tbase + acc * BN;
@@ -467,15 +485,18 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc_fence_after();
             const uint32_t a_addr = smem_u32(smem + stage * kStage);
             const uint64_t ad = sdesc_sw128(a_addr, a_lbo, 1024);
-            const uint64_t bd = sdesc_sw128(a_addr + kAParts<P> * kABytes, b_lbo, 1024);
+            const uint64_t bd = sdesc_sw128(a_addr + KS * kAParts<P> * kABytes, b_lbo, 1024);
             if (elect_one()) {
 #pragma unroll
-              for (int t = 0; t < kProducts<P>; ++t) {
+              for (int t = 0; t < kProducts<P> * KS; ++t) {
+                constexpr int NP = kProducts<P>;
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk) {
                   const uint32_t accum = (c > c0 || t > 0 || kk > 0) ? 1u : 0u;
-                  const uint64_t da = ad + (part_a<P>(t) * kABytes >> 4) + kk * a_step;
-                  const uint64_t db = bd + (part_b<P>(t) * kBPart >> 4) + kk * b_step;
+                  const int pa = t / NP * kAParts<P> + part_a<P>(t % NP);
+                  const int pb = t / NP * kBParts<P> + part_b<P>(t % NP);
+                  const uint64_t da = ad + (pa * kABytes >> 4) + kk * a_step;
+                  const uint64_t db = bd + (pb * kBPart >> 4) + kk * b_step;
                   if constexpr (CG == 2) umma_f16_pair(d, da, db, idesc, accum);
                   else umma_f16(d, da, db, idesc, accum);
                 }
@@ -546,7 +567,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if constexpr (kRegs) {
 #pragma unroll
         for (int j = 0; j < HC; ++j) sum[j] = 0.f;
-        for (int c0 = 0; c0 < u.nk; c0 += kSegment<P>) {
+        for (int c0 = 0; c0 < u.nk; c0 += kSegment<P>) {   // (chunks; a stage never splits)
           acquire();
 #pragma unroll
           for (int c = 0; c < NB; ++c) {
@@ -614,8 +635,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         constexpr int PC = (!F32 && HC >= 64) ? 2 : 1;   // 32-column blocks per staged pass
         constexpr int RB = 64 * PC;
         auto rp = [&](int plane) {
-          return [&, plane](int r) {
-            return a.dlog + ((size_t)plane * a.d_plane + (row - lane + r)) * a.ld_dlog;
+          return [&, plane](int r) -> __nv_bfloat16* {
+            const int rr = row - lane + r;
+            return rr < a.d_rows ? a.dlog + ((size_t)plane * a.d_plane + rr) * a.ld_dlog : nullptr;
           };
         };
 #pragma unroll(kRegs ? NB : 1)
@@ -628,11 +650,19 @@ __global__ void __launch_bounds__(kThreads, 1)
           float v[32 * PC];
 #pragma unroll
           for (int s2 = 0; s2 < PC; ++s2) load(c + s2, v + 32 * s2);
+          // (most blocks hold no target, no row past the last and no column past the vocabulary)
+          const bool plain = __all_sync(0xffffffffu, lim >= 32 * PC && (rel < 0 || rel >= 32 * PC));
+          if (plain && !F32) {
+            const float off = -lse * kLog2e;
 #pragma unroll
-          for (int j = 0; j < 32 * PC; ++j) {
-            float p = ex2((v[j] - lse) * kLog2e);
-            if (j == rel) p -= 1.f;
-            v[j] = j < lim ? p * g : 0.f;
+            for (int j = 0; j < 32 * PC; ++j) v[j] = ex2(fmaf(v[j], kLog2e, off)) * g;
+          } else {
+#pragma unroll
+            for (int j = 0; j < 32 * PC; ++j) {
+              float p = ex2((v[j] - lse) * kLog2e);
+              if (j == rel) p -= 1.f;
+              v[j] = j < lim ? p * g : 0.f;
+            }
           }
           // the parts one after the other, each the rounding of what the ones before leave
           for (int pl = 0; pl < a.d_parts; ++pl) {
@@ -641,9 +671,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             flush_rows<__nv_bfloat16, RB, false>(st, lane, col, a.ld_dlog, true, rp(pl));
             if (pl + 1 < a.d_parts) {
 #pragma unroll
-              for (int j = 0; j < 32 * PC; ++j) {
-                const float hi = __bfloat162float(__float2bfloat16_rn(v[j]));
-                v[j] = fabsf(hi) <= 3.3895314e38f ? v[j] - hi : 0.f;
+              for (int j = 0; j < 32 * PC; j += 2) {
+                const uint32_t hi = pack_bf16(v[j], v[j + 1]);
+                v[j] -= __uint_as_float(hi << 16);
+                v[j + 1] -= __uint_as_float(hi & 0xffff0000u);
               }
             }
           }
@@ -710,6 +741,269 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     if constexpr (CG == 2) tmem_dealloc_pair(tbase, 2 * BN);
     else tmem_dealloc(tbase, 2 * BN);
+  }
+}
+
+// ------------------------------------------------------------------------------------------
+// Gradients of one row tile (at most 128 rows that take part, bf16)
+// ------------------------------------------------------------------------------------------
+// With so few rows both products of D are bound by bytes: dH reads the weights, dW writes their
+// gradient.  A CTA keeps 128 columns of everything: its columns of the hidden rows stay in shared
+// memory, its columns of dH stay in tensor memory, and for 64 vocabulary rows at a time it loads
+// D once for both products and its columns of the weights, adds to dH, and drains dW.  That
+// moves half of the bytes of separate tiles from L2 to the SMs, and the reads of one vocabulary
+// block overlap the writes of the last.
+//
+//   dH [128 r][128 c]  += D [128 r][64 v] W [64 v][128 c]        (both parts of D)
+//   dW^T [128 c][64 v]  = H^T [128 c][r] D [r][64 v]
+//
+// dW comes out transposed (a lane per column), so that 64 vocabulary rows are enough for an
+// M = 128 product; the epilogue turns it around in shared memory.  What bounds the loop is shared
+// memory's 128 bytes per clock: an MMA of N columns reads 4 KB of A and 32 N bytes of B.  H^T
+// therefore goes to tensor memory once and is dW's A operand from there.
+constexpr int kNarrowD = 2 * 128 * 128;         // a stage: D, two parts of [128 r][64 v]
+constexpr int kNarrowW = 2 * 64 * 128;          // and W, two runs of 64 columns [64 v][64 c]
+constexpr int kNarrowStage = kNarrowD + kNarrowW;
+constexpr int kNarrowStages = 3;
+constexpr int kNarrowH = 2 * 128 * 128;         // H: two runs of 64 columns [128 r][64 c]
+
+__global__ void __launch_bounds__(kThreads, 1)
+    head_narrow_kernel(const __grid_constant__ CUtensorMap tm_h,    // box {64, 64}
+                       const __grid_constant__ CUtensorMap tm_hc,
+                       const __grid_constant__ CUtensorMap tm_w,    // box {64, 64}
+                       const __grid_constant__ CUtensorMap tm_dk,   // box {64, 128}
+                       const HeadDev a, int slots) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~uintptr_t(1023));
+  uint8_t* sh_h = smem + kNarrowStages * kNarrowStage;
+  uint8_t* sh_st = sh_h + kNarrowH;
+  uint64_t* full = reinterpret_cast<uint64_t*>(sh_st + kStagingBytes);
+  uint64_t* empty = full + kNarrowStages;
+  uint64_t* acc_full = empty + kNarrowStages;    // [2] dW
+  uint64_t* acc_empty = acc_full + 2;
+  uint64_t* h_full = acc_empty + 2;
+  uint64_t* dh_full = h_full + 1;
+  uint64_t* ht_full = dh_full + 1;               // H^T is in tensor memory
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(ht_full + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kNarrowStages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&acc_full[i], 1);
+      mbar_init(&acc_empty[i], kEpiWarps);
+    }
+    mbar_init(h_full, 1);
+    mbar_init(dh_full, 1);
+    mbar_init(ht_full, kEpiWarps);
+    *abort_flag = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(&tm_w);
+    tma_prefetch_desc(&tm_dk);
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_holder, 512);                // dH: 128 columns; dW: 2 x 64; H^T: 64
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tbase = *tmem_holder;
+  griddep_launch();
+  griddep_wait();
+
+  const int n = a.meta->n;
+  const bool dense = a.meta->dense != 0;
+  const int c0 = blockIdx.x * 128, slot = blockIdx.y;
+  const int blocks = n > 0 ? (a.vc + 63) >> 6 : 0;   // 64-row blocks of the vocabulary
+  const int mine = slot < blocks ? (blocks - 1 - slot) / slots + 1 : 0;
+
+  if (warp == 0) {
+    const uint64_t pol = policy_evict_normal();
+    if (mine > 0 && elect_one()) {
+      const CUtensorMap* th = dense ? &tm_h : &tm_hc;
+      mbar_arrive_expect_tx(h_full, kNarrowH);
+      for (int j = 0; j < 2; ++j)
+        for (int k = 0; k < 2; ++k)
+          tma_load_2d(sh_h + j * 16384 + k * 8192, th, h_full, c0 + j * 64, k * 64, pol);
+    }
+    __syncwarp();
+    int stage = 0;
+    uint32_t phase = 0;
+    for (int i = 0; i < mine; ++i) {
+      if (!warp_wait(&empty[stage], phase ^ 1, abort_flag, a.status)) break;
+      if (elect_one()) {
+        uint8_t* D = smem + stage * kNarrowStage;
+        uint8_t* W = D + kNarrowD;
+        const int v = (slot + i * slots) * 64;
+        mbar_arrive_expect_tx(&full[stage], 2 * a.d_rows * 128 + kNarrowW);
+        for (int p = 0; p < 2; ++p)
+          tma_load_2d(D + p * 16384, &tm_dk, &full[stage], v, p * a.d_plane, pol);
+        for (int j = 0; j < 2; ++j)
+          tma_load_2d(W + j * 8192, &tm_w, &full[stage], c0 + j * 64, a.w_row0 + v, pol);
+      }
+      __syncwarp();
+      if (++stage == kNarrowStages) { stage = 0; phase ^= 1; }
+    }
+  } else if (warp == 1) {
+    bool ok = mine > 0 && warp_wait(ht_full, 0, abort_flag, a.status);
+    const uint32_t id_w = idesc_bf16(128, 64, 0, 1), id_h = idesc_bf16(128, 128, 0, 1);
+    int stage = 0, acc = 0;
+    uint32_t phase = 0, acc_phase = 0;
+    for (int i = 0; ok && i < mine; ++i) {
+      if (!warp_wait(&full[stage], phase, abort_flag, a.status)) { ok = false; break; }
+      if (!warp_wait(&acc_empty[acc], acc_phase ^ 1, abort_flag, a.status)) { ok = false; break; }
+      tc_fence_after();
+      const uint32_t d_addr = smem_u32(smem + stage * kNarrowStage);
+      const uint64_t db = sdesc_sw128(d_addr, 16, 1024);     // D, both ways it is read
+      const uint64_t wd = sdesc_sw128(d_addr + kNarrowD, 8192, 1024);
+      if (elect_one()) {
+        // dW first: its epilogue can start while dH is added to
+        // (straight-line code: a runtime loop around each MMA costs its issue half again)
+        auto dw = [&](auto steps) {
+#pragma unroll
+          for (int p = 1; p >= 0; --p)
+#pragma unroll
+            for (int kk = 0; kk < decltype(steps)::value; ++kk)
+              umma_f16_ts(tbase + 128 + acc * 64, tbase + 256 + kk * 8,
+                          db + p * (16384 >> 4) + kk * (2048 >> 4), id_w,
+                          (p == 0 || kk > 0) ? 1u : 0u);
+        };
+        if (n > 64) dw(std::integral_constant<int, 8>());
+        else if (n > 16) dw(std::integral_constant<int, 4>());
+        else dw(std::integral_constant<int, 1>());
+        umma_commit(&acc_full[acc]);
+#pragma unroll
+        for (int p = 1; p >= 0; --p)
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            umma_f16(tbase, db + p * (16384 >> 4) + kk * (32 >> 4), wd + kk * (2048 >> 4), id_h,
+                     (i > 0 || p == 0 || kk > 0) ? 1u : 0u);
+        umma_commit(&empty[stage]);
+        if (i == mine - 1) umma_commit(dh_full);
+      }
+      __syncwarp();
+      if (++stage == kNarrowStages) { stage = 0; phase ^= 1; }
+      acc ^= 1;
+      if (acc == 0) acc_phase ^= 1;
+    }
+  } else {
+    const int q = warp & 3, half = (warp - 2) >> 2;
+    const uint32_t lanes = uint32_t(q * 32) << 16;
+    uint8_t* st = sh_st + (warp - 2) * 4096;
+    __nv_bfloat16* out_w = static_cast<__nv_bfloat16*>(a.out_w);
+    int acc = 0;
+    uint32_t acc_phase = 0;
+    if (mine > 0) {
+      // H^T: lane c, a 32-bit column for every two rows; this warp's 32 columns and 64 rows
+      mbar_wait(h_full, 0, abort_flag, a.status);
+      const int c = q * 32 + lane;
+      const uint8_t* src = sh_h + (c >> 6) * 16384 + (c & 7) * 2;
+      uint32_t w[32];
+#pragma unroll
+      for (int j = 0; j < 32; ++j) {
+        const int r = half * 64 + 2 * j;       // (rows of 128 bytes, 16-byte words swizzled)
+        const uint32_t lo = *reinterpret_cast<const uint16_t*>(
+            src + r * 128 + ((((c & 63) >> 3) ^ (r & 7)) << 4));
+        const uint32_t hi = *reinterpret_cast<const uint16_t*>(
+            src + (r + 1) * 128 + ((((c & 63) >> 3) ^ ((r + 1) & 7)) << 4));
+        w[j] = lo | (hi << 16);
+      }
+      tmem_st32(tbase + lanes + 256 + half * 32, w);
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(ht_full);
+    }
+    for (int i = 0; i < mine; ++i) {
+      mbar_wait(&acc_full[acc], acc_phase, abort_flag, a.status);
+      tc_fence_after();
+      float v[32];                               // column c0 + 32 q + lane, 32 vocabulary rows
+      tmem_ld32(tbase + lanes + 128 + acc * 64 + half * 32, v);
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&acc_empty[acc]);
+      acc ^= 1;
+      if (acc == 0) acc_phase ^= 1;
+      if (!a.do_w) continue;
+      __nv_bfloat16* t = reinterpret_cast<__nv_bfloat16*>(st);   // [32 v][32 c]
+#pragma unroll
+      for (int j = 0; j < 32; ++j) t[j * 32 + lane] = __float2bfloat16_rn(v[j]);
+      __syncwarp();
+      const int v0 = (slot + i * slots) * 64 + half * 32, c = c0 + q * 32 + (lane & 3) * 8;
+      uint4 w[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        w[k] = *reinterpret_cast<const uint4*>(t + (k * 8 + (lane >> 2)) * 32 + (lane & 3) * 8);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int r = v0 + k * 8 + (lane >> 2);
+        if (r >= a.vc || c >= a.d) continue;
+        __nv_bfloat16* dst = out_w + (size_t)r * a.d + c;
+        if (a.vec_ok && c + 8 <= a.d) {
+          __stcs(reinterpret_cast<uint4*>(dst), w[k]);
+        } else {
+          const __nv_bfloat16* e = reinterpret_cast<const __nv_bfloat16*>(&w[k]);
+          for (int x = 0; x < 8; ++x)
+            if (c + x < a.d) dst[x] = e[x];
+        }
+      }
+      __syncwarp();
+    }
+    if (a.do_w && n == 0) {
+      // no row takes part: zeros
+      for (int v = slot * 8 + (warp - 2); v < a.vc; v += slots * 8)
+        for (int c = c0 + lane; c < min(a.d, c0 + 128); c += 32)
+          out_w[(size_t)v * a.d + c] = __nv_bfloat16(0.f);
+    }
+    if (a.do_h) {
+      // this slot's sums of dH (zeros when it had no block)
+      if (mine > 0) {
+        mbar_wait(dh_full, 0, abort_flag, a.status);
+        tc_fence_after();
+      }
+      const int row = q * 32 + lane;
+      float* base = a.acc + (size_t)slot * a.r_pad * a.d_pad;
+#pragma unroll 1
+      for (int b = 0; b < 2; ++b) {
+        const int col = c0 + half * 64 + b * 32;
+        float v[32];
+        if (mine > 0) {
+          tmem_ld32(tbase + lanes + half * 64 + b * 32, v);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 32; ++j) v[j] = 0.f;
+        }
+        stage_f32(st, lane, v);
+        if (a.acc_add) {
+          __syncwarp();
+#pragma unroll
+          for (int it = 0; it < 8; ++it) {
+            const int r = it * 4 + (lane >> 3), ch = lane & 7;
+            if (row - lane + r < n && col + ch * 4 < a.d_pad) {
+              float4* s4 = reinterpret_cast<float4*>(stage_at<128>(st, r, ch));
+              const float4 o = *reinterpret_cast<const float4*>(
+                  base + (size_t)(row - lane + r) * a.d_pad + col + ch * 4);
+              float4 w = *s4;
+              w.x += o.x; w.y += o.y; w.z += o.z; w.w += o.w;
+              *s4 = w;
+            }
+          }
+        }
+        flush_rows<float, 128, false>(st, lane, col, a.d_pad, true, [&](int r) -> float* {
+          return row - lane + r < n ? base + (size_t)(row - lane + r) * a.d_pad : nullptr;
+        });
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tbase, 512);
   }
 }
 
@@ -898,9 +1192,9 @@ __global__ void __launch_bounds__(256) head_rows_kernel(RowsArgs a, WeightArgs w
       }
     }
   }
-  // the rows up to the next multiple of 64 are summed over by dW: zeros
+  // the rows up to the next multiple of 64 (128 with one row tile) are summed over by dW: zeros
   if ((int)blockIdx.x == a.row_ctas - 1 && !dense) {
-    const int end = min(a.r_pad, (n + 63) & ~63);
+    const int end = a.rows <= 128 ? 128 : (n + 63) & ~63;
     const size_t plane = (size_t)a.r_pad * a.d_pad;
     for (int r = n + warp; r < end; r += 8)
       for (int p = 0; p < (a.f32 ? 3 : 1); ++p)
@@ -985,6 +1279,7 @@ __global__ void __launch_bounds__(256)
     if (c >= d) continue;
     const float* p = acc + (size_t)r * d_pad + c;
     float4 s = *reinterpret_cast<const float4*>(p);
+#pragma unroll 8
     for (int k = 1; k < splits; ++k) {
       const float4 t = *reinterpret_cast<const float4*>(p + k * plane);
       s.x += t.x; s.y += t.y; s.z += t.z; s.w += t.w;
@@ -997,6 +1292,38 @@ __global__ void __launch_bounds__(256)
         if constexpr (F32) static_cast<float*>(out)[o + k] = v[k];
         else static_cast<__nv_bfloat16*>(out)[o + k] = __float2bfloat16_rn(v[k]);
       }
+  }
+}
+
+// The same for many K ranges and few rows: a CTA per row and 128 columns, eight warps over the
+// ranges (each in order), then the warps' sums in order.
+__global__ void __launch_bounds__(256)
+    head_sum_deep_kernel(const HeadMeta* meta, const int* row_idx, const float* acc, int splits,
+                         int r_pad, int d, int d_pad, __nv_bfloat16* out) {
+  griddep_launch();
+  griddep_wait();
+  __shared__ __align__(16) float sh[8][128];
+  const int r = blockIdx.y;
+  if (r >= meta->n) return;
+  const int lane = threadIdx.x & 31, g = threadIdx.x >> 5;
+  const int c = blockIdx.x * 128 + lane * 4;
+  const size_t plane = (size_t)r_pad * d_pad;
+  float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (c < d_pad) {
+    const float* p = acc + (size_t)r * d_pad + c;
+#pragma unroll 4
+    for (int k = g; k < splits; k += 8) {
+      const float4 t = *reinterpret_cast<const float4*>(p + k * plane);
+      s.x += t.x; s.y += t.y; s.z += t.z; s.w += t.w;
+    }
+  }
+  *reinterpret_cast<float4*>(&sh[g][lane * 4]) = s;
+  __syncthreads();
+  const int cc = blockIdx.x * 128 + threadIdx.x;
+  if (threadIdx.x < 128 && cc < d) {
+    float t = 0.f;
+    for (int i = 0; i < 8; ++i) t += sh[i][threadIdx.x];
+    out[(size_t)row_idx[r] * d + cc] = __float2bfloat16_rn(t);
   }
 }
 
@@ -1024,6 +1351,7 @@ struct Plan {
   size_t meta, row_idx, hid, part, tlogit, wst, dlog, acc, total;
   int cfg, cfg_g;     // tile configuration of the logits' product and of the gradients'
   int splits, n_part;
+  int narrow;         // > 0: head_narrow_kernel, with this many vocabulary slots (= splits)
 };
 
 // Tile configurations: {CTAs per tile, columns}.
@@ -1069,7 +1397,7 @@ Plan make_plan(int rows, int d, int vocab, long long ld_head, bool f32, bool gra
   p.r_pad = (int)up(rows, 256);
   p.d_pad = (int)up(d, 64);
   p.staged = !weight_in_place(d, ld_head, f32);
-  p.few = head_few_fits(rows, d) && (grad || p.staged);
+  p.few = head_few_fits(rows, d) && p.staged;
   if (p.few) {
     p.total = head_few_bytes(rows, d, vocab, sms);
     return p;
@@ -1107,6 +1435,13 @@ Plan make_plan(int rows, int d, int vocab, long long ld_head, bool f32, bool gra
       const double t = ch * std::max(std::max(share, uw), uh / s + epi);
       if (c == 0 || t <= best) { best = t; p.cfg_g = c; p.splits = s; }
     }
+    // one row tile: a column group per CTA, as many vocabulary slots as fill the SMs
+    if (!f32 && rows <= 128) {
+      const int groups = (d + 127) / 128;
+      p.narrow = (int)std::min<long long>(std::max(1, sms / groups), kh);
+      p.splits = p.narrow;
+      p.cfg = 0;
+    }
   }
   size_t off = 0;
   auto take = [&](size_t b) {
@@ -1124,7 +1459,7 @@ Plan make_plan(int rows, int d, int vocab, long long ld_head, bool f32, bool gra
   if (p.staged) p.wst = take((size_t)p.parts * p.piece * p.d_pad * 2);
   if (grad) {
     p.dlog = take((size_t)p.d_parts * p.r_pad * p.piece * 2);
-    if (p.splits > 1 || p.n_pieces > 1) p.acc = take((size_t)p.splits * p.r_pad * p.d_pad * 4);
+    if (p.narrow || p.splits > 1 || p.n_pieces > 1) p.acc = take((size_t)p.splits * p.r_pad * p.d_pad * 4);
   }
   p.total = off;
   return p;
@@ -1171,7 +1506,8 @@ int max_pairs(K kern, int smem) {
 
 template <int kMode, int CG, int BN, int P>
 cudaError_t launch_one(const Maps& m, HeadDev a, long long units, int sms, cudaStream_t st) {
-  constexpr int kStage = kAParts<P> * kABytes + kBParts<P> * (BN / CG * 128);
+  constexpr int kStage = kChunks<kMode, CG, BN, P> *
+                         (kAParts<P> * kABytes + kBParts<P> * (BN / CG * 128));
   const int budget = kSmemLimit - 1024 - kStagingBytes - 512;
   a.nstages = std::min(kMaxStages, budget / kStage);
   a.staging_off = a.nstages * kStage;
@@ -1221,6 +1557,23 @@ cudaError_t launch_mode(int parts, int cfg, const Maps& m, const HeadDev& a, lon
   if constexpr (kMode == kGrad)
     if (parts == 2) return launch_cfg<kMode, 2>(cfg, m, a, units, sms, st);
   return launch_cfg<kMode, 1>(cfg, m, a, units, sms, st);
+}
+
+cudaError_t launch_narrow(const Maps& m, const HeadDev& a, int slots, cudaStream_t st) {
+  constexpr int smem = kNarrowStages * kNarrowStage + kNarrowH + kStagingBytes + 512 + 1024;
+  static_assert(smem <= kSmemLimit, "narrow kernel's shared memory");
+  static bool ready[64];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  if (!ready[dev]) {
+    e = cudaFuncSetAttribute(head_narrow_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    ready[dev] = true;
+  }
+  return launch_pdl(head_narrow_kernel, dim3((a.d + 127) / 128, slots), dim3(kThreads),
+                    (size_t)smem, st, 1, m.h, m.hc, m.w, m.dk, a, slots);
 }
 
 #define TRY(x)                        \
@@ -1339,6 +1692,8 @@ struct Call {
     a.status = h.status;
     return a;
   }
+  // Rows of D that head_narrow_kernel reads for rows that take part: its steps over them.
+  int narrow_rows() const { return h.rows <= 16 ? 16 : h.rows <= 64 ? 64 : 128; }
   // rows of A that one box brings: no more than there are (a multiple of 8)
   int a_box() const { return (int)std::min<size_t>(128, up(h.rows, 8)); }
 };
@@ -1365,7 +1720,7 @@ int head_loss_launches(const HeadArgs& a) {
 int head_grad_launches(const HeadArgs& a) {
   const Plan p = make_plan(a.rows, a.d, a.vocab, a.ld_head, a.f32, true);
   if (p.few) return a.grad_hidden ? 3 : 2;
-  const bool sums = p.splits > 1 || p.n_pieces > 1;
+  const bool sums = p.narrow || p.splits > 1 || p.n_pieces > 1;
   return 1 + 2 * p.n_pieces + (p.staged ? p.n_pieces - 1 : 0) + (sums && a.grad_hidden ? 1 : 0);
 }
 
@@ -1406,7 +1761,7 @@ cudaError_t launch_head_grad(const HeadArgs& h, cudaStream_t st) {
   const int cg = kCfgCG[p.cfg], bn = kCfgBN[p.cfg];
   const int gcg = kCfgCG[p.cfg_g], gbn = kCfgBN[p.cfg_g];
   const size_t es = h.f32 ? 4 : 2;
-  const bool sums = p.splits > 1 || p.n_pieces > 1;
+  const bool sums = p.narrow || p.splits > 1 || p.n_pieces > 1;
   for (int i = 0; i < p.n_pieces; ++i) {
     const int v0 = i * p.piece, vc = std::min(p.piece, h.vocab - v0);
     TRY(c.weights(v0, vc, st));
@@ -1417,6 +1772,7 @@ cudaError_t launch_head_grad(const HeadArgs& h, cudaStream_t st) {
       return cudaErrorInvalidValue;
     m.dk = m.dm = m.hc;
     a.d_parts = p.d_parts;
+    a.d_rows = p.narrow ? c.narrow_rows() : p.r_pad;
     a.lse = h.lse;
     a.grad_nll = h.grad_nll;
     a.dlog = c.at<__nv_bfloat16>(p.dlog);
@@ -1425,7 +1781,8 @@ cudaError_t launch_head_grad(const HeadArgs& h, cudaStream_t st) {
     TRY(launch_mode<kDlog>(p.parts, p.cfg, m, a, units, c.sms, st));
     // both products of D: 64-row boxes for the MN-major operands
     if (!c.hidden_maps(&m.h, &m.hc, 64) || !c.weight_map(&m.w, vc, 64) ||
-        !encode_bf16(&m.dk, a.dlog, p.piece, (uint64_t)p.d_parts * p.r_pad, p.piece, 64, 128) ||
+        !encode_bf16(&m.dk, a.dlog, p.piece, (uint64_t)p.d_parts * p.r_pad, p.piece, 64,
+                     p.narrow ? a.d_rows : 128) ||
         !encode_bf16(&m.dm, a.dlog, p.piece, (uint64_t)p.d_parts * p.r_pad, p.piece, 64, 64))
       return cudaErrorInvalidValue;
     a.terms = p.g_terms;
@@ -1438,12 +1795,21 @@ cudaError_t launch_head_grad(const HeadArgs& h, cudaStream_t st) {
     a.out_w = h.grad_head ? static_cast<uint8_t*>(h.grad_head) + (size_t)v0 * h.d * es : nullptr;
     a.vec_ok = (size_t)h.d * es % 16 == 0 && (!h.grad_hidden || aligned16(h.grad_hidden)) &&
                (!h.grad_head || aligned16(h.grad_head));
+    if (p.narrow) {
+      TRY(launch_narrow(m, a, p.narrow, st));
+      continue;
+    }
     const long long nt = (h.d + gbn - 1) / gbn;
     const long long gu = (a.do_h ? nt * ((h.rows + 128 * gcg - 1) / (128 * gcg)) * p.splits : 0) +
                          (a.do_w ? nt * ((vc + 128 * gcg - 1) / (128 * gcg)) : 0);
     TRY(launch_mode<kGrad>(p.d_parts, p.cfg_g, m, a, gu, c.sms, st));
   }
   if (sums && h.grad_hidden) {
+    if (p.narrow)
+      return launch_pdl(head_sum_deep_kernel, dim3((h.d + 127) / 128, h.rows), dim3(256), 0, st, 1,
+                        c.at<HeadMeta>(p.meta), c.at<int>(p.row_idx), c.at<float>(p.acc),
+                        p.splits, p.r_pad, h.d, p.d_pad,
+                        static_cast<__nv_bfloat16*>(h.grad_hidden));
     const long long n4 = (long long)h.rows * (p.d_pad / 4);
     const int grid = (int)std::min<long long>((n4 + 255) / 256, (long long)c.sms * 16);
     auto k = h.f32 ? head_sum_kernel<true> : head_sum_kernel<false>;
