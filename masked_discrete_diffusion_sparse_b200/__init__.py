@@ -8,6 +8,7 @@ anywhere, but creating a model raises if the library is not built or no GPU is p
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import Optional, Sequence
 
@@ -432,13 +433,20 @@ def smdm_forward_stepcausal_noalloc(cfg: smdm_config, weights: dict, ids, pos, t
 _DTYPES = {torch.float32: SMDM_F32, torch.bfloat16: SMDM_BF16}
 
 
-def _dtype(t) -> int:
-    dt = t.dtype if isinstance(t, torch.Tensor) else t
-    if dt in (SMDM_F32, SMDM_BF16) and not isinstance(dt, torch.dtype):
-        return dt
-    if dt not in _DTYPES:
-        raise ValueError(f"expected float32 or bfloat16, got {dt}")
-    return _DTYPES[dt]
+def _dtype(dt) -> int:
+    """SMDM_* constant of a torch dtype (or of itself)."""
+    c = _DTYPES.get(dt)
+    if c is None:
+        if not isinstance(dt, int) or dt not in (SMDM_F32, SMDM_BF16):
+            raise ValueError(f"expected float32 or bfloat16, got {dt}")
+        c = dt
+    return c
+
+
+# Shape arguments of recent calls: building one takes as long as the call that it is passed to.
+_head_struct, _norm_struct, _embed_struct = (
+    functools.lru_cache(maxsize=256)(lambda *a, t=t: ctypes.byref(t(*a)))
+    for t in (smdm_head_shape, smdm_rmsnorm_shape, smdm_embed_shape))
 
 
 def _typed(t: torch.Tensor, dt: torch.dtype, name: str):
@@ -493,7 +501,7 @@ def _call(fn: str, stream, tensors, *args):
     for t in tensors:
         if t is not None and t.get_device() != dev:
             raise ValueError("all tensors must be on one device")
-    f = getattr(lib(), fn)
+    f = getattr(_lib or lib(), fn)
     if stream is None and dev == torch.cuda.current_device():
         r = f(*args, torch._C._cuda_getCurrentRawStream(dev))
     else:
@@ -532,28 +540,28 @@ def _head_shape(hidden, lm_head, target):
     if lm_head.shape[1] != d:
         raise ValueError("hidden and lm_head must share their width")
     _shape(target, (n,), "target")
-    s = smdm_head_shape(n, d, lm_head.shape[0], _dtype(hidden), ld_h, ld_w)
-    return s, h, w
+    v = lm_head.shape[0]
+    return _head_struct(n, d, v, _dtype(hidden.dtype), ld_h, ld_w), h, w, n, d, v
 
 
 def smdm_head_loss_workspace_bytes(rows: int, d_model: int, vocab: int, dtype,
                                    grad: bool = False) -> int:
     """dtype: torch.float32, torch.bfloat16 or the SMDM_* constant."""
-    s = smdm_head_shape(rows, d_model, vocab, _dtype(dtype), d_model, d_model)
-    return _bytes(lib().smdm_head_loss_workspace_bytes(ctypes.byref(s), 1 if grad else 0))
+    s = _head_struct(rows, d_model, vocab, _dtype(dtype), d_model, d_model)
+    return _bytes(lib().smdm_head_loss_workspace_bytes(s, 1 if grad else 0))
 
 
 def smdm_head_loss(hidden, lm_head, target, nll, lse, workspace, status=None, stream=None):
     """Cross entropy of the LM head without its logits: hidden [R][d] and lm_head [V][d] (float32
     or bfloat16, rows may lie apart), target int32 [R] (negative: the row takes no part) ->
     nll, lse (fp32 [R])."""
-    s, h, w = _head_shape(hidden, lm_head, target)
+    s, h, w, n, _, _ = _head_shape(hidden, lm_head, target)
     for name, t in (("nll", nll), ("lse", lse)):
-        _shape(t, (s.rows,), name)
+        _shape(t, (n,), name)
         _typed(t, torch.float32, name)
     ws, nb = _ws(workspace)
-    _call("smdm_head_loss", stream, (hidden, lm_head, target, nll, lse, workspace, status),
-          ctypes.byref(s), h, w, _adr(_i32(target), "target"), _adr(nll, "nll"), _adr(lse, "lse"), ws, nb,
+    _call("smdm_head_loss", stream, (hidden, lm_head, target, nll, lse, workspace, status), s, h,
+          w, _adr(_i32(target), "target"), _adr(nll, "nll"), _adr(lse, "lse"), ws, nb,
           _status(status))
 
 
@@ -561,20 +569,21 @@ def smdm_head_loss_grad(hidden, lm_head, target, lse, grad_nll, grad_hidden, gra
                         workspace, status=None, stream=None):
     """Gradient of smdm_head_loss: lse from it and grad_nll (fp32 [R], the rows' weights) ->
     grad_hidden [R][d] and grad_lm_head [V][d] in hidden's dtype (either may be None)."""
-    s, h, w = _head_shape(hidden, lm_head, target)
+    s, h, w, n, d, v = _head_shape(hidden, lm_head, target)
     for name, t in (("lse", lse), ("grad_nll", grad_nll)):
-        _shape(t, (s.rows,), name)
+        _shape(t, (n,), name)
         _typed(t, torch.float32, name)
-    for name, t, shape in (("grad_hidden", grad_hidden, (s.rows, s.d_model)),
-                           ("grad_lm_head", grad_lm_head, (s.vocab, s.d_model))):
+    for name, t, shape in (("grad_hidden", grad_hidden, (n, d)),
+                           ("grad_lm_head", grad_lm_head, (v, d))):
         if t is not None:
             _shape(t, shape, name)
             _typed(t, hidden.dtype, name)
     ws, nb = _ws(workspace)
     _call("smdm_head_loss_grad", stream,
           (hidden, lm_head, target, lse, grad_nll, grad_hidden, grad_lm_head, workspace, status),
-          ctypes.byref(s), h, w, _adr(_i32(target), "target"), _adr(lse, "lse"), _adr(grad_nll, "grad_nll"),
-          _adr(grad_hidden, "grad_hidden"), _adr(grad_lm_head, "grad_lm_head"), ws, nb, _status(status))
+          s, h, w, _adr(_i32(target), "target"), _adr(lse, "lse"), _adr(grad_nll, "grad_nll"),
+          _adr(grad_hidden, "grad_hidden"), _adr(grad_lm_head, "grad_lm_head"), ws, nb,
+          _status(status))
 
 
 def smdm_rmsnorm(x, gain, y, rstd=None, eps: float = 1e-6, stream=None):
@@ -588,14 +597,15 @@ def smdm_rmsnorm(x, gain, y, rstd=None, eps: float = 1e-6, stream=None):
     if rstd is not None:
         _shape(rstd, (x.shape[0],), "rstd")
         _typed(rstd, torch.float32, "rstd")
-    s = smdm_rmsnorm_shape(x.shape[0], x.shape[1], _dtype(x), _dtype(y), ld_x, ld_y, eps)
-    _call("smdm_rmsnorm", stream, (x, gain, y, rstd), ctypes.byref(s), px, _adr(gain, "gain"), py,
+    n, d = x.shape
+    s = _norm_struct(n, d, _dtype(x.dtype), _dtype(y.dtype), ld_x, ld_y, eps)
+    _call("smdm_rmsnorm", stream, (x, gain, y, rstd), s, px, _adr(gain, "gain"), py,
           _adr(rstd, "rstd"))
 
 
 def smdm_rmsnorm_grad_workspace_bytes(rows: int, d_model: int) -> int:
-    s = smdm_rmsnorm_shape(rows, d_model, SMDM_F32, SMDM_F32, d_model, d_model, 0.0)
-    return _bytes(lib().smdm_rmsnorm_grad_workspace_bytes(ctypes.byref(s)))
+    s = _norm_struct(rows, d_model, SMDM_F32, SMDM_F32, d_model, d_model, 0.0)
+    return _bytes(lib().smdm_rmsnorm_grad_workspace_bytes(s))
 
 
 def smdm_rmsnorm_grad(x, gain, rstd, grad_y, grad_x, grad_gain, workspace, grad_add=None,
@@ -613,10 +623,10 @@ def smdm_rmsnorm_grad(x, gain, rstd, grad_y, grad_x, grad_gain, workspace, grad_
         if t is not None:
             _shape(t, shape, name)
             _typed(t, want, name)
-    s = smdm_rmsnorm_shape(n, d, _dtype(x), _dtype(grad_y), ld_x, ld_y, 0.0)
+    s = _norm_struct(n, d, _dtype(x.dtype), _dtype(grad_y.dtype), ld_x, ld_y, 0.0)
     ws, nb = _ws(workspace)
     _call("smdm_rmsnorm_grad", stream,
-          (x, gain, rstd, grad_y, grad_x, grad_gain, workspace, grad_add), ctypes.byref(s), px,
+          (x, gain, rstd, grad_y, grad_x, grad_gain, workspace, grad_add), s, px,
           _adr(gain, "gain"), _adr(rstd, "rstd"), pg, _adr(grad_add, "grad_add"), _adr(grad_x, "grad_x"), _adr(grad_gain, "grad_gain"), ws, nb)
 
 
@@ -625,15 +635,15 @@ def smdm_embed(ids, table, out, scale: float = 1.0, status=None, stream=None):
     pt, ld = _rows(table, "table")
     _shape(ids, (out.shape[0],), "ids")
     _shape(out, (out.shape[0], table.shape[1]), "out")
-    s = smdm_embed_shape(ids.numel(), table.shape[1], table.shape[0], _dtype(table), _dtype(out),
-                         ld, scale)
-    _call("smdm_embed", stream, (ids, table, out, status), ctypes.byref(s), _adr(_i32(ids), "ids"), pt,
+    n_emb, d = table.shape
+    s = _embed_struct(ids.numel(), d, n_emb, _dtype(table.dtype), _dtype(out.dtype), ld, scale)
+    _call("smdm_embed", stream, (ids, table, out, status), s, _adr(_i32(ids), "ids"), pt,
           _adr(out, "out"), _status(status))
 
 
 def smdm_embed_grad_workspace_bytes(rows: int, d_model: int, n_emb: int) -> int:
-    s = smdm_embed_shape(rows, d_model, n_emb, SMDM_F32, SMDM_F32, d_model, 1.0)
-    return _bytes(lib().smdm_embed_grad_workspace_bytes(ctypes.byref(s)))
+    s = _embed_struct(rows, d_model, n_emb, SMDM_F32, SMDM_F32, d_model, 1.0)
+    return _bytes(lib().smdm_embed_grad_workspace_bytes(s))
 
 
 def smdm_embed_grad(ids, grad_out, grad_table, workspace, scale: float = 1.0, status=None,
@@ -642,11 +652,11 @@ def smdm_embed_grad(ids, grad_out, grad_table, workspace, scale: float = 1.0, st
     pg, ld = _rows(grad_out, "grad_out")
     _shape(ids, (grad_out.shape[0],), "ids")
     _shape(grad_table, (grad_table.shape[0], grad_out.shape[1]), "grad_table")
-    s = smdm_embed_shape(ids.numel(), grad_out.shape[1], grad_table.shape[0], _dtype(grad_table),
-                         _dtype(grad_out), ld, scale)
+    s = _embed_struct(ids.numel(), grad_out.shape[1], grad_table.shape[0],
+                      _dtype(grad_table.dtype), _dtype(grad_out.dtype), ld, scale)
     ws, nb = _ws(workspace)
-    _call("smdm_embed_grad", stream, (ids, grad_out, grad_table, workspace, status),
-          ctypes.byref(s), _adr(_i32(ids), "ids"), pg, _adr(grad_table, "grad_table"), ws, nb, _status(status))
+    _call("smdm_embed_grad", stream, (ids, grad_out, grad_table, workspace, status), s,
+          _adr(_i32(ids), "ids"), pg, _adr(grad_table, "grad_table"), ws, nb, _status(status))
 
 
 def make_config(n_layers, d_model, n_heads, d_head, d_ffn, vocab, n_reg=64, dtype=SMDM_BF16,

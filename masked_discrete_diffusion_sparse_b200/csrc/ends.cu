@@ -234,12 +234,20 @@ __global__ void __launch_bounds__(kNormThreads) train_rms_grad_kernel(RmsArgs a)
       }
     }
   }
+  // (a single CTA's share is the gradient)
   float* ws = a.ws + (size_t)blockIdx.x * a.d;
+  T* gg = static_cast<T*>(a.grad_gain);
   if constexpr (RPC == 1) {
 #pragma unroll
     for (int u = 0; u < NU; ++u) {
       const int i = tid + u * TPR;
-      if (i < units) store_v<VEC>(ws + (size_t)i * VEC, acc + u * VEC);
+      if (i >= units) continue;
+      if (gridDim.x == 1) {
+#pragma unroll
+        for (int k = 0; k < VEC; ++k) gg[i * VEC + k] = from_f<T>(acc[u * VEC + k]);
+      } else {
+        store_v<VEC>(ws + (size_t)i * VEC, acc + u * VEC);
+      }
     }
   } else {
     // the warps' shares side by side in shared memory, added in order
@@ -254,7 +262,8 @@ __global__ void __launch_bounds__(kNormThreads) train_rms_grad_kernel(RmsArgs a)
       float t = 0.f;
 #pragma unroll
       for (int w = 0; w < RPC; ++w) t += sh[(size_t)w * a.d + i];
-      ws[i] = t;
+      if (gridDim.x == 1) gg[i] = from_f<T>(t);
+      else ws[i] = t;
     }
   }
 }
@@ -365,7 +374,9 @@ __global__ void __launch_bounds__(TH, 512 / TH) train_rms_grad_ring_kernel(RmsAr
 #pragma unroll
   for (int u = 0; u < NU; ++u) {
     const int i = tid + u * TH;
-    if (i < units) store4(ws + (size_t)i * 4, acc + u * 4);
+    if (i >= units) continue;
+    if (gridDim.x == 1) store4(static_cast<T*>(a.grad_gain) + (size_t)i * 4, acc + u * 4);
+    else store4(ws + (size_t)i * 4, acc + u * 4);
   }
 }
 
@@ -435,7 +446,7 @@ __global__ void __launch_bounds__(256) embed_kernel(EmbedArgs a) {
 
 // Sorting (id, row) pairs as 64-bit words: all different, so any sorting method is a stable one
 // and the sums below always add a token's rows in the same order.
-constexpr int kChunk = 2048, kWays = 8;
+constexpr int kChunk = 2048;
 
 // Each of the first `chunks` CTAs sorts one chunk of `size` words (a power of two, up to kChunk): a
 // bitonic network, two words per thread.  Exchanges over distances below 64 stay within a warp
@@ -525,18 +536,19 @@ __global__ void __launch_bounds__(1024) embed_sort_kernel(const int* ids, int n,
   if (base + 2 * t + 1 < n) out[base + 2 * t + 1] = wide(y);
 }
 
-// Merge groups of kWays sorted runs of `run` words: a word's place is its place in its own run
+// Merge groups of `ways` (a power of two, at most 32) sorted runs of `run` words: a word's place is its place in its own run
 // plus the number of smaller words in each of the others, found by one lane per run.
 __global__ void __launch_bounds__(256) embed_merge_kernel(const unsigned long long* in, int n,
-                                                          int run, unsigned long long* out) {
+                                                          int run, int ways,
+                                                          unsigned long long* out) {
   griddep_launch();
   griddep_wait();
   const long long t = (long long)blockIdx.x * 256 + threadIdx.x;
-  const int way = (int)(t % kWays);
-  const long long i = t / kWays;
+  const int way = (int)(t & (ways - 1));
+  const long long i = t / ways;
   const bool in_range = i < n;
   const unsigned long long x = in_range ? in[i] : 0;
-  const long long group = i / ((long long)run * kWays) * run * kWays;
+  const long long group = i / ((long long)run * ways) * run * ways;
   const long long lo0 = group + (long long)way * run;
   int rank = 0;
   if (in_range && lo0 < n) {
@@ -553,8 +565,7 @@ __global__ void __launch_bounds__(256) embed_merge_kernel(const unsigned long lo
       rank = lo;
     }
   }
-#pragma unroll
-  for (int o = kWays / 2; o > 0; o >>= 1) rank += __shfl_xor_sync(0xffffffffu, rank, o);
+  for (int o = ways / 2; o > 0; o >>= 1) rank += __shfl_xor_sync(0xffffffffu, rank, o);
   if (in_range && way == 0) out[group + rank] = x;
 }
 
@@ -655,14 +666,15 @@ __global__ void __launch_bounds__(256) embed_sum_kernel(EmbedGradArgs a) {
 }
 
 // Add up the parts of every run that starts in one piece and goes on in the next: eight groups
-// of warps take every eighth part in order, then the groups are added in order.  Every CTA finds
-// all such runs itself (pieces of 256 threads at a time) and takes every gridDim-th (run,
-// column block); a CTA per piece would mostly start CTAs that have nothing to do.
-template <typename T, int VEC>
+// of warps take every eighth part in order, then the groups are added in order.  The CTAs with one
+// blockIdx.x look at the same 256 pieces, find the runs that start there and share their (run,
+// column block) pairs; a CTA per piece would mostly start CTAs that have nothing to do.
+// VECT: a lane's four columns lie together, else 32 apart.
+template <typename T, bool VECT>
 __global__ void __launch_bounds__(256) embed_join_kernel(EmbedGradArgs a) {
   griddep_launch();
   griddep_wait();
-  constexpr int kCols = 32 * VEC;
+  constexpr int VEC = 4, kCols = 32 * VEC;
   __shared__ int s_run[256];
   __shared__ int s_warp[8];
   __shared__ float sh[8][kCols];
@@ -670,69 +682,69 @@ __global__ void __launch_bounds__(256) embed_join_kernel(EmbedGradArgs a) {
   const int lane = threadIdx.x & 31, grp = threadIdx.x >> 5;
   const int blocks = (d + kCols - 1) / kCols;
   T* table = static_cast<T*>(a.e.grad_table);
-  long long job0 = 0;                      // jobs of the earlier batches of pieces
-  for (int p0 = 0; p0 + 1 < a.pieces; p0 += 256) {
-    const int p = p0 + threadIdx.x;
-    bool starts = false;
-    if (p + 1 < a.pieces) {
-      const int i0 = p * a.per, i1 = i0 + a.per;
-      const int key = key_of(a.list[i1 - 1]);
-      starts = key < a.e.n_emb && key_of(a.list[i1]) == key &&
-               !(i0 > 0 && key_of(a.list[i0 - 1]) == key);
-    }
-    const unsigned m = __ballot_sync(0xffffffffu, starts);
-    __syncthreads();                       // the previous batch's list has been read
-    if (lane == 0) s_warp[grp] = __popc(m);
-    __syncthreads();
-    int at = 0, runs = 0;
-    for (int w = 0; w < 8; ++w) {
-      if (w < grp) at += s_warp[w];
-      runs += s_warp[w];
-    }
-    if (starts) s_run[at + __popc(m & ((1u << lane) - 1u))] = p;
-    __syncthreads();
-    const long long jobs = (long long)runs * blocks;
-    // this CTA's jobs of the batch
-    long long j = ((long long)blockIdx.x - job0 % gridDim.x + gridDim.x) % gridDim.x;
-    for (; j < jobs; j += gridDim.x) {
-      const int first = s_run[j / blocks];
-      const int c = (int)(j % blocks) * kCols + lane * VEC;
-      const int key = key_of(a.list[(size_t)(first + 1) * a.per]);
-      // part 0: slot 1 of the first piece; part k: slot 0 of the k-th piece after it, as long as
-      // that piece begins with this token (its list entry is read along with the part)
-      float s[VEC];
+  const int p = blockIdx.x * 256 + threadIdx.x;
+  bool starts = false;
+  if (p + 1 < a.pieces) {
+    const int i0 = p * a.per, i1 = i0 + a.per;
+    const int key = key_of(a.list[i1 - 1]);
+    starts = key < a.e.n_emb && key_of(a.list[i1]) == key &&
+             !(i0 > 0 && key_of(a.list[i0 - 1]) == key);
+  }
+  const unsigned m = __ballot_sync(0xffffffffu, starts);
+  if (lane == 0) s_warp[grp] = __popc(m);
+  __syncthreads();
+  int at = 0, runs = 0;
+  for (int w = 0; w < 8; ++w) {
+    if (w < grp) at += s_warp[w];
+    runs += s_warp[w];
+  }
+  if (starts) s_run[at + __popc(m & ((1u << lane) - 1u))] = p;
+  __syncthreads();
+  const long long jobs = (long long)runs * blocks;
+  for (long long j = blockIdx.y; j < jobs; j += gridDim.y) {
+    const int first = s_run[j / blocks];
+    const int c0 = (int)(j % blocks) * kCols;
+    auto col = [&](int e) { return VECT ? lane * VEC + e : e * 32 + lane; };
+    const int key = key_of(a.list[(size_t)(first + 1) * a.per]);
+    // part 0: slot 1 of the first piece; part k: slot 0 of the k-th piece after it, as long as
+    // that piece begins with this token (its list entry is read along with the part)
+    float s[VEC];
 #pragma unroll
-      for (int k = 0; k < VEC; ++k) s[k] = 0.f;
-      bool more = true;
-      for (int k0 = grp; more && first + k0 < a.pieces; k0 += 8 * 4) {
-        float v[4][VEC];
-        bool in[4];
+    for (int k = 0; k < VEC; ++k) s[k] = 0.f;
+    bool more = true;
+    for (int k0 = grp; more && first + k0 < a.pieces; k0 += 8 * 4) {
+      float v[4][VEC];
+      bool in[4];
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const int k = k0 + 8 * u, q = min(first + k, a.pieces - 1);
-          in[u] = first + k < a.pieces && (k == 0 || key_of(a.list[(size_t)q * a.per]) == key);
-          load_v<VEC>(a.part + ((size_t)q * 2 + (k == 0 ? 1 : 0)) * d + min(c, d - VEC), v[u]);
-        }
+      for (int u = 0; u < 4; ++u) {
+        const int k = k0 + 8 * u, q = min(first + k, a.pieces - 1);
+        in[u] = first + k < a.pieces && (k == 0 || key_of(a.list[(size_t)q * a.per]) == key);
+        const float* p = a.part + ((size_t)q * 2 + (k == 0 ? 1 : 0)) * d;
+        if constexpr (VECT) {
+          load4(p + min(c0 + col(0), d - VEC), v[u]);
+        } else {
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          more = more && in[u];
-          if (more)
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) s[e] += v[u][e];
+          for (int e = 0; e < VEC; ++e) v[u][e] = p[min(c0 + col(e), d - 1)];
         }
       }
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) sh[grp][lane * VEC + e] = s[e];
-      __syncthreads();
-      if (threadIdx.x < kCols) {
-        const int cc = (int)(j % blocks) * kCols + threadIdx.x;
-        float t = 0.f;
-        for (int g = 0; g < 8; ++g) t += sh[g][threadIdx.x];
-        if (cc < d) table[(size_t)key * d + cc] = from_f<T>(t * a.e.scale);
+      for (int u = 0; u < 4; ++u) {
+        more = more && in[u];
+        if (more)
+#pragma unroll
+          for (int e = 0; e < VEC; ++e) s[e] += v[u][e];
       }
-      __syncthreads();
     }
-    job0 += jobs;
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) sh[grp][col(e)] = s[e];
+    __syncthreads();
+    if (threadIdx.x < kCols) {
+      const int cc = c0 + threadIdx.x;
+      float t = 0.f;
+      for (int g = 0; g < 8; ++g) t += sh[g][threadIdx.x];
+      if (cc < d) table[(size_t)key * d + cc] = from_f<T>(t * a.e.scale);
+    }
+    __syncthreads();
   }
 }
 
@@ -764,6 +776,7 @@ int norm_tpr(int d) { return d <= 1024 ? 32 : 256; }
 
 int norm_grad_ctas(int rows, int d) {
   const int tpr = norm_tpr(d), rpc = std::max(1, 256 / tpr);
+  if (tpr > 32 && rows <= 4) return 1;
   return std::min((rows + rpc - 1) / rpc, device_sms() * (tpr == 32 ? 4 : 2));
 }
 
@@ -789,7 +802,8 @@ cudaError_t rms_ring(const RmsArgs& a, int* ctas, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     ready[dev] = true;
   }
-  *ctas = std::min(a.rows, device_sms() * (512 / TH));
+  // (four rows one after the other cost less than a second launch)
+  *ctas = a.rows <= 4 ? 1 : std::min(a.rows, device_sms() * (512 / TH));
   return launch_pdl(kern, dim3(*ctas), dim3(TH), (size_t)q.stages * q.stage_bytes, st, 1, a, q);
 }
 
@@ -817,7 +831,8 @@ cudaError_t rms_types(const RmsArgs& a, int* grad, cudaStream_t st) {
   if (v4) {
     const bool ring = grad && tpr > 32 && a.d * sizeof(X) % 16 == 0 && a.d * sizeof(T) % 16 == 0 &&
                       a.ld_x * sizeof(X) % 16 == 0 && a.ld_y * sizeof(T) % 16 == 0 &&
-                      aligned(a.x, 16) && aligned(a.grad_y, 16) && aligned(a.add, 16);
+                      aligned(a.x, 16) && aligned(a.grad_y, 16) && aligned(a.add, 16) &&
+                      aligned(a.grad_gain, 4 * sizeof(T));
     if (ring)
       return a.d <= 4096 ? rms_ring<X, T, 256>(a, grad, st) : rms_ring<X, T, 512>(a, grad, st);
     if (tpr == 32) {
@@ -848,8 +863,8 @@ EmbedPlan embed_plan(int rows, int d) {
   p.chunks = (rows + kChunk - 1) / kChunk;
   p.slabs = (d + 255) / 256;
   // entries of one warp: enough warps to fill the device, few enough parts
-  const long long warps = (long long)device_sms() * 32;
-  p.per = 8;
+  const long long warps = (long long)device_sms() * 16;
+  p.per = rows <= 32 ? 32 : 8;       // (one piece needs no joining)
   while (p.per < 128 && (long long)rows * p.slabs / (2 * p.per) >= warps) p.per *= 2;
   p.pieces = (rows + p.per - 1) / p.per;
   size_t off = 0;
@@ -882,9 +897,10 @@ cudaError_t embed_grad_types(const EmbedGradArgs& g, cudaStream_t st) {
   const cudaError_t e = v ? launch_pdl(embed_sum_kernel<T, O, true>, grid, dim3(256), 0, st, 1, g)
                           : launch_pdl(embed_sum_kernel<T, O, false>, grid, dim3(256), 0, st, 1, g);
   if (e != cudaSuccess || g.pieces < 2) return e;
-  const dim3 jgrid(device_sms() * 8);
-  return a.d % 4 == 0 ? launch_pdl(embed_join_kernel<T, 4>, jgrid, dim3(256), 0, st, 1, g)
-                      : launch_pdl(embed_join_kernel<T, 1>, jgrid, dim3(256), 0, st, 1, g);
+  const int batches = (g.pieces - 1 + 255) / 256;
+  const dim3 jgrid(batches, std::max(1, std::min(65535, device_sms() * 8 / batches)));
+  return a.d % 4 == 0 ? launch_pdl(embed_join_kernel<T, true>, jgrid, dim3(256), 0, st, 1, g)
+                      : launch_pdl(embed_join_kernel<T, false>, jgrid, dim3(256), 0, st, 1, g);
 }
 
 }  // namespace
@@ -898,7 +914,7 @@ size_t rmsnorm_grad_bytes(int rows, int d) {
 cudaError_t launch_train_rmsnorm_grad(const RmsArgs& a, cudaStream_t st) {
   int parts = 0;
   const cudaError_t e = rms_any(a, &parts, st);
-  if (e != cudaSuccess) return e;
+  if (e != cudaSuccess || parts == 1) return e;
   const dim3 grid((a.d + 31) / 32);
   return a.f32 ? launch_pdl(rms_gain_kernel<float>, grid, dim3(1024), 0, st, 1,
                             (const float*)a.ws, parts, a.d, static_cast<float*>(a.grad_gain))
@@ -938,10 +954,12 @@ cudaError_t launch_embed_grad(const EmbedArgs& a, cudaStream_t st) {
                              bytes, a.status);
   if (e != cudaSuccess) return e;
   int cur = 0;
-  for (long long run = kChunk; run < a.rows; run *= kWays, cur ^= 1) {
-    const long long searches = (long long)a.rows * kWays;
+  // as few runs per level as one level takes, up to 32 (every search reads the list from L2)
+  const int ways = p.chunks <= 8 ? 8 : p.chunks <= 16 ? 16 : 32;
+  for (long long run = kChunk; run < a.rows; run *= ways, cur ^= 1) {
+    const long long searches = (long long)a.rows * ways;
     e = launch_pdl(embed_merge_kernel, dim3((unsigned)((searches + 255) / 256)), dim3(256), 0, st, 1,
-                   (const unsigned long long*)list[cur], a.rows, (int)run, list[cur ^ 1]);
+                   (const unsigned long long*)list[cur], a.rows, (int)run, ways, list[cur ^ 1]);
     if (e != cudaSuccess) return e;
   }
   EmbedGradArgs g{};
