@@ -1013,7 +1013,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 struct RowsArgs {
   int rows, d, d_pad, vocab, r_pad, per;   // per: rows of one CTA
   int row_ctas;
-  bool f32, in_place, vec;
+  bool f32, in_place, vec, pad_rows;
   long long ld;
   const void* hidden;
   const int* target;
@@ -1192,11 +1192,12 @@ __global__ void __launch_bounds__(256) head_rows_kernel(RowsArgs a, WeightArgs w
       }
     }
   }
-  // the rows up to the next multiple of 64 (128 with one row tile) are summed over by dW: zeros
-  if ((int)blockIdx.x == a.row_ctas - 1 && !dense) {
+  // the rows up to the next multiple of 64 (128 with one row tile) are summed over by dW: zeros,
+  // every CTA its share
+  if (a.pad_rows && !dense) {
     const int end = a.rows <= 128 ? 128 : (n + 63) & ~63;
     const size_t plane = (size_t)a.r_pad * a.d_pad;
-    for (int r = n + warp; r < end; r += 8)
+    for (int r = n + blockIdx.x * 8 + warp; r < end; r += a.row_ctas * 8)
       for (int p = 0; p < (a.f32 ? 3 : 1); ++p)
         for (int c = lane * 8; c < a.d_pad; c += 256)
           *reinterpret_cast<uint4*>(a.out + p * plane + (size_t)r * a.d_pad + c) =
@@ -1431,7 +1432,7 @@ Plan make_plan(int rows, int d, int vocab, long long ld_head, bool f32, bool gra
       const long long nh = (rows + mt - 1) / mt * nt, nw = (p.piece + mt - 1) / mt * nt;
       const double uh = (double)kh, uw = (double)kw + epi;
       const double share = (nh * (uh + epi) + nw * uw) / slots;
-      const int s = (int)std::min<double>(std::min<long long>(32, kh), std::max(1.0, uh / std::max(share, 8.0)));
+      const int s = (int)std::min<double>(std::min<long long>(32, kh), std::max(1.0, uh / std::max(share, 2.0)));
       const double t = ch * std::max(std::max(share, uw), uh / s + epi);
       if (c == 0 || t <= best) { best = t; p.cfg_g = c; p.splits = s; }
     }
@@ -1606,10 +1607,11 @@ struct Call {
     r.d_pad = p.d_pad;
     r.vocab = h.vocab;
     r.r_pad = p.r_pad;
-    r.per = std::max(8, (h.rows + 1023) / 1024);
+    r.per = std::max(8, (h.rows + 1023) / 1024);   // (a row per warp)
     r.row_ctas = (h.rows + r.per - 1) / r.per;
     r.f32 = h.f32;
     r.in_place = in_place;
+    r.pad_rows = !loss;
     r.vec = whole_words(h.hidden, h.ld_hidden);
     r.ld = h.ld_hidden;
     r.hidden = h.hidden;

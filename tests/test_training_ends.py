@@ -76,10 +76,10 @@ def workspace(nbytes):
 # LM-head loss
 # ------------------------------------------------------------------------------------------------
 class Head:
-    def __init__(self, rows, d, vocab, dt, ignored=0.0, pad=0, offset=0, seed=0, std=0.02):
+    def __init__(self, rows, d, vocab, dt, ignored=0.0, pad=0, offset=0, seed=0, std=0.02, wpad=0):
         g = gen(seed)
         self.dt, self.rows, self.d, self.vocab = dt, rows, d, vocab
-        self.w = rand(g, vocab, d, std=std).to(dt)
+        self.w = rows_apart(rand(g, vocab, d, std=std).to(dt), wpad, dt)
         self.target = torch.randint(0, vocab, (rows,), generator=g, device="cuda").int()
         h = rand(g, rows, d) + 0.4 * torch.rand((rows, 1), generator=g, device="cuda") / std * \
             self.w[self.target.long()].float()
@@ -192,6 +192,14 @@ HEAD_CASES = [
 def test_head_loss_and_gradient(case):
     rows, d, vocab, dt, ignored, pad, offset = case
     x = Head(rows, d, vocab, dt, ignored, pad, offset, seed=rows + d)
+    _, lse = x.check_loss()
+    x.check_grad(lse)
+
+
+@pytest.mark.parametrize("dt,rows,wpad", [(BF16, 150, 8), (BF16, 150, 3), (BF16, 20, 24), (F32, 150, 1),
+                                          (F32, 9, 5), (BF16, 9, 1), (F32, 9, 4)])
+def test_head_weight_rows_apart(dt, rows, wpad):
+    x = Head(rows, 96, 800, dt, 0.2, seed=13, wpad=wpad)
     _, lse = x.check_loss()
     x.check_grad(lse)
 
@@ -564,6 +572,37 @@ def test_chain_captured_and_replayed_with_a_shared_workspace():
     graphs[0].replay()
     torch.cuda.synchronize()
     assert (a.nll == 0).all() and (a.gw == 0).all()
+
+
+FIRST_CALL_CAPTURED = """
+import sys
+sys.path[:0] = [{root!r}, {tests!r}]
+import torch
+from test_training_ends import BF16, Chain
+a = Chain(BF16, seed=25)
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    a.step()
+for t in a.outputs():
+    t.fill_(float("nan"))
+g.replay()
+torch.cuda.synchronize()
+got = [t.clone() for t in a.outputs()]
+a.step()
+torch.cuda.synchronize()
+assert all(torch.equal(x, y) for x, y in zip(got, a.outputs()))
+print("captured")
+"""
+
+
+def test_first_call_of_a_process_may_be_captured():
+    import os
+    import subprocess
+    import sys
+    here = os.path.dirname(os.path.abspath(__file__))
+    code = FIRST_CALL_CAPTURED.format(root=os.path.dirname(here), tests=here)
+    out = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
+    assert out.returncode == 0 and "captured" in out.stdout, out.stderr[-2000:]
 
 
 # ------------------------------------------------------------------------------------------------
