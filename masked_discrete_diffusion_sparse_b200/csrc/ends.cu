@@ -578,89 +578,122 @@ struct EmbedGradArgs {
 
 SMDM_DEV int key_of(unsigned long long w) { return (int)(w >> 32); }
 
-// Sum the rows of every token.  One warp takes `per` sorted entries and 256 columns; a run of
-// one token that lies within the piece is written at once, rounded from its fp32 sum; one that
-// goes on in the next piece leaves its part in slot 1 of the piece where it starts and in slot 0
-// of every later one (embed_join_kernel adds them up in order).
+// First entry of list[from, to) whose id is not `key` (to if there is none); a warp's search.
+SMDM_DEV int run_end(const unsigned long long* list, int from, int to, int key, int lane) {
+  for (int i = from; i < to; i += 32) {
+    const unsigned m = __ballot_sync(0xffffffffu, i + lane < to && key_of(list[i + lane]) != key);
+    if (m) return i + __ffs(m) - 1;
+  }
+  return to;
+}
+
+// Sum the rows of every token.  One warp takes a piece of `per` sorted entries and 256 columns.  A
+// run of one token that starts in a piece and ends within the next one is summed by the warp
+// where it starts and written at once, rounded from its fp32 sum.  A longer one ([MASK]) leaves
+// its part in slot 1 of the piece where it starts and in slot 0 of every later one
+// (embed_join_kernel adds them up in order).
+// Eight rows are in flight per warp.  (Four, loaded while the four before are added: 32 -> 41 us
+// for 12544 rows of 4096 bf16; the wait for memory then covers half as many bytes.)
 template <typename T, typename O, bool VECT>
 __global__ void __launch_bounds__(256) embed_sum_kernel(EmbedGradArgs a) {
   griddep_launch();
   griddep_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int n = a.e.rows, d = a.e.d;
+  const int n = a.e.rows, d = a.e.d, none = a.e.n_emb;   // (id n_emb: takes no part)
   T* table = static_cast<T*>(a.e.grad_table);
   const int job = blockIdx.x * 8 + warp;
   const int piece = job / a.slabs, slab = job % a.slabs;
   if (piece >= a.pieces) return;
-  const int i0 = piece * a.per, i1 = min(n, i0 + a.per);
   // this lane's columns: 8 in a row (bf16 rows), 4 and 4 that lie 128 apart (fp32), or 8 that
   // lie 32 apart (rows off their 16-byte boundaries)
   constexpr int N = !VECT ? 1 : sizeof(O) == 2 ? 8 : 4;
   auto col = [&](int j) { return slab * 256 + (j / N) * 32 * N + lane * N + j % N; };
+  const O* g = static_cast<const O*>(a.e.grad_out);
+
+  // the entries to take: the piece, without a run that the piece before takes whole, and with
+  // the rest of its own last run when that ends within the next piece
+  const int i0 = piece * a.per, i1 = min(n, i0 + a.per);
+  const int first_key = key_of(a.list[i0]), last_key = key_of(a.list[i1 - 1]);
+  const int prev_key = i0 > 0 ? key_of(a.list[i0 - 1]) : -1;
+  int begin = i0, end = i1;
+  if (first_key == prev_key && last_key != prev_key &&
+      (i0 == a.per || key_of(a.list[i0 - a.per - 1]) != prev_key))
+    begin = run_end(a.list, i0, i1, prev_key, lane);
+  const bool starts_here = !(first_key == last_key && prev_key == last_key);
+  if (i1 < n && starts_here && last_key < none && key_of(a.list[i1]) == last_key) {
+    const int next = min(n, i1 + a.per);
+    if (key_of(a.list[next - 1]) != last_key) end = run_end(a.list, i1, next, last_key, lane);
+  }
+  const int after = end < n ? key_of(a.list[end]) : -1;    // the id behind the entries
+
   float acc[8];
 #pragma unroll
   for (int j = 0; j < 8; ++j) acc[j] = 0.f;
-  const O* g = static_cast<const O*>(a.e.grad_out);
-  const int prev_key = i0 > 0 ? key_of(a.list[i0 - 1]) : -1;
-  const int next_key = i1 < n ? key_of(a.list[i1]) : -1;
-  int run_first = 1;       // the current run is the piece's first
+  int base = begin;        // entries base .. base + 63 are in cur and nxt, one per lane
+  int cur_key, cur_row, nxt_key, nxt_row;
+  auto fetch = [&](int at, int& key, int& row) {
+    const unsigned long long w = at + lane < end ? a.list[at + lane] : 0;
+    key = at + lane < end ? key_of(w) : none;
+    row = (int)(unsigned)w;                       // (row 0 where there is no entry)
+  };
+  fetch(base, cur_key, cur_row);
+  fetch(base + 32, nxt_key, nxt_row);
   constexpr int kAhead = 8;
-  for (int b = i0; b < i1; b += 32) {
-    const unsigned long long mine = b + lane < i1 ? a.list[b + lane] : ~0ull;
-    const int my_key = key_of(mine), my_row = b + lane < i1 ? (int)(unsigned)mine : 0;
-    const int cnt = min(32, i1 - b);
-    // the key behind each entry of the batch
-    int my_next = __shfl_down_sync(0xffffffffu, my_key, 1);
-    if (lane == cnt - 1) my_next = b + 32 < i1 ? key_of(a.list[b + 32]) : next_key;
-    for (int h = 0; h < cnt; h += kAhead) {
-      Raw<O, N> v[kAhead][8 / N];
+  Raw<O, N> v[kAhead][8 / N];
+  bool first_run = true;
+  for (int e = begin; e < end; e += kAhead) {
+    // (rows that take no part are read and left out)
 #pragma unroll
-      for (int k = 0; k < kAhead; ++k) {
-        // (rows that take no part are read and left out; past the piece's end, row 0 is)
-        const int row = __shfl_sync(0xffffffffu, my_row, h + k);
-        const O* r = g + (size_t)row * a.e.ld_grad;
+    for (int k = 0; k < kAhead; ++k) {
+      const O* r = g + (size_t)__shfl_sync(0xffffffffu, cur_row, e - base + k) * a.e.ld_grad;
 #pragma unroll
-        for (int j = 0; j < 8; j += N) v[k][j / N].load(r + min(col(j), d - N));
+      for (int j = 0; j < 8; j += N) v[k][j / N].load(r + min(col(j), d - N));
+    }
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      const int at = e - base + k;
+      const int key = __shfl_sync(0xffffffffu, cur_key, at & 31);
+      const int follow = __shfl_sync(0xffffffffu, at == 31 ? nxt_key : cur_key, (at + 1) & 31);
+      if (e + k >= end || key >= none) continue;             // uniform over the warp
+#pragma unroll
+      for (int j = 0; j < 8; j += N) {
+        float w[N];
+        v[k][j / N].get(w);
+#pragma unroll
+        for (int x = 0; x < N; ++x) acc[j + x] += w[x];
       }
+      const bool last = e + k + 1 >= end;
+      if (!last && follow == key) continue;                  // the run goes on
+      const bool from_before = first_run && key == prev_key;
+      const bool goes_on = last && after == key;
+      if (from_before || goes_on) {
+        float* p = a.part + ((size_t)piece * 2 + (from_before ? 0 : 1)) * d;
 #pragma unroll
-      for (int k = 0; k < kAhead; ++k) {
-        const int key = __shfl_sync(0xffffffffu, my_key, h + k);
-        const int following = __shfl_sync(0xffffffffu, my_next, h + k);
-        if (h + k >= cnt || key >= a.e.n_emb) continue;      // uniform over the warp
+        for (int j = 0; j < 8; j += N)
+          if (col(j) < d) {
+            if constexpr (VECT) store_n<N>(p + col(j), acc + j);
+            else p[col(j)] = acc[j];
+          }
+      } else {
+        T* o = table + (size_t)key * d;
 #pragma unroll
-        for (int j = 0; j < 8; j += N) {
-          float w[N];
-          v[k][j / N].get(w);
+        for (int j = 0; j < 8; ++j) acc[j] *= a.e.scale;
 #pragma unroll
-          for (int e = 0; e < N; ++e) acc[j + e] += w[e];
-        }
-        const bool piece_end = b + h + k + 1 >= i1;
-        if (following == key && !piece_end) continue;        // the run goes on
-        const bool from_before = run_first && key == prev_key;
-        const bool goes_on = piece_end && following == key;
-        if (from_before || goes_on) {
-          float* p = a.part + ((size_t)piece * 2 + (from_before ? 0 : 1)) * d;
-#pragma unroll
-          for (int j = 0; j < 8; j += N)
-            if (col(j) < d) {
-              if constexpr (VECT) store_n<N>(p + col(j), acc + j);
-              else p[col(j)] = acc[j];
-            }
-        } else {
-          T* o = table + (size_t)key * d;
-#pragma unroll
-          for (int j = 0; j < 8; ++j) acc[j] *= a.e.scale;
-#pragma unroll
-          for (int j = 0; j < 8; j += N)
-            if (col(j) < d) {
-              if constexpr (VECT) store_n<N>(o + col(j), acc + j);
-              else o[col(j)] = from_f<T>(acc[j]);
-            }
-        }
-        run_first = 0;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) acc[j] = 0.f;
+        for (int j = 0; j < 8; j += N)
+          if (col(j) < d) {
+            if constexpr (VECT) store_n<N>(o + col(j), acc + j);
+            else o[col(j)] = from_f<T>(acc[j]);
+          }
       }
+      first_run = false;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) acc[j] = 0.f;
+    }
+    if (e + kAhead - base == 32) {
+      base += 32;
+      cur_key = nxt_key;
+      cur_row = nxt_row;
+      fetch(base + 32, nxt_key, nxt_row);
     }
   }
 }
@@ -678,7 +711,7 @@ __global__ void __launch_bounds__(256) embed_join_kernel(EmbedGradArgs a) {
   __shared__ int s_run[256];
   __shared__ int s_warp[8];
   __shared__ float sh[8][kCols];
-  const int d = a.e.d;
+  const int d = a.e.d, n = a.e.rows;
   const int lane = threadIdx.x & 31, grp = threadIdx.x >> 5;
   const int blocks = (d + kCols - 1) / kCols;
   T* table = static_cast<T*>(a.e.grad_table);
@@ -687,8 +720,9 @@ __global__ void __launch_bounds__(256) embed_join_kernel(EmbedGradArgs a) {
   if (p + 1 < a.pieces) {
     const int i0 = p * a.per, i1 = i0 + a.per;
     const int key = key_of(a.list[i1 - 1]);
-    starts = key < a.e.n_emb && key_of(a.list[i1]) == key &&
-             !(i0 > 0 && key_of(a.list[i0 - 1]) == key);
+    // it goes on, through the whole next piece, and did not come in
+    starts = key < a.e.n_emb && key_of(a.list[min(n, i1 + a.per) - 1]) == key &&
+             !(i0 > 0 && key_of(a.list[i0]) == key && key_of(a.list[i0 - 1]) == key);
   }
   const unsigned m = __ballot_sync(0xffffffffu, starts);
   if (lane == 0) s_warp[grp] = __popc(m);
