@@ -47,6 +47,7 @@ enum Mode : int { kLoss = 0, kDlog = 1, kGrad = 2 };
 struct HeadMeta {
   int n;       // rows that take part
   int dense;   // 1: all of them do, and the caller's hidden is read in place
+  int heavy;   // rows whose D keeps its rounding's remainder for dW (see kHeavyRows)
 };
 
 struct HeadDev {
@@ -67,6 +68,12 @@ struct HeadDev {
   int r_pad;
   float* tlogit;            // [r_pad]
   // D
+  const int* slot;          // listed row -> its row of d_lo, or -1; null: no such rows
+  __nv_bfloat16* d_lo;      // [kHeavyRows][ld_dlog]
+  float* delta;             // [r_pad] remainder of D at the row's target
+  const void* head;         // the caller's weights
+  long long ld_head;
+  int head_vec;             // they start on 16-byte boundaries
   const float* lse;
   const float* grad_nll;
   __nv_bfloat16* dlog;      // [parts][r_pad][ld_dlog]
@@ -92,20 +99,21 @@ struct Unit {
   int kind;      // 0: H x W^T (loss, D); 1: dH; 2: dW
   int m0, n0;    // first row / column
   int k0, nk;    // first 64-wide K chunk, chunks
+  int k1;        // dW: chunks from here on are the heavy rows' remainders
   int split;
 };
 
 constexpr int kTileCost = 6;
 
-// Operands in parts.  P = 1: bf16 operands.  P = 2 (gradients of few rows): D in two bf16 parts.
-// P = 3 (fp32): both operands in three.  A pipeline stage holds a 64-wide K chunk of all parts,
-// and the products of parts that count are summed from it, smallest first.
+// Operands in parts.  P = 1: bf16 operands.  P = 3 (fp32): both operands in three.  A pipeline
+// stage holds a 64-wide K chunk of all parts, and the products of parts that count are summed
+// from it, smallest first.
 template <int P> constexpr int kAParts = P;
-template <int P> constexpr int kBParts = P == 3 ? 3 : 1;
-template <int P> constexpr int kProducts = P == 3 ? 6 : P;
+template <int P> constexpr int kBParts = P;
+template <int P> constexpr int kProducts = P == 3 ? 6 : 1;
 // parts of A and B in product t (t = 0 the smallest)
 template <int P> __host__ __device__ constexpr int part_a(int t) {
-  return P == 3 ? (0x021010 >> (4 * (5 - t))) & 15 : P - 1 - t;
+  return P == 3 ? (0x021010 >> (4 * (5 - t))) & 15 : 0;
 }
 template <int P> __host__ __device__ constexpr int part_b(int t) {
   return P == 3 ? (0x201100 >> (4 * (5 - t))) & 15 : 0;
@@ -126,11 +134,18 @@ constexpr bool kPromote = P == 3 || kMode == kLoss;
 template <int kMode, int CG, int BN, int P>
 constexpr int kChunks = kMode != kGrad && P == 1 && CG == 1 && BN <= 128 ? 2 : 1;
 
-// Rounding D to one bf16 part adds an error as large as the gradients' own rounding (together
-// 2.4e-3 of their norm against 1.7e-3).  Up to this many rows the products are bound by the
-// weights' traffic, and a second part (the rounding's remainder) costs XX; above it would cost
-// another pair of products (XX).
-constexpr int kTwoPartRows = 256;
+// What rounding D to bf16 costs, and what is done about it.  Alone it adds an error as large as the
+// gradients' own rounding (2.4e-3 of their norm against 1.7e-3), and up to 1.7 times that where a
+// few rows with large weights make up the norm.
+//  - A row's largest entry is its target's (it is minus the sum of the others).  Its remainder
+//    times the target's weights is added to dH in the epilogue, in fp32: dH's error falls back
+//    to its own rounding's, for every row.
+//  - For dW the heaviest rows (up to kHeavyRows, by |grad_nll|) keep their remainders as rows of a
+//    second, small matrix that is multiplied with copies of their hidden rows: two more K
+//    chunks per dW tile.
+//  - One row tile (head_narrow_kernel) keeps all remainders.
+constexpr int kHeavyRows = 128;
+
 // The work of one slot (CTA or pair) p of P.  Loss and D: tiles round robin, in groups of 16 row
 // tiles so that a group's rows stay in L2 while the weights pass once.  Gradients: the dH units
 // round robin, then the dW tiles so that every slot ends at about the same number of K chunks
@@ -138,10 +153,10 @@ constexpr int kTwoPartRows = 256;
 template <int kMode, int CG, int BN>
 struct Schedule {
   int p, P, n, kc, mt, nt;
-  int kw, nh, nw, mt_w, nt_d, my_h, qa, my_w, n_rem;
+  int kw, kx, nh, nw, mt_w, nt_d, my_h, qa, my_w, n_rem;
   int kch, kper;
 
-  SMDM_DEV Schedule(const HeadDev& a, int n_, int p_, int P_) : p(p_), P(P_), n(n_) {
+  SMDM_DEV Schedule(const HeadDev& a, int n_, int heavy, int p_, int P_) : p(p_), P(P_), n(n_) {
     constexpr int MT = 128 * CG;
     mt = (n + MT - 1) / MT;
     if constexpr (kMode != kGrad) {
@@ -152,6 +167,7 @@ struct Schedule {
       kch = (a.vc + 63) >> 6;
       kper = (kch + a.splits - 1) / a.splits;
       kw = (n + 63) >> 6;
+      kx = (heavy + 63) >> 6;
       mt_w = (a.vc + MT - 1) / MT;
       nh = a.do_h ? mt * nt_d * a.splits : 0;
       nw = a.do_w ? mt_w * nt_d : 0;
@@ -160,7 +176,7 @@ struct Schedule {
       my_h = c + (p < n_rem ? 1 : 0);
       // finishing time T of all slots, raised from the mean until every dW tile fits.  In fp32:
       // every thread of the grid computes the same values, and rounding only moves the balance.
-      const float ch = (float)kper * a.terms + kTileCost, cw = (float)kw * a.terms + kTileCost;
+      const float ch = (float)kper * a.terms + kTileCost, cw = (float)(kw + kx) * a.terms + kTileCost;
       auto fit = [&](float T, float used) {
         return T > used ? (int)fminf(__fdividef(T - used, cw), (float)nw) : 0;
       };
@@ -221,7 +237,8 @@ struct Schedule {
       u.m0 = (q / nt_d) * MT;
       u.n0 = (q % nt_d) * BN;
       u.k0 = 0;
-      u.nk = kw;
+      u.nk = kw + kx;
+      u.k1 = kw;
       return true;
     }
   }
@@ -322,6 +339,27 @@ SMDM_DEV void stage_f32(uint8_t* st, int lane, const float* v) {
         make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
 }
 
+// 32 columns of a row of dH: plus the remainder of D at the row's target times the target's weights.
+SMDM_DEV void add_target(const HeadDev& a, int tgt, float delta, int col, float* v) {
+  const __nv_bfloat16* w = static_cast<const __nv_bfloat16*>(a.head) + (size_t)tgt * a.ld_head + col;
+  if (a.head_vec && col + 32 <= a.d) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const uint4 u = *reinterpret_cast<const uint4*>(w + 8 * k);
+      const uint32_t x[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        v[8 * k + 2 * j] = fmaf(delta, __uint_as_float(x[j] << 16), v[8 * k + 2 * j]);
+        v[8 * k + 2 * j + 1] = fmaf(delta, __uint_as_float(x[j] & 0xffff0000u), v[8 * k + 2 * j + 1]);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 32; ++j)
+      if (col + j < a.d) v[j] = fmaf(delta, __bfloat162float(w[j]), v[j]);
+  }
+}
+
 // kMode: what is computed.  CG: CTAs per tile (2: a pair on two SMs, M = 256).  BN: tile
 // columns.  P: operand parts; 3 is the fp32 path.
 template <int kMode, int CG, int BN, int P>
@@ -331,6 +369,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                      const __grid_constant__ CUtensorMap tm_w,    // weights
                      const __grid_constant__ CUtensorMap tm_dk,   // D, K-major box
                      const __grid_constant__ CUtensorMap tm_dm,   // D, MN-major box
+                     const __grid_constant__ CUtensorMap tm_dl,   // its remainders' rows, likewise
+                     const __grid_constant__ CUtensorMap tm_hl,   // those rows' hidden
                      const HeadDev a) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -385,7 +425,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   // (no meta: every row of the caller's hidden, listed or not)
   const int n = a.meta ? a.meta->n : a.rows;
   const bool dense = a.meta ? a.meta->dense != 0 : true;
-  const Schedule<kMode, CG, BN> sch(a, n, blockIdx.x / CG, gridDim.x / CG);
+  const int heavy = kMode != kLoss && a.slot ? a.meta->heavy : 0;
+  const Schedule<kMode, CG, BN> sch(a, n, heavy, blockIdx.x / CG, gridDim.x / CG);
   auto lead_addr = [&](uint64_t* bar) -> uint32_t {
     return CG == 2 ? mapa_shared(smem_u32(bar), 0) : smem_u32(bar);
   };
@@ -427,8 +468,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 load(A + p * kABytes, &tm_dk, k * 64, p * a.d_plane + m0);
               } else {                    // dW: D (M contiguous)
 #pragma unroll
-                for (int j = 0; j < 2; ++j)
-                  load(A + p * kABytes + j * 8192, &tm_dm, m0 + j * 64, p * a.d_plane + k * 64);
+                for (int j = 0; j < 2; ++j) {
+                  if (k < u.k1)
+                    load(A + p * kABytes + j * 8192, &tm_dm, m0 + j * 64, p * a.d_plane + k * 64);
+                  else
+                    load(A + p * kABytes + j * 8192, &tm_dl, m0 + j * 64, (k - u.k1) * 64);
+                }
               }
             }
 #pragma unroll
@@ -439,8 +484,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                   load(B + (s * kBParts<P> + p) * kBPart, &tm_w, (k + s) * 64,
                        a.w_row0 + p * a.w_plane + n0);
               } else {                    // dH: W, dW: H (N contiguous)
-                const CUtensorMap* tb = u.kind == 1 ? &tm_w : th;
-                const int y = (u.kind == 1 ? a.w_row0 + p * a.w_plane : p * h_plane) + k * 64;
+                const bool lo = u.kind == 2 && k >= u.k1;
+                const CUtensorMap* tb = u.kind == 1 ? &tm_w : lo ? &tm_hl : th;
+                const int y = lo ? (k - u.k1) * 64
+                                 : (u.kind == 1 ? a.w_row0 + p * a.w_plane : p * h_plane) + k * 64;
 #pragma unroll
                 for (int j = 0; j < kBRows / 64; ++j)
                   load(B + p * kBPart + j * 8192, tb, n0 + j * 64, y);
@@ -531,7 +578,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; sch.get(a, i, u); ++i) {
       const int row = u.m0 + (int)rank * 128 + q * 32 + lane;   // row of the product
       const bool empty_sum = u.nk == 0;
-      int my_row = 0, tgt = -1;
+      int my_row = 0, tgt = -1, my_slot = -1;
       float lse = 0.f, g = 0.f;
       if (kMode != kGrad || u.kind == 1) {
         if (row < n) {
@@ -540,6 +587,17 @@ __global__ void __launch_bounds__(kThreads, 1)
           if constexpr (kMode == kDlog) {
             lse = a.lse[my_row];
             g = a.grad_nll[my_row];
+            if (!F32 && a.slot) my_slot = a.slot[row];
+          }
+          if constexpr (kMode == kGrad && !F32) {
+            // (kind 1) the row's target, where this unit's columns hold it
+            if (a.slot) {
+              const int t = a.target[my_row] - a.v0;
+              if (t >= u.k0 * 64 && t < min(a.vc, (u.k0 + u.nk) * 64)) {
+                tgt = t + a.v0;
+                g = a.delta[row];
+              }
+            }
           }
         }
       }
@@ -657,12 +715,16 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int j = 0; j < 32 * PC; ++j) v[j] = ex2(fmaf(v[j], kLog2e, off)) * g;
           } else {
+            float tv = 0.f;
 #pragma unroll
             for (int j = 0; j < 32 * PC; ++j) {
               float p = ex2((v[j] - lse) * kLog2e);
               if (j == rel) p -= 1.f;
               v[j] = j < lim ? p * g : 0.f;
+              if (j == rel) tv = v[j];
             }
+            if (!F32 && a.slot && row < n && rel >= 0 && rel < 32 * PC)
+              a.delta[row] = tv - __bfloat162float(__float2bfloat16_rn(tv));
           }
           // the parts one after the other, each the rounding of what the ones before leave
           for (int pl = 0; pl < a.d_parts; ++pl) {
@@ -678,6 +740,29 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
             }
           }
+          if (!F32 && my_slot >= 0) {
+            // (one or two lanes of a warp: straight from the registers)
+            uint4* dst = reinterpret_cast<uint4*>(a.d_lo + (size_t)my_slot * a.ld_dlog + col);
+#pragma unroll
+            for (int k = 0; k < 4 * PC; ++k) {
+              uint32_t w[4];
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                const float x = v[8 * k + 2 * j], y = v[8 * k + 2 * j + 1];
+                const uint32_t hi = pack_bf16(x, y);
+                w[j] = pack_bf16(x - __uint_as_float(hi << 16), y - __uint_as_float(hi & 0xffff0000u));
+              }
+              dst[k] = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+          }
+          if (!F32 && a.slot && u.m0 == 0 && rank == 0 && q == 0) {
+            // the last chunk of remainders is filled up with rows of zeros
+            const int zc = col + (lane & 7) * 8;
+            if ((lane & 7) * 8 < 32 * PC)
+              for (int r = heavy + (lane >> 3); r < ((heavy + 63) & ~63); r += 4)
+                *reinterpret_cast<uint4*>(a.d_lo + (size_t)r * a.ld_dlog + zc) =
+                    make_uint4(0, 0, 0, 0);
+          }
         }
       } else if (u.kind == 1 && a.acc) {
         // fp32 sums of this piece and K range
@@ -687,6 +772,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int col = ccol + c * 32;
           float v[32];
           load(c, v);
+          if (!F32 && tgt >= 0) add_target(a, tgt, g, col, v);
           stage_f32(st, lane, v);
           if (a.acc_add) {
             __syncwarp();
@@ -725,6 +811,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int s2 = 0; s2 < PC; ++s2) {
             float v[32];
             load(c + s2, v);
+            if (!F32 && tgt >= 0) add_target(a, tgt, g, ccol + (c + s2) * 32, v);
             if constexpr (F32) stage_f32(st, lane, v);
             else stage_bf16<RB>(st, lane, s2 * 4, v);
           }
@@ -1020,6 +1107,9 @@ struct RowsArgs {
   HeadMeta* meta;
   int* row_idx;
   __nv_bfloat16* out;          // [parts][r_pad][d_pad]
+  const float* grad_nll;       // heavy rows are looked for; null: not
+  int* slot;                   // [r_pad]
+  __nv_bfloat16* heavy_out;    // [kHeavyRows][d_pad]
   float *nll, *lse;            // loss: zero for the rows that take no part
   void* grad_hidden;           // gradient: likewise
   bool gvec;
@@ -1078,9 +1168,9 @@ SMDM_DEV void put_row(const T* x, int d, int d_pad, bool vec, __nv_bfloat16* o, 
   }
 }
 
-SMDM_DEV void copy_row(const RowsArgs& a, int src, int dst, int lane) {
+SMDM_DEV void copy_row(const RowsArgs& a, int src, __nv_bfloat16* out, int dst, int lane) {
   const size_t plane = (size_t)a.r_pad * a.d_pad;
-  __nv_bfloat16* o = a.out + (size_t)dst * a.d_pad;
+  __nv_bfloat16* o = out + (size_t)dst * a.d_pad;
   if (a.f32)
     put_row(static_cast<const float*>(a.hidden) + (size_t)src * a.ld, a.d, a.d_pad, a.vec, o, plane,
             lane);
@@ -1127,15 +1217,42 @@ __global__ void __launch_bounds__(256) head_rows_kernel(RowsArgs a, WeightArgs w
   }
   __shared__ int red[2][8];
   __shared__ int s_before, s_total;
+  __shared__ int hist[2048];                  // rows by the leading bits of |grad_nll|
+  __shared__ int s_thr, s_hbefore, s_heavy;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int r0 = blockIdx.x * a.per, r1 = min(a.rows, r0 + a.per);
   int before = 0, total = 0;
-  for (int r = tid; r < a.rows; r += 256) {
-    const int t = a.target[r];
-    const int on = t >= 0 && t < a.vocab;
+  // sign-free bits of grad_nll from the exponent down to three bits of the mantissa
+  auto bin_of = [](float g) { return (int)((__float_as_uint(g) & 0x7fffffffu) >> 20); };
+  auto weight_bin = [&](int r) { return bin_of(a.grad_nll[r]); };
+  // f(row, takes part, bin of its weight) for this thread's share of all rows, eight loads ahead
+  auto scan = [&](auto f) {
+    for (int base = tid; base < a.rows; base += 8 * 256) {
+      int t[8];
+      float g[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int r = min(base + k * 256, a.rows - 1);
+        t[k] = a.target[r];
+        g[k] = a.grad_nll ? a.grad_nll[r] : 0.f;
+      }
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int r = base + k * 256;
+        if (r < a.rows) f(r, t[k] >= 0 && t[k] < a.vocab, bin_of(g[k]));
+      }
+    }
+  };
+  if (a.grad_nll) {
+    for (int i = tid; i < 2048; i += 256) hist[i] = 0;
+    if (tid == 0) s_thr = 0;
+    __syncthreads();
+  }
+  scan([&](int r, bool on, int bin) {
     total += on;
     if (r < r0) before += on;
-  }
+    if (on && a.grad_nll) atomicAdd(&hist[bin], 1);
+  });
   for (int o = 16; o > 0; o >>= 1) {
     before += __shfl_xor_sync(0xffffffffu, before, o);
     total += __shfl_xor_sync(0xffffffffu, total, o);
@@ -1155,7 +1272,52 @@ __global__ void __launch_bounds__(256) head_rows_kernel(RowsArgs a, WeightArgs w
   __syncthreads();
   const int n = s_total;
   const bool dense = a.in_place && n == a.rows;
-  int at = s_before;
+  int at = s_before, hat = 0, thr = 0, heavy = 0;
+  if (a.grad_nll) {
+    // the smallest bin from which on at most kHeavyRows rows lie (thread t: eight bins, the
+    // largest ones first)
+    int mine = 0;
+    for (int k = 0; k < 8; ++k) mine += hist[2047 - 8 * tid - k];
+    int pre = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int x = __shfl_up_sync(0xffffffffu, pre, o);
+      if (lane >= o) pre += x;
+    }
+    if (lane == 31) red[0][warp] = pre;
+    __syncthreads();
+    for (int w = 0; w < warp; ++w) pre += red[0][w];
+    int sum = pre - mine;                      // rows in the bins above this thread's
+    if (sum <= kHeavyRows && pre > kHeavyRows) {
+      int b = 2047 - 8 * tid;
+      while (sum + hist[b] <= kHeavyRows) sum += hist[b--];
+      s_thr = b + 1;
+    }
+    __syncthreads();
+    thr = s_thr;
+    int hb = 0, ht = 0;
+    scan([&](int r, bool on, int bin) {
+      on = on && bin >= thr;
+      ht += on;
+      if (r < r0) hb += on;
+    });
+    for (int o = 16; o > 0; o >>= 1) {
+      hb += __shfl_xor_sync(0xffffffffu, hb, o);
+      ht += __shfl_xor_sync(0xffffffffu, ht, o);
+    }
+    if (lane == 0) { red[0][warp] = hb; red[1][warp] = ht; }
+    __syncthreads();
+    if (tid == 0) {
+      int b = 0, t = 0;
+      for (int w = 0; w < 8; ++w) { b += red[0][w]; t += red[1][w]; }
+      s_hbefore = b;
+      s_heavy = t;
+      if (blockIdx.x == 0) a.meta->heavy = t;
+    }
+    __syncthreads();
+    hat = s_hbefore;
+    heavy = s_heavy;
+  }
   // 32 rows at a time: every warp works out the same listed positions, then takes every 8th row
   for (int b = r0; b < r1; b += 32) {
     const int r = b + lane;
@@ -1165,6 +1327,11 @@ __global__ void __launch_bounds__(256) head_rows_kernel(RowsArgs a, WeightArgs w
     const uint32_t mask = __ballot_sync(0xffffffffu, on);
     const int pos = at + __popc(mask & ((1u << lane) - 1u));
     at += __popc(mask);
+    const bool hv = a.grad_nll && on && weight_bin(r) >= thr;
+    const uint32_t hmask = __ballot_sync(0xffffffffu, hv);
+    const int slot = hv ? hat + __popc(hmask & ((1u << lane) - 1u)) : -1;
+    hat += __popc(hmask);
+    if (warp == 0 && a.grad_nll && on) a.slot[pos] = slot;
     if (warp == 0 && r < r1) {
       if (on) {
         a.row_idx[pos] = r;
@@ -1175,8 +1342,10 @@ __global__ void __launch_bounds__(256) head_rows_kernel(RowsArgs a, WeightArgs w
     }
     for (int i = warp; i < min(32, r1 - b); i += 8) {
       const int p = __shfl_sync(0xffffffffu, pos, i);
+      const int sl = __shfl_sync(0xffffffffu, slot, i);
       if ((mask >> i) & 1u) {
-        if (!dense) copy_row(a, b + i, p, lane);
+        if (!dense) copy_row(a, b + i, a.out, p, lane);
+        if (sl >= 0) copy_row(a, b + i, a.heavy_out, sl, lane);
       } else if (a.grad_hidden) {
         const size_t es = a.f32 ? 4 : 2;
         uint8_t* g = static_cast<uint8_t*>(a.grad_hidden) + (size_t)(b + i) * a.d * es;
@@ -1192,6 +1361,11 @@ __global__ void __launch_bounds__(256) head_rows_kernel(RowsArgs a, WeightArgs w
       }
     }
   }
+  // likewise the heavy rows' last chunk
+  if (a.grad_nll)
+    for (int r = heavy + blockIdx.x * 8 + warp; r < ((heavy + 63) & ~63); r += a.row_ctas * 8)
+      for (int c = lane * 8; c < a.d_pad; c += 256)
+        *reinterpret_cast<uint4*>(a.heavy_out + (size_t)r * a.d_pad + c) = make_uint4(0, 0, 0, 0);
   // the rows up to the next multiple of 64 (128 with one row tile) are summed over by dW: zeros,
   // every CTA its share
   if (a.pad_rows && !dense) {
@@ -1349,7 +1523,8 @@ struct Plan {
   int d_parts, g_terms;   // bf16 parts of D; products summed by the gradients
   bool staged;        // weights go through a bf16 copy of each piece
   int piece, n_pieces;
-  size_t meta, row_idx, hid, part, tlogit, wst, dlog, acc, total;
+  bool heavy;         // the heaviest rows' remainders
+  size_t meta, row_idx, hid, part, tlogit, wst, dlog, acc, slot, delta, hlo, dlo, total;
   int cfg, cfg_g;     // tile configuration of the logits' product and of the gradients'
   int splits, n_part;
   int narrow;         // > 0: head_narrow_kernel, with this many vocabulary slots (= splits)
@@ -1403,8 +1578,9 @@ Plan make_plan(int rows, int d, int vocab, long long ld_head, bool f32, bool gra
     p.total = head_few_bytes(rows, d, vocab, sms);
     return p;
   }
-  p.d_parts = f32 ? 3 : rows <= kTwoPartRows ? 2 : 1;
-  p.g_terms = f32 ? 6 : p.d_parts;
+  p.d_parts = f32 ? 3 : rows <= 128 ? 2 : 1;
+  p.g_terms = f32 ? 6 : 1;
+  p.heavy = grad && p.d_parts == 1;
   // widest piece whose D (gradient) and weight copy (when made) stay below kPieceBytes
   size_t per_col = 0;
   if (grad) per_col = (size_t)p.d_parts * p.r_pad * 2;
@@ -1460,6 +1636,12 @@ Plan make_plan(int rows, int d, int vocab, long long ld_head, bool f32, bool gra
   if (p.staged) p.wst = take((size_t)p.parts * p.piece * p.d_pad * 2);
   if (grad) {
     p.dlog = take((size_t)p.d_parts * p.r_pad * p.piece * 2);
+    if (p.heavy) {
+      p.slot = take((size_t)p.r_pad * 4);
+      p.delta = take((size_t)p.r_pad * 4);
+      p.hlo = take((size_t)kHeavyRows * p.d_pad * 2);
+      p.dlo = take((size_t)kHeavyRows * p.piece * 2);
+    }
     if (p.narrow || p.splits > 1 || p.n_pieces > 1) p.acc = take((size_t)p.splits * p.r_pad * p.d_pad * 4);
   }
   p.total = off;
@@ -1480,7 +1662,7 @@ bool encode_bf16(CUtensorMap* m, const void* base, uint64_t inner, uint64_t oute
 }
 
 struct Maps {
-  CUtensorMap h, hc, w, dk, dm;
+  CUtensorMap h, hc, w, dk, dm, dl, hl;
 };
 
 // Clusters of the pair kernels that fit the device at once (some SM groups are odd).
@@ -1534,7 +1716,7 @@ cudaError_t launch_one(const Maps& m, HeadDev a, long long units, int sms, cudaS
   long long slots = std::min<long long>(ready[dev], units);
   if (slots < 1) slots = 1;
   return launch_pdl(kern, dim3((unsigned)(slots * CG)), dim3(kThreads), (size_t)smem, st, CG, m.h,
-                    m.hc, m.w, m.dk, m.dm, a);
+                    m.hc, m.w, m.dk, m.dm, m.dl, m.hl, a);
 }
 
 template <int kMode, int P>
@@ -1555,8 +1737,6 @@ template <int kMode>
 cudaError_t launch_mode(int parts, int cfg, const Maps& m, const HeadDev& a, long long units,
                         int sms, cudaStream_t st) {
   if (parts == 3) return launch_cfg<kMode, 3>(cfg, m, a, units, sms, st);
-  if constexpr (kMode == kGrad)
-    if (parts == 2) return launch_cfg<kMode, 2>(cfg, m, a, units, sms, st);
   return launch_cfg<kMode, 1>(cfg, m, a, units, sms, st);
 }
 
@@ -1621,6 +1801,11 @@ struct Call {
     r.out = at<__nv_bfloat16>(p.hid);
     r.nll = h.nll;
     r.lse = h.lse_out;
+    if (p.heavy) {
+      r.grad_nll = h.grad_nll;
+      r.slot = at<int>(p.slot);
+      r.heavy_out = at<__nv_bfloat16>(p.hlo);
+    }
     r.grad_hidden = h.grad_hidden;
     r.gvec = whole_words(h.grad_hidden, h.d);
     r.status = h.status;
@@ -1740,7 +1925,7 @@ cudaError_t launch_head_loss(const HeadArgs& h, cudaStream_t st) {
     a.a_box = c.a_box();
     if (!c.hidden_maps(&m.h, &m.hc, a.a_box) || !c.weight_map(&m.w, vc, bn / cg))
       return cudaErrorInvalidValue;
-    m.dk = m.dm = m.hc;
+    m.dk = m.dm = m.dl = m.hl = m.hc;
     a.part = c.at<float2>(p.part);
     a.part0 = 2 * (p.piece / bn) * i;
     a.tlogit = c.at<float>(p.tlogit);
@@ -1772,13 +1957,21 @@ cudaError_t launch_head_grad(const HeadArgs& h, cudaStream_t st) {
     a.a_box = c.a_box();
     if (!c.hidden_maps(&m.h, &m.hc, a.a_box) || !c.weight_map(&m.w, vc, bn / cg))
       return cudaErrorInvalidValue;
-    m.dk = m.dm = m.hc;
+    m.dk = m.dm = m.dl = m.hl = m.hc;
     a.d_parts = p.d_parts;
     a.d_rows = p.narrow ? c.narrow_rows() : p.r_pad;
     a.lse = h.lse;
     a.grad_nll = h.grad_nll;
     a.dlog = c.at<__nv_bfloat16>(p.dlog);
     a.ld_dlog = p.piece;
+    if (p.heavy) {
+      a.slot = c.at<int>(p.slot);
+      a.d_lo = c.at<__nv_bfloat16>(p.dlo);
+      a.delta = c.at<float>(p.delta);
+      a.head = h.head;
+      a.ld_head = h.ld_head;
+      a.head_vec = c.whole_words(h.head, h.ld_head);
+    }
     const long long units = (long long)((h.rows + 128 * cg - 1) / (128 * cg)) * ((vc + bn - 1) / bn);
     TRY(launch_mode<kDlog>(p.parts, p.cfg, m, a, units, c.sms, st));
     // both products of D: 64-row boxes for the MN-major operands
@@ -1786,6 +1979,9 @@ cudaError_t launch_head_grad(const HeadArgs& h, cudaStream_t st) {
         !encode_bf16(&m.dk, a.dlog, p.piece, (uint64_t)p.d_parts * p.r_pad, p.piece, 64,
                      p.narrow ? a.d_rows : 128) ||
         !encode_bf16(&m.dm, a.dlog, p.piece, (uint64_t)p.d_parts * p.r_pad, p.piece, 64, 64))
+      return cudaErrorInvalidValue;
+    if (p.heavy && (!encode_bf16(&m.dl, a.d_lo, p.piece, kHeavyRows, p.piece, 64, 64) ||
+                    !encode_bf16(&m.hl, c.at<__nv_bfloat16>(p.hlo), p.d_pad, kHeavyRows, p.d_pad, 64, 64)))
       return cudaErrorInvalidValue;
     a.terms = p.g_terms;
     a.do_h = h.grad_hidden != nullptr;

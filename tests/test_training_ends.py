@@ -141,10 +141,10 @@ class Head:
         D = p.clone()
         D.scatter_add_(1, t, torch.full_like(g, -1.0))
         D *= g
-        # errors of D: the logit's and exp's (systematic), its rounding (independent; with 256 rows
+        # errors of D: the logit's and exp's (systematic), its rounding (independent; with 128 rows
         # or fewer D keeps two bf16 parts: 2^-16)
         sys_d = g.abs() * p * (dz[:, None] + 2.0 ** -20)
-        u = (2.0 ** -8 if self.rows > 256 else 2.0 ** -16) if self.dt == BF16 else 2.0 ** -23
+        u = (2.0 ** -8 if self.rows > 128 else 2.0 ** -16) if self.dt == BF16 else 2.0 ** -23
         out = u_of(self.dt)
         for what, got, ref, s, q, mag, k in (
                 ("grad_hidden", gh, D @ w, sys_d @ w.abs(), (D * D) @ (w * w), D.abs() @ w.abs(),
