@@ -705,26 +705,29 @@ __global__ void __launch_bounds__(256) embed_sum_kernel(EmbedGradArgs a) {
   }
 }
 
-// Add up the parts of every run that starts in one piece and goes on in the next: eight groups
-// of warps take every eighth part in order, then the groups are added in order.  The CTAs with one
+constexpr int kJoinThreads = 512;
+
+// Add up the parts of every run that starts in one piece and goes on in the next: 16 warps
+// take every 16th part in order, then the warps' sums are added in order.  The CTAs with one
 // blockIdx.x look at the same 256 pieces, find the runs that start there and share their (run,
 // column block) pairs; a CTA per piece would mostly start CTAs that have nothing to do.
 // VECT: a lane's four columns lie together, else 32 apart.
 template <typename T, bool VECT>
-__global__ void __launch_bounds__(256) embed_join_kernel(EmbedGradArgs a) {
+__global__ void __launch_bounds__(kJoinThreads) embed_join_kernel(EmbedGradArgs a) {
   griddep_launch();
   griddep_wait();
   constexpr int VEC = 4, kCols = 32 * VEC;
   __shared__ int s_run[256];
-  __shared__ int s_warp[8];
-  __shared__ float sh[8][kCols];
+  constexpr int kGroups = kJoinThreads / 32;
+  __shared__ int s_warp[kGroups];
+  __shared__ float sh[kGroups][kCols];
   const int d = a.e.d, n = a.e.rows;
   const int lane = threadIdx.x & 31, grp = threadIdx.x >> 5;
   const int blocks = (d + kCols - 1) / kCols;
   T* table = static_cast<T*>(a.e.grad_table);
   const int p = blockIdx.x * 256 + threadIdx.x;
   bool starts = false;
-  if (p + 1 < a.pieces) {
+  if (threadIdx.x < 256 && p + 1 < a.pieces) {
     const int i0 = p * a.per, i1 = i0 + a.per;
     const int key = key_of(a.list[i1 - 1]);
     // it goes on, through the whole next piece, and did not come in
@@ -735,7 +738,7 @@ __global__ void __launch_bounds__(256) embed_join_kernel(EmbedGradArgs a) {
   if (lane == 0) s_warp[grp] = __popc(m);
   __syncthreads();
   int at = 0, runs = 0;
-  for (int w = 0; w < 8; ++w) {
+  for (int w = 0; w < kGroups; ++w) {
     if (w < grp) at += s_warp[w];
     runs += s_warp[w];
   }
@@ -753,12 +756,12 @@ __global__ void __launch_bounds__(256) embed_join_kernel(EmbedGradArgs a) {
 #pragma unroll
     for (int k = 0; k < VEC; ++k) s[k] = 0.f;
     bool more = true;
-    for (int k0 = grp; more && first + k0 < a.pieces; k0 += 8 * 4) {
+    for (int k0 = grp; more && first + k0 < a.pieces; k0 += kGroups * 4) {
       float v[4][VEC];
       bool in[4];
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
-        const int k = k0 + 8 * u, q = min(first + k, a.pieces - 1);
+        const int k = k0 + kGroups * u, q = min(first + k, a.pieces - 1);
         in[u] = first + k < a.pieces && (k == 0 || key_of(a.list[(size_t)q * a.per]) == key);
         const float* p = a.part + ((size_t)q * 2 + (k == 0 ? 1 : 0)) * d;
         if constexpr (VECT) {
@@ -782,7 +785,7 @@ __global__ void __launch_bounds__(256) embed_join_kernel(EmbedGradArgs a) {
     if (threadIdx.x < kCols) {
       const int cc = c0 + threadIdx.x;
       float t = 0.f;
-      for (int g = 0; g < 8; ++g) t += sh[g][threadIdx.x];
+      for (int g = 0; g < kGroups; ++g) t += sh[g][threadIdx.x];
       if (cc < d) table[(size_t)key * d + cc] = from_f<T>(t * a.e.scale);
     }
     __syncthreads();
@@ -940,9 +943,9 @@ cudaError_t embed_grad_types(const EmbedGradArgs& g, cudaStream_t st) {
                           : launch_pdl(embed_sum_kernel<T, O, false>, grid, dim3(256), 0, st, 1, g);
   if (e != cudaSuccess || g.pieces < 2) return e;
   const int batches = (g.pieces - 1 + 255) / 256;
-  const dim3 jgrid(batches, std::max(1, std::min(65535, device_sms() * 8 / batches)));
-  return a.d % 4 == 0 ? launch_pdl(embed_join_kernel<T, true>, jgrid, dim3(256), 0, st, 1, g)
-                      : launch_pdl(embed_join_kernel<T, false>, jgrid, dim3(256), 0, st, 1, g);
+  const dim3 jgrid(batches, std::max(1, std::min(65535, device_sms() * 4 / batches)));
+  return a.d % 4 == 0 ? launch_pdl(embed_join_kernel<T, true>, jgrid, dim3(kJoinThreads), 0, st, 1, g)
+                      : launch_pdl(embed_join_kernel<T, false>, jgrid, dim3(kJoinThreads), 0, st, 1, g);
 }
 
 }  // namespace

@@ -1919,13 +1919,13 @@ bool head_needs_aligned_weight(int d, long long ld_head, bool f32) {
 int head_loss_launches(const HeadArgs& a) {
   const Call c(a, false);
   const Plan& p = c.p;
-  if (p.few) return 2;
+  if (p.few) return 1 + head_few_groups(a.rows, a.d);
   return 1 + (c.listed() ? 1 : 0) + p.n_pieces + (p.staged ? p.n_pieces - 1 : 0);
 }
 
 int head_grad_launches(const HeadArgs& a) {
   const Plan p = make_plan(a.rows, a.d, a.vocab, a.ld_head, a.f32, true);
-  if (p.few) return a.grad_hidden ? 3 : 2;
+  if (p.few) return 1 + head_few_groups(a.rows, a.d) + (a.grad_hidden ? 1 : 0);
   const bool sums = p.narrow || p.splits > 1 || p.n_pieces > 1;
   return 1 + 2 * p.n_pieces + (p.staged ? p.n_pieces - 1 : 0) + (sums && a.grad_hidden ? 1 : 0);
 }

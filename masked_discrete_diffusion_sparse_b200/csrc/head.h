@@ -33,8 +33,9 @@ cudaError_t launch_head_grad(const HeadArgs& a, cudaStream_t st);
 
 // The same for a handful of rows (head_few.cu); `sms`: SMs of the device.
 constexpr int kFewRows = 16;
-constexpr int kFewSmem = 200 * 1024;     // all hidden rows in fp32
+constexpr int kFewSmem = 200 * 1024;     // the hidden rows of a launch in fp32
 bool head_few_fits(int rows, int d);
+int head_few_groups(int rows, int d);    // launches that make the logits
 size_t head_few_bytes(int rows, int d, int vocab, int sms);
 cudaError_t launch_head_few_loss(const HeadArgs& a, int sms, cudaStream_t st);
 cudaError_t launch_head_few_grad(const HeadArgs& a, int sms, cudaStream_t st);

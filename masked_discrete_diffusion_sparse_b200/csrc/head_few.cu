@@ -30,17 +30,18 @@ SMDM_DEV float ex2(float x) {
 
 struct FewDev {
   int rows, d, d_pad, vocab;     // d_pad: d rounded up to 256
+  int row0;                      // logits: first row of the launch's group
   long long ld_hidden, ld_head;
   const void* hidden;
   const void* head;
   const int* target;
   // loss
-  float2* part;                  // [RM][CTAs]
-  float* tlogit;                 // [RM]
+  float2* part;                  // [16][CTAs]
+  float* tlogit;                 // [16]
   // gradient
   const float* lse;
   const float* grad_nll;
-  float* dlog;                   // [RM][ld_dlog]
+  float* dlog;                   // [16][ld_dlog]
   int ld_dlog;
   float* acc;                    // [chunks][RM][d_pad]
   int chunk;                     // vocabulary rows of one gradient CTA
@@ -67,6 +68,13 @@ struct Piece {
     else return __uint_as_float(i & 1 ? w[i >> 1] & 0xffff0000u : w[i >> 1] << 16);
   }
 };
+template <>
+struct Piece<__nv_bfloat16, 2> {
+  uint32_t w;
+  SMDM_DEV void load(const __nv_bfloat16* p) { w = *reinterpret_cast<const uint32_t*>(p); }
+  SMDM_DEV void zero() { w = 0; }
+  SMDM_DEV float get(int i) const { return __uint_as_float(i & 1 ? w & 0xffff0000u : w << 16); }
+};
 template <typename T>
 struct Piece<T, 1> {
   T x;
@@ -77,30 +85,32 @@ struct Piece<T, 1> {
 
 // Logits of RM rows: a warp and four vocabulary rows per turn.  GRAD: their gradient into dlog;
 // else the running (maximum, sum) of every row.
-// E: elements per load (16 bytes, or 1 for rows off those boundaries).
+// E: elements per load (16 bytes; 4 or one element for rows off those boundaries).
 template <typename T, int E, int RM, bool GRAD>
 __global__ void __launch_bounds__(kFewThreads) few_logits_kernel(FewDev a) {
   griddep_launch();
   griddep_wait();
   extern __shared__ __align__(16) float sh[];       // [RM][d_pad]
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  for (int r = warp; r < RM; r += kFewThreads / 32) {
+  for (int i = warp; i < RM; i += kFewThreads / 32) {
     // (a row that takes no part counts as zeros: what it holds reaches nothing)
+    const int r = a.row0 + i;
     const bool on = takes_part(a, r);
     const T* h = static_cast<const T*>(a.hidden) + (size_t)r * a.ld_hidden;
     for (int c = lane; c < a.d_pad; c += 32)
-      sh[(size_t)r * a.d_pad + c] = on && c < a.d ? to_f<T>(h[c]) : 0.f;
+      sh[(size_t)i * a.d_pad + c] = on && c < a.d ? to_f<T>(h[c]) : 0.f;
     if (blockIdx.x == 0 && lane == 0 && r < a.rows && a.target[r] >= a.vocab && a.status)
       atomicOr(a.status, kStatusBounds);
   }
   __syncthreads();
   constexpr int NV = 4, N = NV * RM;                // sums of a turn, index r * NV + v
-  constexpr int U = E == 1 ? 4 : 2;                 // K steps whose loads are in flight together
+  constexpr int U = E * sizeof(T) < 16 ? 8 : 2;     // K steps whose loads are in flight together
   constexpr int KEEP = N >= 32 ? N / 32 : 1;        // sums a lane ends up with
+  constexpr int EH = E < 4 ? E : 4;                 // hidden values per shared load
   constexpr int DUP = N < 32 ? 32 / N : 1;          // lanes that end up with the same sum
   // the lane's sums: index first + 0 .. KEEP - 1
   const int first = lane / DUP * KEEP;
-  const int my_r = first / NV;
+  const int my_r = a.row0 + first / NV;
   const int tgt = takes_part(a, my_r) ? a.target[my_r] : -1;
   float lse = 0.f, g = 0.f;
   if (GRAD && tgt >= 0) {
@@ -133,20 +143,23 @@ __global__ void __launch_bounds__(kFewThreads) few_logits_kernel(FewDev a) {
         // (past d the weights are zero and the copy of the row is, too: d_pad covers it)
         const int k = min(k0 + u * 32 * E, a.d_pad - E);
 #pragma unroll
-        for (int e0 = 0; e0 < E; e0 += (E >= 4 ? 4 : 1)) {
+        for (int e0 = 0; e0 < E; e0 += EH) {
 #pragma unroll
           for (int r = 0; r < RM; ++r) {
             float h[4];
-            if constexpr (E >= 4) {
+            if constexpr (EH == 4) {
               const float4 f = *reinterpret_cast<const float4*>(sh + (size_t)r * a.d_pad + k + e0);
               h[0] = f.x; h[1] = f.y; h[2] = f.z; h[3] = f.w;
+            } else if constexpr (EH == 2) {
+              const float2 f = *reinterpret_cast<const float2*>(sh + (size_t)r * a.d_pad + k);
+              h[0] = f.x; h[1] = f.y;
             } else {
               h[0] = sh[(size_t)r * a.d_pad + k];
             }
 #pragma unroll
             for (int i = 0; i < NV; ++i)
 #pragma unroll
-              for (int e = 0; e < (E >= 4 ? 4 : 1); ++e)
+              for (int e = 0; e < EH; ++e)
                 acc[r * NV + i] = fmaf(p[u][i].get(e0 + e), h[e], acc[r * NV + i]);
           }
         }
@@ -212,7 +225,7 @@ __global__ void __launch_bounds__(kFewThreads) few_logits_kernel(FewDev a) {
       float t = p.y == 0.f ? 0.f : p.y * ex2((p.x - mx) * kLog2e);
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
-      if (lane == 0) a.part[(size_t)r * gridDim.x + blockIdx.x] = make_float2(mx, t);
+      if (lane == 0) a.part[(size_t)(a.row0 + r) * gridDim.x + blockIdx.x] = make_float2(mx, t);
     }
   }
 }
@@ -387,10 +400,16 @@ __global__ void __launch_bounds__(1024) few_sum_kernel(FewDev a, int chunks) {
 size_t up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
 int few_rm(int rows) { return rows <= 4 ? 4 : rows <= 8 ? 8 : 16; }
-size_t few_smem(int rows, int d) { return (size_t)few_rm(rows) * up(d, 256) * 4; }
+// Rows of one logits launch: as many as fit shared memory (0: not even four).
+int few_group(int rows, int d) {
+  int g = few_rm(rows);
+  while (g >= 4 && (size_t)g * up(d, 256) * 4 > (size_t)kFewSmem) g /= 2;
+  return g < 4 ? 0 : g;
+}
+size_t few_smem(int rows, int d) { return (size_t)few_group(rows, d) * up(d, 256) * 4; }
 
 struct FewPlan {
-  int rm, ctas, slabs, chunk, chunks;
+  int rm, group, ctas, slabs, chunk, chunks;
   size_t part, tlogit, dlog, acc, total;
 };
 
@@ -398,6 +417,7 @@ struct FewPlan {
 FewPlan few_plan(int rows, int d, int vocab, int sms, bool wide) {
   FewPlan p{};
   p.rm = few_rm(rows);
+  p.group = few_group(rows, d);
   const int per_sm = few_smem(rows, d) <= 56 * 1024 ? 4 : few_smem(rows, d) <= 110 * 1024 ? 2 : 1;
   p.ctas = std::min((vocab + 31) / 32, sms * per_sm);
   const int cols = kGradThreads * (wide ? 4 : 1);
@@ -441,14 +461,28 @@ cudaError_t logits_one(const FewDev& a, int ctas, cudaStream_t st) {
   return launch_pdl(kern, dim3(ctas), dim3(kFewThreads), (size_t)RM * a.d_pad * 4, st, 1, a);
 }
 
-template <typename T, bool GRAD>
-cudaError_t logits_rm(const FewDev& a, int rm, bool vec, int ctas, cudaStream_t st) {
-  constexpr int E = 16 / (int)sizeof(T);
-  switch (rm) {
-    case 4: return vec ? logits_one<T, E, 4, GRAD>(a, ctas, st) : logits_one<T, 1, 4, GRAD>(a, ctas, st);
-    case 8: return vec ? logits_one<T, E, 8, GRAD>(a, ctas, st) : logits_one<T, 1, 8, GRAD>(a, ctas, st);
-    default: return vec ? logits_one<T, E, 16, GRAD>(a, ctas, st) : logits_one<T, 1, 16, GRAD>(a, ctas, st);
+template <typename T, int E, bool GRAD>
+cudaError_t logits_rm(FewDev a, const FewPlan& p, cudaStream_t st) {
+  for (a.row0 = 0; a.row0 < a.rows; a.row0 += p.group) {
+    const cudaError_t e = p.group == 4   ? logits_one<T, E, 4, GRAD>(a, p.ctas, st)
+                          : p.group == 8 ? logits_one<T, E, 8, GRAD>(a, p.ctas, st)
+                                         : logits_one<T, E, 16, GRAD>(a, p.ctas, st);
+    if (e != cudaSuccess) return e;
   }
+  return cudaSuccess;
+}
+
+template <bool GRAD>
+cudaError_t logits_any(const HeadArgs& h, const FewDev& a, const FewPlan& p, cudaStream_t st) {
+  const uintptr_t base = reinterpret_cast<uintptr_t>(h.head);
+  const int es = h.f32 ? 4 : 2;
+  const bool words = base % 16 == 0 && (long long)h.d * es % 16 == 0 && h.ld_head * es % 16 == 0;
+  if (h.f32)
+    return words ? logits_rm<float, 4, GRAD>(a, p, st) : logits_rm<float, 1, GRAD>(a, p, st);
+  if (words) return logits_rm<__nv_bfloat16, 8, GRAD>(a, p, st);
+  return base % 4 == 0 && h.d % 2 == 0 && h.ld_head % 2 == 0
+             ? logits_rm<__nv_bfloat16, 2, GRAD>(a, p, st)
+             : logits_rm<__nv_bfloat16, 1, GRAD>(a, p, st);
 }
 
 template <typename T, int RM>
@@ -497,7 +531,12 @@ bool weight_words(const HeadArgs& h) {
 
 }  // namespace
 
-bool head_few_fits(int rows, int d) { return rows <= kFewRows && few_smem(rows, d) <= kFewSmem; }
+bool head_few_fits(int rows, int d) { return rows <= kFewRows && few_group(rows, d) > 0; }
+
+int head_few_groups(int rows, int d) {
+  const int g = few_group(rows, d);
+  return (rows + g - 1) / g;
+}
 
 size_t head_few_bytes(int rows, int d, int vocab, int sms) {
   return std::max(few_plan(rows, d, vocab, sms, true).total,
@@ -507,9 +546,7 @@ size_t head_few_bytes(int rows, int d, int vocab, int sms) {
 cudaError_t launch_head_few_loss(const HeadArgs& h, int sms, cudaStream_t st) {
   const FewPlan p = few_plan(h.rows, h.d, h.vocab, sms, true);
   const FewDev a = few_dev(h, p);
-  const bool vec = weight_words(h);
-  const cudaError_t e = h.f32 ? logits_rm<float, false>(a, p.rm, vec, p.ctas, st)
-                              : logits_rm<__nv_bfloat16, false>(a, p.rm, vec, p.ctas, st);
+  const cudaError_t e = logits_any<false>(h, a, p, st);
   if (e != cudaSuccess) return e;
   return launch_pdl(few_finish_kernel, dim3(1), dim3(32 * p.rm), 0, st, 1, a, p.ctas, h.nll,
                     h.lse_out);
@@ -520,8 +557,7 @@ cudaError_t launch_head_few_grad(const HeadArgs& h, int sms, cudaStream_t st) {
   const bool wide = vec && (!h.grad_head || on16(h.grad_head));
   const FewPlan p = few_plan(h.rows, h.d, h.vocab, sms, wide);
   const FewDev a = few_dev(h, p);
-  const cudaError_t e = h.f32 ? logits_rm<float, true>(a, p.rm, vec, p.ctas, st)
-                              : logits_rm<__nv_bfloat16, true>(a, p.rm, vec, p.ctas, st);
+  const cudaError_t e = logits_any<true>(h, a, p, st);
   if (e != cudaSuccess) return e;
   switch (p.rm) {
     case 4: return h.f32 ? grad_rm<float, 4>(a, p, wide, st) : grad_rm<__nv_bfloat16, 4>(a, p, wide, st);

@@ -182,7 +182,8 @@ HEAD_CASES = [
     (16, 589, 3001, F32, 0, 0, 0), (16, 120, 1030, BF16, 0.4, 1, 3), (3, 589, 1999, BF16, 0, 0, 0),
     (7, 4096, 700, F32, 0.2, 4, 0), (13, 4096, 515, F32, 0, 0, 0), (9, 8, 2, BF16, 0, 0, 0),
     (4, 1000, 5003, F32, 0, 0, 0), (12, 2048, 4099, BF16, 0.3, 0, 0), (2, 1, 70, F32, 0, 0, 0),
-    (17, 256, 900, F32, 0, 0, 0),
+    (17, 256, 900, F32, 0, 0, 0), (10, 3219, 1122, F32, 0.5, 0, 0), (16, 6401, 140, BF16, 0, 0, 0),
+    (13, 2834, 333, BF16, 0, 2, 0), (3, 2834, 333, BF16, 0, 0, 0),
     # one row of tiles
     (128, 320, 1500, BF16, 0.3, 0, 0), (100, 1024, 8200, BF16, 0, 8, 0),
 ]
