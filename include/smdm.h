@@ -361,7 +361,8 @@ typedef struct {
   long long ld_head;
 } smdm_head_shape;
 
-/* Workspace of smdm_head_loss (grad == 0) or smdm_head_loss_grad (grad != 0). */
+/* Workspace of smdm_head_loss (grad == 0) or smdm_head_loss_grad (grad != 0).  The two may share
+ * one of the larger size. */
 size_t smdm_head_loss_workspace_bytes(const smdm_head_shape* shape, int grad);
 
 /* Cross entropy of the LM head, without storing logits: with z_v = hidden_r . lm_head_v,

@@ -1346,7 +1346,7 @@ namespace {
 // Workspace of the training form's loss: the loss rows of the residual stream, their norm, and
 // what the head's loss (and the gradients) need.
 struct LossLayout {
-  size_t x, hid, rstd, ghid, head, head_bytes, norm, total;
+  size_t x, hid, rstd, ghid, head, norm, total;
 };
 
 LossLayout loss_layout(const smdm_config* c, int n_rows, bool grad) {
@@ -1362,14 +1362,13 @@ LossLayout loss_layout(const smdm_config* c, int n_rows, bool grad) {
   L.x = take(n_rows * d * 4);
   L.hid = take(n_rows * d * es);
   L.rstd = take((size_t)n_rows * 4);
-  L.head_bytes = head_workspace_bytes(n_rows, c->d_model, c->vocab, f32, false);
   if (grad) {
     L.ghid = take(n_rows * d * es);
     L.norm = take(rmsnorm_grad_bytes(n_rows, c->d_model));
-    L.head_bytes = std::max(L.head_bytes,
-                            head_workspace_bytes(n_rows, c->d_model, c->vocab, f32, true));
   }
-  L.head = take(L.head_bytes);
+  size_t head = head_workspace_bytes(n_rows, c->d_model, c->vocab, f32, false);
+  if (grad) head = std::max(head, head_workspace_bytes(n_rows, c->d_model, c->vocab, f32, true));
+  L.head = take(head);
   L.total = off;
   return L;
 }
@@ -1461,7 +1460,10 @@ smdm_status smdm_loss_stepcausal(smdm_handle* h, const int32_t* d_ids, const int
   na.grad_x = d_grad_x;
   na.grad_gain = d_grad_final_norm;
   na.ws = reinterpret_cast<float*>(ws + L.norm);
-  { Launch lg_(h, SMDM_K_NORM, st, 2); CK(launch_train_rmsnorm_grad(na, st)); }
+  {
+    Launch lg_(h, SMDM_K_NORM, st, rmsnorm_grad_launches(n_rows, d));
+    CK(launch_train_rmsnorm_grad(na, st));
+  }
   return SMDM_OK;
 }
 

@@ -40,9 +40,9 @@ SMDM_DEV void store_v(T* p, const float* v) {
   else *p = from_f<T>(v[0]);
 }
 
-// N elements in as few instructions as their bytes allow (16 each).
-// N elements as loaded, widened when they are used: a conversion next to its load would make the
-// thread wait for each load before it issues the next.
+// N elements as loaded, in as few instructions as their bytes allow (16 each),
+// widened when they are used: a conversion next to its load would make the thread wait for each
+// load before it issues the next.
 template <typename T, int N>
 struct Raw {
   static constexpr int kWords = N * (int)sizeof(T) / 4;
@@ -324,8 +324,9 @@ __global__ void __launch_bounds__(TH, 512 / TH) train_rms_grad_ring_kernel(RmsAr
   int st = 0, turn = 0;
   uint32_t phase = 0;
   for (int row = blockIdx.x; row < a.rows; row += gridDim.x, ++turn) {
-    const float r = a.rstd[row];
-    mbar_wait(&full[st], phase, abort_flag, nullptr);
+    float r = a.rstd[row];
+    // (rows that did not arrive give NaN, not what the stage held before)
+    if (!mbar_wait(&full[st], phase, abort_flag, nullptr)) r = __int_as_float(0x7fffffff);
     const uint8_t* p = ring + (size_t)st * q.stage_bytes;
     const X* x = reinterpret_cast<const X*>(p);
     const T* gy = reinterpret_cast<const T*>(p + q.gy_off);
@@ -375,6 +376,7 @@ __global__ void __launch_bounds__(TH, 512 / TH) train_rms_grad_ring_kernel(RmsAr
     }
     if (++st == q.stages) { st = 0; phase ^= 1; }
   }
+  if (*abort_flag) let_land();
   float* ws = a.ws + (size_t)blockIdx.x * a.d;
 #pragma unroll
   for (int u = 0; u < NU; ++u) {
@@ -955,6 +957,8 @@ cudaError_t launch_train_rmsnorm(const RmsArgs& a, cudaStream_t st) { return rms
 size_t rmsnorm_grad_bytes(int rows, int d) {
   return std::max<size_t>(256, up_to((size_t)norm_grad_ctas(rows, d) * d * 4, 256));
 }
+
+int rmsnorm_grad_launches(int rows, int d) { return norm_grad_ctas(rows, d) > 1 ? 2 : 1; }
 
 cudaError_t launch_train_rmsnorm_grad(const RmsArgs& a, cudaStream_t st) {
   int parts = 0;

@@ -41,6 +41,7 @@ constexpr int kMaxNormWidth = 8192;   // a row is held in the registers of 256 t
 
 cudaError_t launch_train_rmsnorm(const RmsArgs& a, cudaStream_t st);
 size_t rmsnorm_grad_bytes(int rows, int d);
+int rmsnorm_grad_launches(int rows, int d);   // kernels that the gradient launches
 cudaError_t launch_train_rmsnorm_grad(const RmsArgs& a, cudaStream_t st);
 cudaError_t launch_embed(const EmbedArgs& a, cudaStream_t st);
 size_t embed_grad_bytes(int rows, int d, int n_emb);

@@ -15,7 +15,7 @@
 // What bounds it and what it reaches (B200, other inputs on every pass):
 //   loss, 4096 rows, 4096 x 8192     185 us   1.48 PFLOP/s  (a plain bf16 product sustains 1.40,
 //                                             in bursts 1.67: tensor pipe and power)
-//   gradient, 3072 of them           455 us   1.36 PFLOP/s  likewise
+//   gradient, a quarter left out     455 us   1.36 PFLOP/s  likewise
 //   loss, 8 rows, 1024 x 32000       18.5 us  3.5 TB/s      reading 65 MB, and three launches' tails
 //   gradient, 128 rows, likewise     66 us    2.0 TB/s      shared memory (head_narrow_kernel)
 //   fp32 loss, 331 rows, 256 x 1001  12.3 us                latency of three kernels
@@ -47,8 +47,8 @@ constexpr int kStagingBytes = kEpiWarps * 4096;
 constexpr int kMaxStages = 8;
 constexpr int kSmemLimit = 227 * 1024;
 // D (and split weights) held at once.  Pieces that stay in L2 were slower, their kernels' tails
-// cost more than the traffic: 64 MB 437 us and 32 MB 487 us against 437 for 3072 rows of
-// 4096 x 8192, 420 and 482 against 378 for 2400 rows of 1024 x 32000.
+// cost more than the traffic: 64 MB 437 us and 32 MB 487 us against 437 for 4096 rows of
+// 4096 x 8192 with a quarter left out, 420 and 482 against 378 for 2400 rows of 1024 x 32000.
 constexpr size_t kPieceBytes = size_t(256) << 20;
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -511,13 +511,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (++stage == a.nstages) { stage = 0; phase ^= 1; }
         }
       }
-      if constexpr (CG == 2) {
-        // The pair's MMA completions arrive on these barriers from the first CTA: wait until
-        // every stage is released so that no arrival lands after this CTA has exited.
-        for (int s = 0; ok && s < a.nstages; ++s) {
-          if (!warp_wait(&empty[stage], phase ^ 1, abort_flag, a.status)) break;
-          if (++stage == a.nstages) { stage = 0; phase ^= 1; }
-        }
+      // The MMAs' completions arrive on these barriers, a pair's from the first CTA: wait until
+      // every stage is released so that no arrival lands after this CTA has exited.
+      for (int s = 0; ok && s < a.nstages; ++s) {
+        if (!warp_wait(&empty[stage], phase ^ 1, abort_flag, a.status)) break;
+        if (++stage == a.nstages) { stage = 0; phase ^= 1; }
       }
     }
   } else if (warp == 1) {
@@ -834,6 +832,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!kRegs && !empty_sum) release();
     }
   }
+  if (*abort_flag) let_land();
   tc_fence_before();
   __syncthreads();
   if constexpr (CG == 2) cluster_sync_all();
@@ -950,6 +949,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           tma_load_2d(W + j * 8192, &tm_w, &full[stage], c0 + j * 64, a.w_row0 + v, pol);
       }
       __syncwarp();
+      if (++stage == kNarrowStages) { stage = 0; phase ^= 1; }
+    }
+    // every stage released: the last products are done (also those of a dH that is not wanted)
+    for (int s = 0; s < kNarrowStages; ++s) {
+      if (!warp_wait(&empty[stage], phase ^ 1, abort_flag, a.status)) break;
       if (++stage == kNarrowStages) { stage = 0; phase ^= 1; }
     }
   } else if (warp == 1) {
@@ -1102,6 +1106,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   }
+  if (*abort_flag) let_land();
   tc_fence_before();
   __syncthreads();
   if (warp == 1) {

@@ -98,6 +98,12 @@ SMDM_DEV bool mbar_wait_sleep(uint64_t* bar, uint32_t parity, volatile int* abor
   }
 }
 
+// After a wait that gave up: a millisecond in which copies and products in flight land, before the
+// block gives its shared and tensor memory back.
+SMDM_DEV void let_land() {
+  for (int i = 0; i < 16; ++i) __nanosleep(64000);
+}
+
 // ------------------------------------------------------------------------------------------
 // TMA (tiled, no multicast)
 // ------------------------------------------------------------------------------------------

@@ -213,6 +213,64 @@ def test_head_gradient_in_several_pieces(dt, rows, vocab):
     x.check_grad(lse)
 
 
+@pytest.mark.parametrize("many", [300, 40])
+def test_head_rows_of_equal_weight(many):
+    """More rows share the largest weight than keep their remainders, or fewer."""
+    x = Head(300, 128, 700, BF16, 0.1, seed=31)
+    x.weight.fill_(1 / 300)
+    x.weight[many:] /= 64
+    _, lse = x.check_loss()
+    x.check_grad(lse)
+
+
+@pytest.mark.parametrize("rows", [40, 200])
+def test_head_weights_past_32_bit_offsets(rows):
+    """More than 2^31 weights, their gradient too; against the definition, 20000 ids at a time."""
+    d, v, step = 4096, 540000, 20000
+    g = gen(rows)
+    w = torch.empty((v, d), dtype=BF16, device="cuda").normal_(0, 0.02, generator=g)
+    h = rand(g, rows, d).to(BF16)
+    target = torch.randint(0, v, (rows,), generator=g, device="cuda").int()
+    target[:2] = torch.tensor([v - 1, 0])
+    weight = (torch.rand(rows, generator=g, device="cuda") + 0.1) / rows
+    ws = workspace(max(smdm.smdm_head_loss_workspace_bytes(rows, d, v, BF16, grad=b)
+                       for b in (False, True)))
+    nll, lse = (torch.full((rows,), float("nan"), device="cuda") for _ in range(2))
+    smdm.smdm_head_loss(h, w, target, nll, lse, ws)
+    gh, gw = torch.full_like(h, float("nan")), torch.empty_like(w)
+    smdm.smdm_head_loss_grad(h, w, target, lse, weight, gh, gw, ws)
+    hd, wt, l64 = h.to(f64), weight.to(f64)[:, None], lse.to(f64)[:, None]
+    per = (d / 16 + 17) * 2.0 ** -23
+    parts, dz = [], torch.zeros((rows, 1), dtype=f64, device="cuda")
+    sums = [torch.zeros((rows, d), dtype=f64, device="cuda") for _ in range(4)]
+    for a in range(0, v, step):
+        c = w[a:a + step].to(f64)
+        z = hd @ c.T
+        dz = torch.maximum(dz, per * (hd.abs() @ c.abs().T).max(dim=1, keepdim=True).values)
+        parts.append(torch.logsumexp(z, dim=1))
+        p = torch.exp(z - l64)
+        D = p * wt
+        t = target.long() - a
+        on = (t >= 0) & (t < len(c))
+        D[on.nonzero()[:, 0], t[on]] -= wt[on, 0]
+        for s, m in zip(sums, (D @ c, (D * D) @ (c * c), D.abs() @ c.abs(), (p * wt) @ c.abs())):
+            s += m
+    rlse = torch.logsumexp(torch.stack(parts), dim=0)
+    dz = dz + 2.0 ** -20
+    within(lse, rlse, dz[:, 0] + 2.0 ** -23 * rlse.abs(), "lse")
+    # (as Head.check_grad)
+    u = 2.0 ** -8 if rows > 128 else 2.0 ** -16
+    ref, q, mag, sp = sums
+    bound = dz * sp + 6 * u * (q / 3).sqrt() + (2 * v / 16 + 17) * 2.0 ** -23 * mag
+    within(gh, ref, bound + u_of(BF16) * (ref.abs() + bound) + 1e-37, "grad_hidden")
+    D, p = D[:, -64:], p[:, -64:]              # the last ids
+    ref = D.T @ hd
+    bound = (p * wt * dz).T @ hd.abs() + 6 * u * ((D * D).T @ (hd * hd) / 3).sqrt() + \
+        (2 * rows / 16 + 17) * 2.0 ** -23 * (D.abs().T @ hd.abs())
+    within(gw[-64:], ref, bound + u_of(BF16) * (ref.abs() + bound) + 1e-37, "grad_lm_head")
+    assert torch.isfinite(gw[::997]).all()
+
+
 @pytest.mark.parametrize("rows,d,dt", [(200, 128, BF16), (100, 64, BF16), (14, 128, BF16),
                                        (14, 30, F32), (150, 30, F32)])
 def test_head_rows_without_a_target_reach_nothing(rows, d, dt):
@@ -456,6 +514,70 @@ def test_embedding_ids_beyond_the_table_and_no_rows():
     smdm.smdm_embed(none, table, e)
     smdm.smdm_embed_grad(none, e, gt, ws)
     assert (gt == 0).all()
+
+
+@pytest.mark.parametrize("dt", [BF16, F32])
+def test_row_strides_past_32_bit_offsets(dt):
+    """Rows 2^26 elements apart: the last ones lie past 2^31.  The same bits as rows together."""
+    n, d, ld = 36, 128, 1 << 26
+    g = gen(40)
+    buf = torch.empty((n - 1) * ld + 4 * d, dtype=dt, device="cuda")
+    near = [rand(g, n, d).to(dt) for _ in range(3)]
+    near[1] *= 0.1
+    far = [buf[i * d:].as_strided((n, d), (ld, 1)) for i in range(4)]
+    for f, t in zip(far, near):
+        f.copy_(t)
+    x, w, y = near
+    fx, fw, fy, fo = far
+    target = torch.arange(n, device="cuda").int()
+    target[5] = -1
+    weight = torch.rand(n, generator=g, device="cuda")
+    gain = rand(g, d).to(dt)
+    ws = workspace(max(smdm.smdm_head_loss_workspace_bytes(n, d, n, dt),
+                       smdm.smdm_head_loss_workspace_bytes(n, d, n, dt, grad=True),
+                       smdm.smdm_head_loss_workspace_bytes(9, d, n, dt),
+                       smdm.smdm_head_loss_workspace_bytes(9, d, n, dt, grad=True),
+                       smdm.smdm_rmsnorm_grad_workspace_bytes(n, d),
+                       smdm.smdm_embed_grad_workspace_bytes(n, d, n)))
+
+    def run(x, w, y, out, rows):
+        r = [torch.full((n,), float("nan"), device="cuda") for _ in range(3)]
+        m = [torch.full((n, d), float("nan"), dtype=dt, device="cuda") for _ in range(5)]
+        gg = torch.empty_like(gain)
+        smdm.smdm_head_loss(x[:rows], w, target[:rows], r[0][:rows], r[1][:rows], ws)
+        smdm.smdm_head_loss_grad(x[:rows], w, target[:rows], r[1][:rows], weight[:rows], m[0][:rows],
+                                 m[1], ws)
+        smdm.smdm_rmsnorm(x, gain, out, r[2])
+        smdm.smdm_rmsnorm_grad(x, gain, r[2], y, m[2], gg, ws)
+        smdm.smdm_embed(target, w, m[3])
+        smdm.smdm_embed_grad(target, y, m[4], ws)
+        return [t[:rows] for t in r[:2]] + [m[0][:rows], r[2], *m[1:], gg, out]
+
+    for rows in (n, 9):
+        a = run(x, w, y, torch.empty_like(x), rows)
+        b = run(fx, fw, fy, fo, rows)
+        for i, (s, t) in enumerate(zip(a, b)):
+            assert torch.equal(s, t), i
+            assert torch.isfinite(s.float()).all(), i
+
+
+def test_embedding_past_32_bit_offsets():
+    n, d = 40000, 65536
+    g = gen(41)
+    table = rand(g, 50, d).to(BF16)
+    ids = torch.randint(0, 50, (n,), generator=g, device="cuda").int()
+    out = torch.empty((n, d), dtype=BF16, device="cuda")
+    smdm.smdm_embed(ids, table, out)
+    for a in range(0, n, 5000):
+        assert torch.equal(out[a:a + 5000], table[ids[a:a + 5000].long()])
+    rows = torch.tensor([0, n - 1, 17, n - 1, 32769, n - 2], dtype=torch.int32, device="cuda")
+    go = rand(g, 6, d).to(BF16)
+    out.fill_(float("nan"))
+    smdm.smdm_embed_grad(rows, go, out, workspace(smdm.smdm_embed_grad_workspace_bytes(6, d, n)))
+    twice = (go[1].float() + go[3].float()).to(BF16)      # one fp32 addition, rounded once
+    for row, want in ((0, go[0]), (17, go[2]), (32769, go[4]), (n - 2, go[5]), (n - 1, twice)):
+        assert torch.equal(out[row], want), row
+    assert sum(int(out[a:a + 5000].any(dim=1).sum()) for a in range(0, n, 5000)) == 5
 
 
 # ------------------------------------------------------------------------------------------------
