@@ -16,8 +16,8 @@
 //   loss, 4096 rows, 4096 x 8192     185 us   1.48 PFLOP/s  (a plain bf16 product sustains 1.40,
 //                                             in bursts 1.67: tensor pipe and power)
 //   gradient, a quarter left out     455 us   1.36 PFLOP/s  likewise
-//   loss, 8 rows, 1024 x 32000       18.5 us  3.5 TB/s      reading 65 MB, and three launches' tails
-//   gradient, 128 rows, likewise     66 us    2.0 TB/s      shared memory (head_narrow_kernel)
+//   loss, 8 rows, 1024 x 32000       18.3 us  3.6 TB/s      reading 65 MB (a bare read: 14), two tails
+//   gradient, 128 rows, likewise     62 us    2.1 TB/s      see head_narrow_kernel
 //   fp32 loss, 331 rows, 256 x 1001  12.3 us                latency of three kernels
 //
 // One kernel does all products (`head_gemm_kernel`): persistent CTAs (or pairs, cta_group::2),
@@ -73,6 +73,11 @@ struct HeadDev {
   int h_plane, w_plane, d_plane;   // rows between the parts of H, W, D in their maps
   int a_box;                // rows of A that one box brings (K-major H)
   int nstages, staging_off, bar_off;
+  // With one row of tiles every slot starts at another place of K where the weight rows lie a
+  // multiple of 2 KB apart: all slots at the same place of such rows keep to few of HBM's channels.
+  // Loss of 8 / 128 rows of 1024 x 32000 19.0 -> 18.3, 20.1 -> 18.8 us, 100 rows of 4096 x 8192
+  // 23.2 -> 20.3; rows of 1 or 3 KB are no faster for it (13.4 -> 13.8, 19.4 -> 19.7).
+  int spread;
   // loss
   float2* part;             // [column group][r_pad]
   int part0;                // first column group of this piece
@@ -456,6 +461,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int i = 0; ok && sch.get(a, i, u); ++i) {
         const int m0 = u.m0 + (int)rank * 128;
         const int n0 = u.n0 + (int)rank * kBRows;
+        int kx = 0, span = 0;              // loss and D: where this slot is in K, and K's end
+        if constexpr (kMode != kGrad) {
+          span = (u.nk + KS - 1) / KS * KS;
+          if (a.spread && sch.mt == 1) kx = (int)(blockIdx.x / CG) * KS % span;
+        }
         for (int k = u.k0; k < u.k0 + u.nk; k += KS) {
           if (!warp_wait(&empty[stage], phase ^ 1, abort_flag, a.status)) { ok = false; break; }
           uint8_t* A = smem + stage * kStage;
@@ -476,7 +486,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // (a chunk past the row's end arrives as zeros)
 #pragma unroll
                 for (int s = 0; s < KS; ++s)
-                  load(A + (s * kAParts<P> + p) * kABytes, th, (k + s) * 64, p * h_plane + m0);
+                  load(A + (s * kAParts<P> + p) * kABytes, th, (kx + s) * 64, p * h_plane + m0);
               } else if (u.kind == 1) {   // dH: D (K = columns, contiguous)
                 load(A + p * kABytes, &tm_dk, k * 64, p * a.d_plane + m0);
               } else {                    // dW: D (M contiguous)
@@ -494,7 +504,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               if constexpr (kMode != kGrad) {
 #pragma unroll
                 for (int s = 0; s < KS; ++s)
-                  load(B + (s * kBParts<P> + p) * kBPart, &tm_w, (k + s) * 64,
+                  load(B + (s * kBParts<P> + p) * kBPart, &tm_w, (kx + s) * 64,
                        a.w_row0 + p * a.w_plane + n0);
               } else {                    // dH: W, dW: H (N contiguous)
                 const bool lo = u.kind == 2 && k >= u.k1;
@@ -508,6 +518,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
           __syncwarp();
+          if constexpr (kMode != kGrad) kx = kx + KS == span ? 0 : kx + KS;
           if (++stage == a.nstages) { stage = 0; phase ^= 1; }
         }
       }
@@ -857,17 +868,35 @@ __global__ void __launch_bounds__(kThreads, 1)
 //   dW^T [128 c][64 v]  = H^T [128 c][r] D [r][64 v]
 //
 // dW comes out transposed (a lane per column), so that 64 vocabulary rows are enough for an
-// M = 128 product; the epilogue turns it around in shared memory.  What bounds the loop is shared
-// memory's 128 bytes per clock: an MMA of N columns reads 4 KB of A and 32 N bytes of B.  H^T
-// therefore goes to tensor memory once and is dW's A operand from there.
+// M = 128 product; the epilogue turns it around by an exchange between neighbouring lanes and
+// through shared memory (without the exchange, two bytes of a lane at a time, 5 us more).  What
+// bounds the loop: loads alone take 20 us, the writes of dW 7, the products 5 that do not
+// overlap.  An MMA of N columns reads 4 KB of A and 32 N bytes of B from shared memory, 128 bytes
+// per clock; H^T therefore goes to tensor memory once and is dW's A operand from there.
 //
-// With 1024 x 32000 weights, other weights on every pass: 128 rows 66 us, 8 rows 56 us for the whole
-// gradient; 79 and 84 us with head_gemm_kernel's tiles, 75 with H^T in shared memory.
+// With 1024 x 32000 weights, other weights on every pass: 128 rows 62 us, 8 rows 56 us for the whole
+// gradient, 34 and 32 of them here; 79 and 84 us with head_gemm_kernel's tiles.  With H^T in shared
+// memory 9 us more; a deeper ring of stages changed nothing.
 constexpr int kNarrowD = 2 * 128 * 128;         // a stage: D, two parts of [128 r][64 v]
 constexpr int kNarrowW = 2 * 64 * 128;          // and W, two runs of 64 columns [64 v][64 c]
 constexpr int kNarrowStage = kNarrowD + kNarrowW;
 constexpr int kNarrowStages = 3;
 constexpr int kNarrowH = 2 * 128 * 128;         // H: two runs of 64 columns [128 r][64 c]
+
+// Lane l holds 32 values of column l; afterwards, rounded to bf16, columns l & ~1 and l | 1 of the
+// values 2 k + l % 2 in a[k].
+SMDM_DEV void pair_columns(const float* v, int lane, uint32_t* a) {
+  const bool odd = lane & 1;
+  const uint32_t lo = odd ? 0x1054 : 0x5410, hi = odd ? 0x3276 : 0x7632;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {              // values 4 k and 4 k + 2, or 4 k + 1 and 4 k + 3
+    const uint32_t e = pack_bf16(v[4 * k], v[4 * k + 2]), o = pack_bf16(v[4 * k + 1], v[4 * k + 3]);
+    const uint32_t mine = odd ? o : e;
+    const uint32_t other = __shfl_xor_sync(0xffffffffu, odd ? e : o, 1);
+    a[2 * k] = __byte_perm(mine, other, lo);
+    a[2 * k + 1] = __byte_perm(mine, other, hi);
+  }
+}
 
 __global__ void __launch_bounds__(kThreads, 1)
     head_narrow_kernel(const __grid_constant__ CUtensorMap tm_h,    // box {64, 64}
@@ -1036,15 +1065,19 @@ __global__ void __launch_bounds__(kThreads, 1)
       acc ^= 1;
       if (acc == 0) acc_phase ^= 1;
       if (!a.do_w) continue;
-      __nv_bfloat16* t = reinterpret_cast<__nv_bfloat16*>(st);   // [32 v][32 c]
+      // [32 v][32 c]: a store writes two rows, a word of every bank
+      uint32_t* t = reinterpret_cast<uint32_t*>(st);
+      uint32_t x[16];
+      pair_columns(v, lane, x);
 #pragma unroll
-      for (int j = 0; j < 32; ++j) t[j * 32 + lane] = __float2bfloat16_rn(v[j]);
+      for (int k = 0; k < 16; ++k) t[(2 * k + (lane & 1)) * 16 + (lane >> 1)] = x[k];
       __syncwarp();
       const int v0 = (slot + i * slots) * 64 + half * 32, c = c0 + q * 32 + (lane & 3) * 8;
       uint4 w[4];
 #pragma unroll
       for (int k = 0; k < 4; ++k)
-        w[k] = *reinterpret_cast<const uint4*>(t + (k * 8 + (lane >> 2)) * 32 + (lane & 3) * 8);
+        w[k] = *reinterpret_cast<const uint4*>(t + (k * 8 + (lane >> 2)) * 16 + (lane & 3) * 4);
+      __syncwarp();
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         const int r = v0 + k * 8 + (lane >> 2);
@@ -1058,7 +1091,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (c + x < a.d) dst[x] = e[x];
         }
       }
-      __syncwarp();
     }
     if (a.do_w && n == 0) {
       // no row takes part: zeros
@@ -1894,6 +1926,7 @@ struct Call {
     a.v0 = v0;
     a.vc = vc;
     a.w_row0 = p.staged ? 0 : v0;
+    a.spread = (p.staged ? p.d_pad : h.ld_head) * 2 % 2048 == 0;
     a.terms = p.terms;
     a.h_plane = p.r_pad;
     a.w_plane = p.staged ? (int)up(vc, 256) : 0;
