@@ -13,10 +13,10 @@
 // of a padded batch) reaches no sum.  When every row takes part the rows are read in place.
 //
 // What bounds it and what it reaches (B200, other inputs on every pass):
-//   loss, 4096 rows, 4096 x 8192     185 us   1.48 PFLOP/s  (a plain bf16 product sustains 1.40,
+//   loss, 4096 rows, 4096 x 8192     187 us   1.47 PFLOP/s  (a plain bf16 product sustains 1.40,
 //                                             in bursts 1.67: tensor pipe and power)
-//   gradient, a quarter left out     455 us   1.36 PFLOP/s  likewise
-//   loss, 8 rows, 1024 x 32000       18.3 us  3.6 TB/s      reading 65 MB (a bare read: 14), two tails
+//   gradient, a quarter left out     460 us   1.34 PFLOP/s  likewise
+//   loss, 8 rows, 1024 x 32000       18.6 us  3.5 TB/s      reading 65 MB (a bare read: 14), two tails
 //   gradient, 128 rows, likewise     62 us    2.1 TB/s      see head_narrow_kernel
 //   fp32 loss, 331 rows, 256 x 1001  12.3 us                latency of three kernels
 //
