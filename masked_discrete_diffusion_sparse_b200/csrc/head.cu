@@ -136,15 +136,19 @@ template <int P> __host__ __device__ constexpr int part_b(int t) {
   return P == 3 ? (0x201100 >> (4 * (5 - t))) & 15 : 0;
 }
 
-// The tensor core cuts its fp32 sums instead of rounding them: measured, every 16-term step takes
-// 2^-26 of the sum's value off (1.0e-6 at K = 1024, 4.0e-6 at 4096).  Where the result is fp32
-// (the loss, and everything of the fp32 path) the tensor core therefore sums kSegment chunks at a
-// time, 24 to 32 steps, and the epilogue threads add the segments in registers, rounded to
-// nearest.  Where the result is rounded to bf16 next, the cut does not matter and K is summed
-// whole.
-template <int P> constexpr int kSegment = P == 3 ? 1 : 8;
-template <int kMode, int P>
-constexpr bool kPromote = P == 3 || kMode == kLoss;
+// The tensor core cuts its fp32 sums instead of rounding them, always towards zero.  Measured on sums
+// of one sign, every 16-term step takes 1e-8 (terms of like size) to 1e-7 of the final value off:
+// 1.6e-3 over 2^18 rows, as much as bf16's rounding.  It therefore sums kSegment chunks at a
+// time, and the epilogue threads add the segments in registers, rounded to nearest: 24 or 32 steps
+// where the result is fp32 (the loss, and everything of the fp32 path).  The bf16 gradients are
+// rounded to 8 bits next; their segments are kWholeK chunks (512 steps, 5e-5 of the value at most,
+// 1/40 of that rounding), and K ranges up to that long are summed whole, by a kernel of its own:
+// the registers for the sums cost up to 10 % (200 rows of 1024 x 32000: 92.7 -> 101 us).  D's
+// product is summed whole.
+constexpr int kWholeK = 128;
+template <int kMode, int P> constexpr int kSegment = P == 3 ? 1 : kMode == kGrad ? kWholeK : 8;
+template <int kMode, int P, bool kLong>
+constexpr bool kPromote = P == 3 || kMode == kLoss || kLong;
 
 // 64-wide K chunks per pipeline stage.  Waiting for a stage and releasing it takes the issuing
 // warp about 300 clocks, as much as the MMAs of a narrow tile, so those take two at a time.
@@ -379,8 +383,8 @@ SMDM_DEV void add_target(const HeadDev& a, int tgt, float delta, int col, float*
 }
 
 // kMode: what is computed.  CG: CTAs per tile (2: a pair on two SMs, M = 256).  BN: tile
-// columns.  P: operand parts; 3 is the fp32 path.
-template <int kMode, int CG, int BN, int P>
+// columns.  P: operand parts; 3 is the fp32 path.  kLong: K in segments (kWholeK).
+template <int kMode, int CG, int BN, int P, bool kLong>
 __global__ void __launch_bounds__(kThreads, 1)
     head_gemm_kernel(const __grid_constant__ CUtensorMap tm_h,    // caller's hidden (K-major box)
                      const __grid_constant__ CUtensorMap tm_hc,   // listed rows, or same box
@@ -545,7 +549,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t a_step = a_mn ? 2048 >> 4 : 32 >> 4, b_step = b_mn ? 2048 >> 4 : 32 >> 4;
         // (no chunks at all: nothing to sum, the epilogue writes zeros)
         for (int c0 = 0; ok && c0 < total;) {
-          const int c1 = kPromote<kMode, P> ? min(total, c0 + kSegment<P> / KS) : total;
+          const int c1 = kPromote<kMode, P, kLong> ? min(total, c0 + kSegment<kMode, P> / KS) : total;
           if (!warp_wait(&acc_empty[acc], acc_phase ^ 1, abort_flag, a.status)) { ok = false; break; }
           tc_fence_after();
           const uint32_t d = tbase + acc * BN;
@@ -641,13 +645,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (acc == 0) acc_phase ^= 1;
       };
       // Promoted sums: this thread's HC columns live in registers once the last segment is in.
-      constexpr bool kRegs = kPromote<kMode, P>;
+      constexpr bool kRegs = kPromote<kMode, P, kLong>;
       constexpr int NB = HC / 32;
       float sum[kRegs ? HC : 1];
       if constexpr (kRegs) {
 #pragma unroll
         for (int j = 0; j < HC; ++j) sum[j] = 0.f;
-        for (int c0 = 0; c0 < u.nk; c0 += kSegment<P>) {   // (chunks; a stage never splits)
+        for (int c0 = 0; c0 < u.nk; c0 += kSegment<kMode, P>) {   // (chunks; a stage never splits)
           acquire();
 #pragma unroll
           for (int c = 0; c < NB; ++c) {
@@ -881,6 +885,7 @@ constexpr int kNarrowD = 2 * 128 * 128;         // a stage: D, two parts of [128
 constexpr int kNarrowW = 2 * 64 * 128;          // and W, two runs of 64 columns [64 v][64 c]
 constexpr int kNarrowStage = kNarrowD + kNarrowW;
 constexpr int kNarrowStages = 3;
+constexpr int kNarrowBlocks = 256;              // of 8 steps each: 2e-4 at most (see kWholeK)
 constexpr int kNarrowH = 2 * 128 * 128;         // H: two runs of 64 columns [128 r][64 c]
 
 // Lane l holds 32 values of column l; afterwards, rounded to bf16, columns l & ~1 and l | 1 of the
@@ -1621,6 +1626,9 @@ int pick_cfg(long long m, long long n, int sms, int parts) {
   return best;
 }
 
+// Vocabulary slots of head_narrow_kernel: one column group per CTA, a CTA per SM.
+int narrow_slots(int d, int sms) { return std::max(1, sms / ((d + 127) / 128)); }
+
 Plan make_plan(int rows, int d, int vocab, long long ld_head, bool f32, bool grad) {
   Plan p{};
   const int sms = sm_count();
@@ -1644,6 +1652,9 @@ Plan make_plan(int rows, int d, int vocab, long long ld_head, bool f32, bool gra
   const int v_pad = (int)up(vocab, 256);
   p.piece = v_pad;
   if (per_col) p.piece = (int)std::min<size_t>(v_pad, std::max<size_t>(256, kPieceBytes / per_col / 256 * 256));
+  // one row tile: no slot of head_narrow_kernel sums more than kNarrowBlocks blocks into its dH
+  if (grad && !f32 && rows <= 128)
+    p.piece = (int)std::min<long long>(p.piece, (long long)narrow_slots(d, sms) * kNarrowBlocks * 64 / 256 * 256);
   p.n_pieces = (vocab + p.piece - 1) / p.piece;
   // pieces of equal width
   p.piece = (int)up((vocab + p.n_pieces - 1) / p.n_pieces, 256);
@@ -1670,8 +1681,7 @@ Plan make_plan(int rows, int d, int vocab, long long ld_head, bool f32, bool gra
     }
     // one row tile: a column group per CTA, as many vocabulary slots as fill the SMs
     if (!f32 && rows <= 128) {
-      const int groups = (d + 127) / 128;
-      p.narrow = (int)std::min<long long>(std::max(1, sms / groups), kh);
+      p.narrow = (int)std::min<long long>(narrow_slots(d, sms), kh);
       p.splits = p.narrow;
       p.cfg = 0;
     }
@@ -1743,7 +1753,7 @@ int max_pairs(K kern, int smem) {
   return n;
 }
 
-template <int kMode, int CG, int BN, int P>
+template <int kMode, int CG, int BN, int P, bool kLong = false>
 cudaError_t launch_one(const Maps& m, HeadDev a, long long units, int sms, cudaStream_t st) {
   constexpr int kStage = kChunks<kMode, CG, BN, P> *
                          (kAParts<P> * kABytes + kBParts<P> * (BN / CG * 128));
@@ -1752,7 +1762,7 @@ cudaError_t launch_one(const Maps& m, HeadDev a, long long units, int sms, cudaS
   a.staging_off = a.nstages * kStage;
   a.bar_off = a.staging_off + kStagingBytes;
   const int smem = a.bar_off + 512 + 1024;
-  auto kern = head_gemm_kernel<kMode, CG, BN, P>;
+  auto kern = head_gemm_kernel<kMode, CG, BN, P, kLong>;
   // per device: the shared-memory opt-in and the number of pairs that fit
   static int ready[64];
   int dev = 0;
@@ -1775,16 +1785,16 @@ cudaError_t launch_one(const Maps& m, HeadDev a, long long units, int sms, cudaS
                     m.hc, m.w, m.dk, m.dm, m.dl, m.hl, a);
 }
 
-template <int kMode, int P>
+template <int kMode, int P, bool kLong = false>
 cudaError_t launch_cfg(int cfg, const Maps& m, const HeadDev& a, long long units, int sms,
                        cudaStream_t st) {
   switch (cfg) {
-    case 0: return launch_one<kMode, 1, 64, P>(m, a, units, sms, st);
-    case 1: return launch_one<kMode, 1, 128, P>(m, a, units, sms, st);
+    case 0: return launch_one<kMode, 1, 64, P, kLong>(m, a, units, sms, st);
+    case 1: return launch_one<kMode, 1, 128, P, kLong>(m, a, units, sms, st);
     case 2:
       if constexpr (kMode != kGrad && P == 1) return launch_one<kMode, 1, 256, P>(m, a, units, sms, st);
       break;
-    case 3: return launch_one<kMode, 2, 256, P>(m, a, units, sms, st);
+    case 3: return launch_one<kMode, 2, 256, P, kLong>(m, a, units, sms, st);
   }
   return cudaErrorInvalidValue;
 }
@@ -1793,6 +1803,11 @@ template <int kMode>
 cudaError_t launch_mode(int parts, int cfg, const Maps& m, const HeadDev& a, long long units,
                         int sms, cudaStream_t st) {
   if (parts == 3) return launch_cfg<kMode, 3>(cfg, m, a, units, sms, st);
+  if constexpr (kMode == kGrad) {
+    const long long rows = a.do_w ? a.rows : 0, ids = a.do_h ? (a.vc + a.splits - 1) / a.splits : 0;
+    if (std::max(rows, ids) > 64 * kWholeK)
+      return launch_cfg<kMode, 1, true>(cfg, m, a, units, sms, st);
+  }
   return launch_cfg<kMode, 1>(cfg, m, a, units, sms, st);
 }
 
