@@ -26,7 +26,8 @@
 // operands differ in their boxes and descriptors only, so D and W are multiplied as they lie.
 //
 // bf16: products of the given values, fp32 sums.  D is rounded to bf16 (half a step, 2^-8
-// relative to each of its values); kHeavyRows below says what becomes of the remainders.
+// relative to each of its values); "What rounding D to bf16 costs" below says what becomes of the
+// remainders.
 // fp32: every operand is split into three bf16 parts (8 + 8 + 8 significant bits) and the six
 // products that reach 2^-16 of the largest are summed, smallest first (2^-23 is left out).
 #include "head.h"
@@ -58,7 +59,6 @@ enum Mode : int { kLoss = 0, kDlog = 1, kGrad = 2 };
 struct HeadMeta {
   int n;       // rows that take part
   int dense;   // 1: all of them do, and the caller's hidden is read in place
-  int heavy;   // rows whose D keeps its rounding's remainder for dW (see kHeavyRows)
 };
 
 struct HeadDev {
@@ -84,9 +84,14 @@ struct HeadDev {
   int r_pad;
   float* tlogit;            // [r_pad]
   // D
-  const int* slot;          // listed row -> its row of d_lo, or -1; null: no such rows
-  __nv_bfloat16* d_lo;      // [kHeavyRows][ld_dlog]
-  float* delta;             // [r_pad] remainder of D at the row's target
+  const int* row_tgt;       // [r_pad] targets of the listed rows
+  float* delta;             // [r_pad] remainder of D at the row's target; null: not kept
+  int2* ids;                // [vocab] a listed row with the id as its target, and their number
+  int* next;                // [r_pad] the next listed row with the same target
+  const __nv_bfloat16* rest;   // [r_pad][d_pad] sums of the remainders' part of dW (see RestArgs)
+  const void* hidden;       // the caller's rows
+  long long ld_hidden;
+  const __nv_bfloat16* hid; // the listed rows
   const void* head;         // the caller's weights
   long long ld_head;
   int head_vec;             // they start on 16-byte boundaries
@@ -115,7 +120,6 @@ struct Unit {
   int kind;      // 0: H x W^T (loss, D); 1: dH; 2: dW
   int m0, n0;    // first row / column
   int k0, nk;    // first 64-wide K chunk, chunks
-  int k1;        // dW: chunks from here on are the heavy rows' remainders
   int split;
 };
 
@@ -155,17 +159,16 @@ constexpr bool kPromote = P == 3 || kMode == kLoss || kLong;
 template <int kMode, int CG, int BN, int P>
 constexpr int kChunks = kMode != kGrad && P == 1 && CG == 1 && BN <= 128 ? 2 : 1;
 
-// What rounding D to bf16 costs, and what is done about it.  Alone it adds an error as large as the
-// gradients' own rounding (2.4e-3 of their norm against 1.7e-3), and up to 1.7 times that where a
-// few rows with large weights make up the norm.
-//  - A row's largest entry is its target's (it is minus the sum of the others).  Its remainder
-//    times the target's weights is added to dH in the epilogue, in fp32: dH's error falls back
-//    to its own rounding's, for every row.
-//  - For dW the heaviest rows (up to kHeavyRows, by |grad_nll|) keep their remainders as rows of a
-//    second, small matrix that is multiplied with copies of their hidden rows: two more K
-//    chunks per dW tile.
-//  - One row tile (head_narrow_kernel) keeps all remainders.
-constexpr int kHeavyRows = 128;
+// What rounding D to bf16 costs, and what is done about it.  Alone it makes dW's error 1.4 times its
+// own rounding's, and dH's up to 1.7 times where a few rows with large weights make up the norm.
+// A row's largest entry is its target's (it is minus the sum of the others), so its remainder
+// delta_r is kept in fp32, and added to
+//   row r of dH     delta_r times the weights of r's target,
+//   row v of dW     the sum of delta_r h_r over the rows r whose target is v (head_rest_kernel),
+// by the epilogues before they round: both errors fall back to the output's own rounding, whatever
+// the rows' weights.  (A row that is certain of another id has a second entry as large, which is
+// rounded: up to 1.2 times in its row of dH, 1.4 times in that id's row of dW.)
+// One row tile (head_narrow_kernel) keeps the remainders of all entries.
 
 // The work of one slot (CTA or pair) p of P.  Loss and D: tiles round robin, in groups of 16 row
 // tiles so that a group's rows stay in L2 while the weights pass once.  Gradients: the dH units
@@ -174,10 +177,10 @@ constexpr int kHeavyRows = 128;
 template <int kMode, int CG, int BN>
 struct Schedule {
   int p, P, n, kc, mt, nt;
-  int kw, kx, nh, nw, mt_w, nt_d, my_h, qa, my_w, n_rem;
+  int kw, nh, nw, mt_w, nt_d, my_h, qa, my_w, n_rem;
   int kch, kper;
 
-  SMDM_DEV Schedule(const HeadDev& a, int n_, int heavy, int p_, int P_) : p(p_), P(P_), n(n_) {
+  SMDM_DEV Schedule(const HeadDev& a, int n_, int p_, int P_) : p(p_), P(P_), n(n_) {
     constexpr int MT = 128 * CG;
     mt = (n + MT - 1) / MT;
     if constexpr (kMode != kGrad) {
@@ -188,7 +191,6 @@ struct Schedule {
       kch = (a.vc + 63) >> 6;
       kper = (kch + a.splits - 1) / a.splits;
       kw = (n + 63) >> 6;
-      kx = (heavy + 63) >> 6;
       mt_w = (a.vc + MT - 1) / MT;
       nh = a.do_h ? mt * nt_d * a.splits : 0;
       nw = a.do_w ? mt_w * nt_d : 0;
@@ -197,7 +199,7 @@ struct Schedule {
       my_h = c + (p < n_rem ? 1 : 0);
       // finishing time T of all slots, raised from the mean until every dW tile fits.  In fp32:
       // every thread of the grid computes the same values, and rounding only moves the balance.
-      const float ch = (float)kper * a.terms + kTileCost, cw = (float)(kw + kx) * a.terms + kTileCost;
+      const float ch = (float)kper * a.terms + kTileCost, cw = (float)kw * a.terms + kTileCost;
       auto fit = [&](float T, float used) {
         return T > used ? (int)fminf(__fdividef(T - used, cw), (float)nw) : 0;
       };
@@ -258,8 +260,7 @@ struct Schedule {
       u.m0 = (q / nt_d) * MT;
       u.n0 = (q % nt_d) * BN;
       u.k0 = 0;
-      u.nk = kw + kx;
-      u.k1 = kw;
+      u.nk = kw;
       return true;
     }
   }
@@ -361,24 +362,24 @@ SMDM_DEV void stage_f32(uint8_t* st, int lane, const float* v) {
         make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
 }
 
-// 32 columns of a row of dH: plus the remainder of D at the row's target times the target's weights.
-SMDM_DEV void add_target(const HeadDev& a, int tgt, float delta, int col, float* v) {
-  const __nv_bfloat16* w = static_cast<const __nv_bfloat16*>(a.head) + (size_t)tgt * a.ld_head + col;
-  if (a.head_vec && col + 32 <= a.d) {
+// 32 columns of a row of a gradient: plus f times the row w of the other operand.
+SMDM_DEV void add_row(const __nv_bfloat16* w, bool vec, float f, int col, int d, float* v) {
+  w += col;
+  if (vec && col + 32 <= d) {
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       const uint4 u = *reinterpret_cast<const uint4*>(w + 8 * k);
       const uint32_t x[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        v[8 * k + 2 * j] = fmaf(delta, __uint_as_float(x[j] << 16), v[8 * k + 2 * j]);
-        v[8 * k + 2 * j + 1] = fmaf(delta, __uint_as_float(x[j] & 0xffff0000u), v[8 * k + 2 * j + 1]);
+        v[8 * k + 2 * j] = fmaf(f, __uint_as_float(x[j] << 16), v[8 * k + 2 * j]);
+        v[8 * k + 2 * j + 1] = fmaf(f, __uint_as_float(x[j] & 0xffff0000u), v[8 * k + 2 * j + 1]);
       }
     }
   } else {
 #pragma unroll
     for (int j = 0; j < 32; ++j)
-      if (col + j < a.d) v[j] = fmaf(delta, __bfloat162float(w[j]), v[j]);
+      if (col + j < d) v[j] = fmaf(f, __bfloat162float(w[j]), v[j]);
   }
 }
 
@@ -391,8 +392,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                      const __grid_constant__ CUtensorMap tm_w,    // weights
                      const __grid_constant__ CUtensorMap tm_dk,   // D, K-major box
                      const __grid_constant__ CUtensorMap tm_dm,   // D, MN-major box
-                     const __grid_constant__ CUtensorMap tm_dl,   // its remainders' rows, likewise
-                     const __grid_constant__ CUtensorMap tm_hl,   // those rows' hidden
                      const HeadDev a) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -447,8 +446,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   // (no meta: every row of the caller's hidden, listed or not)
   const int n = a.meta ? a.meta->n : a.rows;
   const bool dense = a.meta ? a.meta->dense != 0 : true;
-  const int heavy = kMode != kLoss && a.slot ? a.meta->heavy : 0;
-  const Schedule<kMode, CG, BN> sch(a, n, heavy, blockIdx.x / CG, gridDim.x / CG);
+  const Schedule<kMode, CG, BN> sch(a, n, blockIdx.x / CG, gridDim.x / CG);
   auto lead_addr = [&](uint64_t* bar) -> uint32_t {
     return CG == 2 ? mapa_shared(smem_u32(bar), 0) : smem_u32(bar);
   };
@@ -495,12 +493,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 load(A + p * kABytes, &tm_dk, k * 64, p * a.d_plane + m0);
               } else {                    // dW: D (M contiguous)
 #pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                  if (k < u.k1)
-                    load(A + p * kABytes + j * 8192, &tm_dm, m0 + j * 64, p * a.d_plane + k * 64);
-                  else
-                    load(A + p * kABytes + j * 8192, &tm_dl, m0 + j * 64, (k - u.k1) * 64);
-                }
+                for (int j = 0; j < 2; ++j)
+                  load(A + p * kABytes + j * 8192, &tm_dm, m0 + j * 64, p * a.d_plane + k * 64);
               }
             }
 #pragma unroll
@@ -511,10 +505,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                   load(B + (s * kBParts<P> + p) * kBPart, &tm_w, (kx + s) * 64,
                        a.w_row0 + p * a.w_plane + n0);
               } else {                    // dH: W, dW: H (N contiguous)
-                const bool lo = u.kind == 2 && k >= u.k1;
-                const CUtensorMap* tb = u.kind == 1 ? &tm_w : lo ? &tm_hl : th;
-                const int y = lo ? (k - u.k1) * 64
-                                 : (u.kind == 1 ? a.w_row0 + p * a.w_plane : p * h_plane) + k * 64;
+                const CUtensorMap* tb = u.kind == 1 ? &tm_w : th;
+                const int y = (u.kind == 1 ? a.w_row0 + p * a.w_plane : p * h_plane) + k * 64;
 #pragma unroll
                 for (int j = 0; j < kBRows / 64; ++j)
                   load(B + p * kBPart + j * 8192, tb, n0 + j * 64, y);
@@ -604,7 +596,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; sch.get(a, i, u); ++i) {
       const int row = u.m0 + (int)rank * 128 + q * 32 + lane;   // row of the product
       const bool empty_sum = u.nk == 0;
-      int my_row = 0, tgt = -1, my_slot = -1;
+      int my_row = 0, tgt = -1;
       float lse = 0.f, g = 0.f;
       if (kMode != kGrad || u.kind == 1) {
         if (row < n) {
@@ -613,12 +605,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           if constexpr (kMode == kDlog) {
             lse = a.lse[my_row];
             g = a.grad_nll[my_row];
-            if (!F32 && a.slot) my_slot = a.slot[row];
           }
           if constexpr (kMode == kGrad && !F32) {
             // (kind 1) the row's target, where this unit's columns hold it
-            if (a.slot) {
-              const int t = a.target[my_row] - a.v0;
+            if (a.delta) {
+              const int t = a.row_tgt[row] - a.v0;
               if (t >= u.k0 * 64 && t < min(a.vc, (u.k0 + u.nk) * 64)) {
                 tgt = t + a.v0;
                 g = a.delta[row];
@@ -627,6 +618,24 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
+      // the remainder of D at this row's target, or the remainders whose target is this row's id
+      const __nv_bfloat16* with = nullptr;
+      if constexpr (kMode == kGrad && !F32) {
+        if (u.kind == 1) {
+          if (tgt >= 0) with = static_cast<const __nv_bfloat16*>(a.head) + (size_t)tgt * a.ld_head;
+        } else if (a.rest && row < a.vc) {
+          const int2 id = a.ids[a.v0 + row];
+          if (id.y == 1) {
+            with = dense ? static_cast<const __nv_bfloat16*>(a.hidden) + (size_t)id.x * a.ld_hidden
+                         : a.hid + (size_t)id.x * a.d_pad;
+            g = a.delta[id.x];
+          } else if (id.y > 1) {
+            with = a.rest + (size_t)id.x * a.d_pad;
+            g = 1.f;
+          }
+        }
+      }
+      const bool with_vec = u.kind == 2 || a.head_vec;
       const uint32_t lanes = uint32_t(q * 32) << 16;
       // a wait that gave up only flags the status word; the results are then garbage but the
       // kernel ends
@@ -749,8 +758,16 @@ __global__ void __launch_bounds__(kThreads, 1)
               v[j] = j < lim ? p * g : 0.f;
               if (j == rel) tv = v[j];
             }
-            if (!F32 && a.slot && row < n && rel >= 0 && rel < 32 * PC)
+            if (!F32 && a.delta && row < n && rel >= 0 && rel < 32 * PC) {
               a.delta[row] = tv - __bfloat162float(__float2bfloat16_rn(tv));
+              if (a.ids) {
+                // (which row comes first depends on timing; the sums do not: they are made in
+                // row order)
+                int2* id = a.ids + (col + rel + a.v0);
+                a.next[row] = atomicExch(&id->x, row);
+                atomicAdd(&id->y, 1);
+              }
+            }
           }
           // the parts one after the other, each the rounding of what the ones before leave
           for (int pl = 0; pl < a.d_parts; ++pl) {
@@ -766,29 +783,6 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
             }
           }
-          if (!F32 && my_slot >= 0) {
-            // (one or two lanes of a warp: straight from the registers)
-            uint4* dst = reinterpret_cast<uint4*>(a.d_lo + (size_t)my_slot * a.ld_dlog + col);
-#pragma unroll
-            for (int k = 0; k < 4 * PC; ++k) {
-              uint32_t w[4];
-#pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                const float x = v[8 * k + 2 * j], y = v[8 * k + 2 * j + 1];
-                const uint32_t hi = pack_bf16(x, y);
-                w[j] = pack_bf16(x - __uint_as_float(hi << 16), y - __uint_as_float(hi & 0xffff0000u));
-              }
-              dst[k] = make_uint4(w[0], w[1], w[2], w[3]);
-            }
-          }
-          if (!F32 && a.slot && u.m0 == 0 && rank == 0 && q == 0) {
-            // the last chunk of remainders is filled up with rows of zeros
-            const int zc = col + (lane & 7) * 8;
-            if ((lane & 7) * 8 < 32 * PC)
-              for (int r = heavy + (lane >> 3); r < ((heavy + 63) & ~63); r += 4)
-                *reinterpret_cast<uint4*>(a.d_lo + (size_t)r * a.ld_dlog + zc) =
-                    make_uint4(0, 0, 0, 0);
-          }
         }
       } else if (u.kind == 1 && a.acc) {
         // fp32 sums of this piece and K range
@@ -798,7 +792,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int col = ccol + c * 32;
           float v[32];
           load(c, v);
-          if (!F32 && tgt >= 0) add_target(a, tgt, g, col, v);
+          if (!F32 && with) add_row(with, with_vec, g, col, a.d, v);
           stage_f32(st, lane, v);
           if (a.acc_add) {
             __syncwarp();
@@ -837,7 +831,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int s2 = 0; s2 < PC; ++s2) {
             float v[32];
             load(c + s2, v);
-            if (!F32 && tgt >= 0) add_target(a, tgt, g, ccol + (c + s2) * 32, v);
+            if (!F32 && with) add_row(with, with_vec, g, ccol + (c + s2) * 32, a.d, v);
             if constexpr (F32) stage_f32(st, lane, v);
             else stage_bf16<RB>(st, lane, s2 * 4, v);
           }
@@ -1165,9 +1159,8 @@ struct RowsArgs {
   HeadMeta* meta;
   int* row_idx;
   __nv_bfloat16* out;          // [parts][r_pad][d_pad]
-  const float* grad_nll;       // heavy rows are looked for; null: not
-  int* slot;                   // [r_pad]
-  __nv_bfloat16* heavy_out;    // [kHeavyRows][d_pad]
+  int* row_tgt;                // [r_pad] targets of the listed rows; null: not wanted
+  int2* ids;                   // [vocab] to clear; null: not wanted
   float *nll, *lse;            // loss: zero for the rows that take no part
   void* grad_hidden;           // gradient: likewise
   bool gvec;
@@ -1275,42 +1268,21 @@ __global__ void __launch_bounds__(256) head_rows_kernel(RowsArgs a, WeightArgs w
   }
   __shared__ int red[2][8];
   __shared__ int s_before, s_total;
-  __shared__ int hist[2048];                  // rows by the leading bits of |grad_nll|
-  __shared__ int s_thr, s_hbefore, s_heavy;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int r0 = blockIdx.x * a.per, r1 = min(a.rows, r0 + a.per);
   int before = 0, total = 0;
-  // sign-free bits of grad_nll from the exponent down to three bits of the mantissa
-  auto bin_of = [](float g) { return (int)((__float_as_uint(g) & 0x7fffffffu) >> 20); };
-  auto weight_bin = [&](int r) { return bin_of(a.grad_nll[r]); };
-  // f(row, takes part, bin of its weight) for this thread's share of all rows, eight loads ahead
-  auto scan = [&](auto f) {
-    for (int base = tid; base < a.rows; base += 8 * 256) {
-      int t[8];
-      float g[8];
+  for (int base = tid; base < a.rows; base += 8 * 256) {
+    int t[8];
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const int r = min(base + k * 256, a.rows - 1);
-        t[k] = a.target[r];
-        g[k] = a.grad_nll ? a.grad_nll[r] : 0.f;
-      }
+    for (int k = 0; k < 8; ++k) t[k] = a.target[min(base + k * 256, a.rows - 1)];
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const int r = base + k * 256;
-        if (r < a.rows) f(r, t[k] >= 0 && t[k] < a.vocab, bin_of(g[k]));
-      }
+    for (int k = 0; k < 8; ++k) {
+      const int r = base + k * 256;
+      const bool on = r < a.rows && t[k] >= 0 && t[k] < a.vocab;
+      total += on;
+      if (r < r0) before += on;
     }
-  };
-  if (a.grad_nll) {
-    for (int i = tid; i < 2048; i += 256) hist[i] = 0;
-    if (tid == 0) s_thr = 0;
-    __syncthreads();
   }
-  scan([&](int r, bool on, int bin) {
-    total += on;
-    if (r < r0) before += on;
-    if (on && a.grad_nll) atomicAdd(&hist[bin], 1);
-  });
   for (int o = 16; o > 0; o >>= 1) {
     before += __shfl_xor_sync(0xffffffffu, before, o);
     total += __shfl_xor_sync(0xffffffffu, total, o);
@@ -1330,52 +1302,10 @@ __global__ void __launch_bounds__(256) head_rows_kernel(RowsArgs a, WeightArgs w
   __syncthreads();
   const int n = s_total;
   const bool dense = a.in_place && n == a.rows;
-  int at = s_before, hat = 0, thr = 0, heavy = 0;
-  if (a.grad_nll) {
-    // the smallest bin from which on at most kHeavyRows rows lie (thread t: eight bins, the
-    // largest ones first)
-    int mine = 0;
-    for (int k = 0; k < 8; ++k) mine += hist[2047 - 8 * tid - k];
-    int pre = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int x = __shfl_up_sync(0xffffffffu, pre, o);
-      if (lane >= o) pre += x;
-    }
-    if (lane == 31) red[0][warp] = pre;
-    __syncthreads();
-    for (int w = 0; w < warp; ++w) pre += red[0][w];
-    int sum = pre - mine;                      // rows in the bins above this thread's
-    if (sum <= kHeavyRows && pre > kHeavyRows) {
-      int b = 2047 - 8 * tid;
-      while (sum + hist[b] <= kHeavyRows) sum += hist[b--];
-      s_thr = b + 1;
-    }
-    __syncthreads();
-    thr = s_thr;
-    int hb = 0, ht = 0;
-    scan([&](int r, bool on, int bin) {
-      on = on && bin >= thr;
-      ht += on;
-      if (r < r0) hb += on;
-    });
-    for (int o = 16; o > 0; o >>= 1) {
-      hb += __shfl_xor_sync(0xffffffffu, hb, o);
-      ht += __shfl_xor_sync(0xffffffffu, ht, o);
-    }
-    if (lane == 0) { red[0][warp] = hb; red[1][warp] = ht; }
-    __syncthreads();
-    if (tid == 0) {
-      int b = 0, t = 0;
-      for (int w = 0; w < 8; ++w) { b += red[0][w]; t += red[1][w]; }
-      s_hbefore = b;
-      s_heavy = t;
-      if (blockIdx.x == 0) a.meta->heavy = t;
-    }
-    __syncthreads();
-    hat = s_hbefore;
-    heavy = s_heavy;
-  }
+  int at = s_before;
+  if (a.ids)
+    for (int v = blockIdx.x * 256 + tid; v < a.vocab; v += a.row_ctas * 256)
+      a.ids[v] = make_int2(0, 0);
   // 32 rows at a time: every warp works out the same listed positions, then takes every 8th row
   for (int b = r0; b < r1; b += 32) {
     const int r = b + lane;
@@ -1385,14 +1315,10 @@ __global__ void __launch_bounds__(256) head_rows_kernel(RowsArgs a, WeightArgs w
     const uint32_t mask = __ballot_sync(0xffffffffu, on);
     const int pos = at + __popc(mask & ((1u << lane) - 1u));
     at += __popc(mask);
-    const bool hv = a.grad_nll && on && weight_bin(r) >= thr;
-    const uint32_t hmask = __ballot_sync(0xffffffffu, hv);
-    const int slot = hv ? hat + __popc(hmask & ((1u << lane) - 1u)) : -1;
-    hat += __popc(hmask);
-    if (warp == 0 && a.grad_nll && on) a.slot[pos] = slot;
     if (warp == 0 && r < r1) {
       if (on) {
         a.row_idx[pos] = r;
+        if (a.row_tgt) a.row_tgt[pos] = t;
       } else if (a.nll) {
         a.nll[r] = 0.f;
         a.lse[r] = 0.f;
@@ -1400,10 +1326,8 @@ __global__ void __launch_bounds__(256) head_rows_kernel(RowsArgs a, WeightArgs w
     }
     for (int i = warp; i < min(32, r1 - b); i += 8) {
       const int p = __shfl_sync(0xffffffffu, pos, i);
-      const int sl = __shfl_sync(0xffffffffu, slot, i);
       if ((mask >> i) & 1u) {
         if (!dense) copy_row(a, b + i, a.out, p, lane);
-        if (sl >= 0) copy_row(a, b + i, a.heavy_out, sl, lane);
       } else if (a.grad_hidden) {
         const size_t es = a.f32 ? 4 : 2;
         uint8_t* g = static_cast<uint8_t*>(a.grad_hidden) + (size_t)(b + i) * a.d * es;
@@ -1419,11 +1343,6 @@ __global__ void __launch_bounds__(256) head_rows_kernel(RowsArgs a, WeightArgs w
       }
     }
   }
-  // likewise the heavy rows' last chunk
-  if (a.grad_nll)
-    for (int r = heavy + blockIdx.x * 8 + warp; r < ((heavy + 63) & ~63); r += a.row_ctas * 8)
-      for (int c = lane * 8; c < a.d_pad; c += 256)
-        *reinterpret_cast<uint4*>(a.heavy_out + (size_t)r * a.d_pad + c) = make_uint4(0, 0, 0, 0);
   // the rows up to the next multiple of 64 (128 with one row tile) are summed over by dW: zeros,
   // every CTA its share
   if (a.pad_rows && !dense) {
@@ -1434,6 +1353,132 @@ __global__ void __launch_bounds__(256) head_rows_kernel(RowsArgs a, WeightArgs w
         for (int c = lane * 8; c < a.d_pad; c += 256)
           *reinterpret_cast<uint4*>(a.out + p * plane + (size_t)r * a.d_pad + c) =
               make_uint4(0, 0, 0, 0);
+  }
+}
+
+// rest[x] = the sum of delta_r h_r over the listed rows r with one target, in row order, for the
+// targets of a piece that two or more rows have (one row's is added as it lies); x is the row
+// where their chain begins.  A warp takes 256 columns and looks at four listed rows.  Up to 32 rows it
+// finds by the chain and puts in order; more it looks up among all listed rows, 256 at a time.
+// Summed in fp32, eight rows in flight; kept in bf16, which is 2^-9 of 2^-9 of D's part of dW.
+// 4096 rows of 4096 over 8192 ids: 13.6 us, most of them the latency of looking.
+struct RestArgs {
+  const HeadMeta* meta;
+  const int* row_tgt;
+  const float* delta;
+  const int2* ids;
+  const int* next;
+  const void* hidden;          // the caller's rows
+  long long ld_hidden;
+  const __nv_bfloat16* hid;    // the listed rows
+  int d, d_pad, slabs, v0, vc;
+  __nv_bfloat16* out;          // [r_pad][d_pad]
+};
+
+constexpr int kRestWarps = 8, kRestRows = 4;
+
+__global__ void __launch_bounds__(kRestWarps * 32) head_rest_kernel(RestArgs a) {
+  griddep_launch();
+  griddep_wait();
+  __shared__ int lists[kRestWarps][288];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int n = a.meta->n;
+  const long long job = (long long)blockIdx.x * kRestWarps + warp;
+  const int row0 = (int)(job / a.slabs) * kRestRows, c = (int)(job % a.slabs) * 256 + lane * 8;
+  if (row0 >= n) return;
+  // both kinds of rows start on 16 bytes and fill 16-byte words
+  const bool dense = a.meta->dense != 0;
+  const __nv_bfloat16* h = dense ? static_cast<const __nv_bfloat16*>(a.hidden) : a.hid;
+  const long long ld = dense ? a.ld_hidden : a.d_pad;
+  const bool in = c < (dense ? a.d : a.d_pad);
+  int* list = lists[warp];
+  int my_t = -1, my_count = 0;
+  if (lane < kRestRows && row0 + lane < n) {
+    my_t = a.row_tgt[row0 + lane];
+    if (my_t >= a.v0 && my_t < a.v0 + a.vc) {
+      const int2 id = a.ids[my_t];
+      if (id.x == row0 + lane) my_count = id.y;
+    }
+  }
+  for (uint32_t m = __ballot_sync(0xffffffffu, my_count > 1); m; m &= m - 1) {
+    const int i = __ffs(m) - 1, row = row0 + i;
+    const int t = __shfl_sync(0xffffffffu, my_t, i);
+    int left = __shfl_sync(0xffffffffu, my_count, i);
+    float s[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) s[j] = 0.f;
+    // the rows r of lanes 0 .. cnt - 1, in the lanes' order
+    auto add = [&](int r, int cnt) {
+      const float delta = lane < cnt ? a.delta[r] : 0.f;
+      for (int e0 = 0; e0 < cnt; e0 += 8) {
+        uint4 x[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const int from = __shfl_sync(0xffffffffu, r, e0 + k);
+          x[k] = in && e0 + k < cnt ? *reinterpret_cast<const uint4*>(h + (size_t)from * ld + c)
+                                    : make_uint4(0, 0, 0, 0);
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const float f = __shfl_sync(0xffffffffu, delta, e0 + k);
+          const uint32_t w[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            s[2 * j] = fmaf(f, __uint_as_float(w[j] << 16), s[2 * j]);
+            s[2 * j + 1] = fmaf(f, __uint_as_float(w[j] & 0xffff0000u), s[2 * j + 1]);
+          }
+        }
+      }
+    };
+    if (left <= 32) {
+      int r = row, mine = 0x7fffffff;
+      for (int k = 0; k < left; ++k) {
+        if (lane == k) mine = r;
+        if (k + 1 < left) r = a.next[r];
+      }
+      int rank = 0;
+      for (int k = 0; k < left; ++k) rank += __shfl_sync(0xffffffffu, mine, k) < mine;
+      if (lane < left) list[rank] = mine;
+      __syncwarp();
+      mine = lane < left ? list[lane] : row;
+      __syncwarp();
+      add(mine, left);
+    } else {
+      int cnt = 0;
+      for (int base = 0; base < n; base += 256) {
+        int v[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const int r = base + k * 32 + lane;
+          v[k] = r < n ? a.row_tgt[r] : -1;
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const uint32_t hit = __ballot_sync(0xffffffffu, v[k] == t);
+          if (v[k] == t) list[cnt + __popc(hit & ((1u << lane) - 1u))] = base + k * 32 + lane;
+          cnt += __popc(hit);
+          left -= __popc(hit);
+        }
+        __syncwarp();
+        // 32 rows at a time; the last few wait for more
+        const bool end = left <= 0 || base + 256 >= n;
+        int e0 = 0;
+        for (; e0 + 32 <= cnt || (end && e0 < cnt); e0 += 32)
+          add(e0 + lane < cnt ? list[e0 + lane] : row, min(32, cnt - e0));
+        cnt = max(0, cnt - e0);
+        const int keep = lane < cnt ? list[e0 + lane] : 0;
+        __syncwarp();
+        if (lane < cnt) list[lane] = keep;
+        if (end) break;
+      }
+    }
+    if (c < a.d_pad) {
+      uint32_t w[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) w[j] = pack_bf16(s[2 * j], s[2 * j + 1]);
+      *reinterpret_cast<uint4*>(a.out + (size_t)row * a.d_pad + c) =
+          make_uint4(w[0], w[1], w[2], w[3]);
+    }
   }
 }
 
@@ -1581,8 +1626,8 @@ struct Plan {
   int d_parts, g_terms;   // bf16 parts of D; products summed by the gradients
   bool staged;        // weights go through a bf16 copy of each piece
   int piece, n_pieces;
-  bool heavy;         // the heaviest rows' remainders
-  size_t meta, row_idx, hid, part, tlogit, wst, dlog, acc, slot, delta, hlo, dlo, total;
+  bool rest;          // D's remainders at the targets
+  size_t meta, row_idx, hid, part, tlogit, wst, dlog, acc, row_tgt, delta, ids, next, rest_rows, total;
   int cfg, cfg_g;     // tile configuration of the logits' product and of the gradients'
   int splits, n_part;
   int narrow;         // > 0: head_narrow_kernel, with this many vocabulary slots (= splits)
@@ -1644,7 +1689,7 @@ Plan make_plan(int rows, int d, int vocab, long long ld_head, bool f32, bool gra
   }
   p.d_parts = f32 ? 3 : rows <= 128 ? 2 : 1;
   p.g_terms = f32 ? 6 : 1;
-  p.heavy = grad && p.d_parts == 1;
+  p.rest = grad && p.d_parts == 1;
   // widest piece whose D (gradient) and weight copy (when made) stay below kPieceBytes
   size_t per_col = 0;
   if (grad) per_col = (size_t)p.d_parts * p.r_pad * 2;
@@ -1702,11 +1747,12 @@ Plan make_plan(int rows, int d, int vocab, long long ld_head, bool f32, bool gra
   if (p.staged) p.wst = take((size_t)p.parts * p.piece * p.d_pad * 2);
   if (grad) {
     p.dlog = take((size_t)p.d_parts * p.r_pad * p.piece * 2);
-    if (p.heavy) {
-      p.slot = take((size_t)p.r_pad * 4);
+    if (p.rest) {
+      p.row_tgt = take((size_t)p.r_pad * 4);
       p.delta = take((size_t)p.r_pad * 4);
-      p.hlo = take((size_t)kHeavyRows * p.d_pad * 2);
-      p.dlo = take((size_t)kHeavyRows * p.piece * 2);
+      p.ids = take((size_t)vocab * 8);
+      p.next = take((size_t)p.r_pad * 4);
+      p.rest_rows = take((size_t)p.r_pad * p.d_pad * 2);
     }
     if (p.narrow || p.splits > 1 || p.n_pieces > 1) p.acc = take((size_t)p.splits * p.r_pad * p.d_pad * 4);
   }
@@ -1728,7 +1774,7 @@ bool encode_bf16(CUtensorMap* m, const void* base, uint64_t inner, uint64_t oute
 }
 
 struct Maps {
-  CUtensorMap h, hc, w, dk, dm, dl, hl;
+  CUtensorMap h, hc, w, dk, dm;
 };
 
 // Clusters of the pair kernels that fit the device at once (some SM groups are odd).
@@ -1782,7 +1828,7 @@ cudaError_t launch_one(const Maps& m, HeadDev a, long long units, int sms, cudaS
   long long slots = std::min<long long>(ready[dev], units);
   if (slots < 1) slots = 1;
   return launch_pdl(kern, dim3((unsigned)(slots * CG)), dim3(kThreads), (size_t)smem, st, CG, m.h,
-                    m.hc, m.w, m.dk, m.dm, m.dl, m.hl, a);
+                    m.hc, m.w, m.dk, m.dm, a);
 }
 
 template <int kMode, int P, bool kLong = false>
@@ -1872,10 +1918,9 @@ struct Call {
     r.out = at<__nv_bfloat16>(p.hid);
     r.nll = h.nll;
     r.lse = h.lse_out;
-    if (p.heavy) {
-      r.grad_nll = h.grad_nll;
-      r.slot = at<int>(p.slot);
-      r.heavy_out = at<__nv_bfloat16>(p.hlo);
+    if (p.rest) {
+      r.row_tgt = at<int>(p.row_tgt);
+      if (h.grad_head) r.ids = at<int2>(p.ids);
     }
     r.grad_hidden = h.grad_hidden;
     r.gvec = whole_words(h.grad_hidden, h.d);
@@ -1980,7 +2025,7 @@ int head_grad_launches(const HeadArgs& a) {
   const Plan p = make_plan(a.rows, a.d, a.vocab, a.ld_head, a.f32, true);
   if (p.few) return 1 + head_few_groups(a.rows, a.d) + (a.grad_hidden ? 1 : 0);
   const bool sums = p.narrow || p.splits > 1 || p.n_pieces > 1;
-  return 1 + 2 * p.n_pieces + (p.staged ? p.n_pieces - 1 : 0) + (sums && a.grad_hidden ? 1 : 0);
+  return 1 + (p.rest && a.grad_head ? 3 : 2) * p.n_pieces + (p.staged ? p.n_pieces - 1 : 0) + (sums && a.grad_hidden ? 1 : 0);
 }
 
 cudaError_t launch_head_loss(const HeadArgs& h, cudaStream_t st) {
@@ -1997,7 +2042,7 @@ cudaError_t launch_head_loss(const HeadArgs& h, cudaStream_t st) {
     a.a_box = c.a_box();
     if (!c.hidden_maps(&m.h, &m.hc, a.a_box) || !c.weight_map(&m.w, vc, bn / cg))
       return cudaErrorInvalidValue;
-    m.dk = m.dm = m.dl = m.hl = m.hc;
+    m.dk = m.dm = m.hc;
     a.part = c.at<float2>(p.part);
     a.part0 = 2 * (p.piece / bn) * i;
     a.tlogit = c.at<float>(p.tlogit);
@@ -2029,31 +2074,44 @@ cudaError_t launch_head_grad(const HeadArgs& h, cudaStream_t st) {
     a.a_box = c.a_box();
     if (!c.hidden_maps(&m.h, &m.hc, a.a_box) || !c.weight_map(&m.w, vc, bn / cg))
       return cudaErrorInvalidValue;
-    m.dk = m.dm = m.dl = m.hl = m.hc;
+    m.dk = m.dm = m.hc;
     a.d_parts = p.d_parts;
     a.d_rows = p.narrow ? c.narrow_rows() : p.r_pad;
     a.lse = h.lse;
     a.grad_nll = h.grad_nll;
     a.dlog = c.at<__nv_bfloat16>(p.dlog);
     a.ld_dlog = p.piece;
-    if (p.heavy) {
-      a.slot = c.at<int>(p.slot);
-      a.d_lo = c.at<__nv_bfloat16>(p.dlo);
+    if (p.rest) {
+      a.row_tgt = c.at<int>(p.row_tgt);
       a.delta = c.at<float>(p.delta);
+      if (h.grad_head) {
+        a.ids = c.at<int2>(p.ids);
+        a.next = c.at<int>(p.next);
+        a.hidden = h.hidden;
+        a.ld_hidden = h.ld_hidden;
+        a.hid = c.at<__nv_bfloat16>(p.hid);
+        a.rest = c.at<__nv_bfloat16>(p.rest_rows);
+      }
       a.head = h.head;
       a.ld_head = h.ld_head;
       a.head_vec = c.whole_words(h.head, h.ld_head);
     }
     const long long units = (long long)((h.rows + 128 * cg - 1) / (128 * cg)) * ((vc + bn - 1) / bn);
     TRY(launch_mode<kDlog>(p.parts, p.cfg, m, a, units, c.sms, st));
+    if (a.rest) {
+      const int slabs = (p.d_pad + 255) / 256;
+      const RestArgs r{a.meta, a.row_tgt, a.delta, a.ids, a.next, h.hidden, h.ld_hidden,
+                       c.at<__nv_bfloat16>(p.hid), h.d, p.d_pad, slabs, v0, vc,
+                       c.at<__nv_bfloat16>(p.rest_rows)};
+      const long long jobs = (long long)((h.rows + kRestRows - 1) / kRestRows) * slabs;
+      TRY(launch_pdl(head_rest_kernel, dim3((unsigned)((jobs + kRestWarps - 1) / kRestWarps)),
+                     dim3(kRestWarps * 32), 0, st, 1, r));
+    }
     // both products of D: 64-row boxes for the MN-major operands
     if (!c.hidden_maps(&m.h, &m.hc, 64) || !c.weight_map(&m.w, vc, 64) ||
         !encode_bf16(&m.dk, a.dlog, p.piece, (uint64_t)p.d_parts * p.r_pad, p.piece, 64,
                      p.narrow ? a.d_rows : 128) ||
         !encode_bf16(&m.dm, a.dlog, p.piece, (uint64_t)p.d_parts * p.r_pad, p.piece, 64, 64))
-      return cudaErrorInvalidValue;
-    if (p.heavy && (!encode_bf16(&m.dl, a.d_lo, p.piece, kHeavyRows, p.piece, 64, 64) ||
-                    !encode_bf16(&m.hl, c.at<__nv_bfloat16>(p.hlo), p.d_pad, kHeavyRows, p.d_pad, 64, 64)))
       return cudaErrorInvalidValue;
     a.terms = p.g_terms;
     a.do_h = h.grad_hidden != nullptr;

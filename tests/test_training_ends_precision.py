@@ -6,7 +6,7 @@ import pytest
 import torch
 
 import masked_discrete_diffusion_sparse_b200 as smdm
-from test_training_ends import BF16, Head, _gpu, f64  # noqa: F401
+from test_training_ends import BF16, Head, _gpu, f64, gen  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -31,3 +31,62 @@ def test_head_gradient_sums_over_very_many_rows():
     ref = D.T @ x.h.to(f64)
     rel = ((gw.to(f64) - ref) / ref)[1:]
     assert rel.mean().abs() <= 2.0 ** -14 + 5 * 1.8e-5, rel.mean().item()
+
+
+def norm_error_bounds(x, lse):
+    """The gradients of a Head case and, for each output, its value in 64 bits and the error that
+    rounding the output once and D off the targets may leave, in the Frobenius norm: D's rounding
+    is off by at most half a step u = 2^-8 of its value, independently from entry to entry, so the
+    squares add up to at most u^2 / 3 D_rv^2 |w_v|^2 (or |h_r|^2) over r and v != t(r)."""
+    on, h, w, z, t, _, _, _ = x.reference()
+    p = torch.exp(z - lse.to(f64)[:, None])
+    g = torch.where(on, x.weight, torch.zeros_like(x.weight)).to(f64)[:, None]
+    D = p * g
+    off = D.scatter(1, t, 0.0).square()
+    D.scatter_add_(1, t, -g)
+    out = []
+    for ref, var in ((D @ w, (off @ w.square()).sum()), (D.T @ h, (off.T @ h.square()).sum())):
+        own = (ref.to(BF16).to(f64) - ref).norm()
+        out.append((ref, (own.square() + 2.0 ** -16 / 3 * var).sqrt().item()))
+    return out
+
+
+@pytest.mark.parametrize("kind", ["row", "equal", "sequence"])
+@pytest.mark.parametrize("case", [(1024, 512, 2048, 0.0), (300, 128, 700, 0.1),
+                                  (2000, 256, 5000, 0.25), (333, 251, 1001, 0.5)],
+                         ids=lambda c: "-".join(map(str, c)))
+def test_head_gradients_keep_their_own_rounding(case, kind):
+    """Weights per row, the same for all rows (the mean), and per sequence of rows (1 / t): both
+    gradients' errors are their own rounding's (at least 2^18 outputs: the norms' spread is below
+    1 %; 3 % of room).  With D's rounding at the targets in them they are up to 1.45 times as large."""
+    rows, d, vocab, ignored = case
+    x = Head(rows, d, vocab, BF16, ignored, seed=rows)
+    if kind == "equal":
+        x.weight.fill_(1 / rows)
+    elif kind == "sequence":
+        x.weight = (1 / torch.tensor([0.05, 0.2, 0.5, 0.9], device="cuda") / rows) \
+            .repeat_interleave((rows + 3) // 4)[:rows].contiguous()
+    _, lse = x.check_loss()
+    got = x.check_grad(lse)
+    for what, o, (ref, bound) in zip(("grad_hidden", "grad_lm_head"), got,
+                                     norm_error_bounds(x, lse)):
+        err = (o.to(f64) - ref).norm().item()
+        assert err <= 1.03 * bound, f"{what}: {err / bound:.3f} times its rounding"
+
+
+@pytest.mark.parametrize("rows,d,vocab", [(700, 96, 40), (5000, 264, 3), (400, 1000, 1),
+                                          (1500, 320, 900)])
+def test_head_gradient_of_targets_with_many_rows(rows, d, vocab):
+    """Few ids take all targets, or one id most of them: hundreds of remainders add to one row."""
+    x = Head(rows, d, vocab, BF16, 0.2, pad=3 if d == 264 else 0, seed=d)
+    if vocab == 900:
+        x.target[torch.rand(rows, generator=gen(1), device="cuda") < 0.7] = 571
+    x.weight.fill_(1 / rows)
+    _, lse = x.check_loss()
+    got = x.check_grad(lse)
+    if vocab > 1:                      # (one id: D is nothing but the error of exp)
+        ref, bound = norm_error_bounds(x, lse)[1]
+        err = (got[1].to(f64) - ref).norm().item()
+        assert err <= 1.05 * bound, err / bound
+    again = x.grad(lse)
+    assert torch.equal(got[0], again[0]) and torch.equal(got[1], again[1])
