@@ -144,15 +144,16 @@ template <int P> __host__ __device__ constexpr int part_b(int t) {
 // of one sign, every 16-term step takes 1e-8 (terms of like size) to 1e-7 of the final value off:
 // 1.6e-3 over 2^18 rows, as much as bf16's rounding.  It therefore sums kSegment chunks at a
 // time, and the epilogue threads add the segments in registers, rounded to nearest: 24 or 32 steps
-// where the result is fp32 (the loss, and everything of the fp32 path).  The bf16 gradients are
-// rounded to 8 bits next; their segments are kWholeK chunks (512 steps, 5e-5 of the value at most,
-// 1/40 of that rounding), and K ranges up to that long are summed whole, by a kernel of its own:
-// the registers for the sums cost up to 10 % (200 rows of 1024 x 32000: 92.7 -> 101 us).  D's
-// product is summed whole.
+// for logits (the loss's, and the gradient's: what is left of exp(z - lse) - 1 at a certain target
+// is as exact as z and lse are to each other) and for everything of the fp32 path.  The bf16
+// gradients are rounded to 8 bits next; their segments are kWholeK chunks (512 steps, 5e-5 of the
+// value at most, 1/40 of that rounding), and K ranges up to that long are summed whole, by a
+// kernel of its own: the registers for the sums cost up to 10 % (200 rows of 1024 x 32000:
+// 92.7 -> 101 us).
 constexpr int kWholeK = 128;
 template <int kMode, int P> constexpr int kSegment = P == 3 ? 1 : kMode == kGrad ? kWholeK : 8;
 template <int kMode, int P, bool kLong>
-constexpr bool kPromote = P == 3 || kMode == kLoss || kLong;
+constexpr bool kPromote = P == 3 || kMode != kGrad || kLong;
 
 // 64-wide K chunks per pipeline stage.  Waiting for a stage and releasing it takes the issuing
 // warp about 300 clocks, as much as the MMAs of a narrow tile, so those take two at a time.
@@ -725,7 +726,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (row < n)
           a.part[(size_t)(a.part0 + 2 * (u.n0 / BN) + half) * a.r_pad + row] = make_float2(m, s);
       } else if constexpr (kMode == kDlog) {
-        constexpr int PC = (!F32 && HC >= 64) ? 2 : 1;   // 32-column blocks per staged pass
+        // 32-column blocks per staged pass (two of 128 columns' sums would spill: 190 -> 195 us for
+        // 4096 rows of 4096 x 8192)
+        constexpr int PC = !F32 && HC == 64 ? 2 : 1;
         constexpr int RB = 64 * PC;
         auto rp = [&](int plane) {
           return [&, plane](int r) -> __nv_bfloat16* {
@@ -769,12 +772,14 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
             }
           }
-          // the parts one after the other, each the rounding of what the ones before leave
-          for (int pl = 0; pl < a.d_parts; ++pl) {
+          // the parts one after the other, each the rounding of what the ones before leave (more
+          // than one of bf16 only in tiles of 64 columns)
+          const int parts = F32 || BN == 64 ? a.d_parts : 1;
+          for (int pl = 0; pl < parts; ++pl) {
 #pragma unroll
             for (int s2 = 0; s2 < PC; ++s2) stage_bf16<RB>(st, lane, s2 * 4, v + 32 * s2);
             flush_rows<__nv_bfloat16, RB, false>(st, lane, col, a.ld_dlog, true, rp(pl));
-            if (pl + 1 < a.d_parts) {
+            if (pl + 1 < parts) {
 #pragma unroll
               for (int j = 0; j < 32 * PC; j += 2) {
                 const uint32_t hi = pack_bf16(v[j], v[j + 1]);

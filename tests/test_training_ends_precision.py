@@ -6,9 +6,52 @@ import pytest
 import torch
 
 import masked_discrete_diffusion_sparse_b200 as smdm
-from test_training_ends import BF16, Head, _gpu, f64, gen  # noqa: F401
+from test_training_ends import BF16, Head, _gpu, f64, gen, rand, workspace  # noqa: F401
 
 pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("rows", [40, 200])
+@pytest.mark.parametrize("rest", [1e-2, 1e-3])
+def test_head_gradient_of_certain_targets(rows, rest):
+    """p_target = 1 - rest at a logit of 30: D at the target is -rest, the difference of exp(z - lse)
+    and 1, and every other entry is about rest / vocab.
+
+    z_target and lse come from the same kind of sum, off by at most dz: the tensor core cuts up to
+    2^-23 of a segment's value off in each of its 32 steps, the 8 segments are added with 2^-24 of a
+    growing sum each, and z, lse and z - lse are rounded to 2^-24: 30 (2^-18 + 2^-22 + 3 2^-24), and
+    2^-22 of exp.  grad_hidden is rest times a difference of weight rows, so dz / rest is its
+    relative error, plus the output's rounding and D's (2^-9 in the norm each, 2^-8 together).
+    With K summed whole (256 steps) dz alone would be 30 2^-15."""
+    d, vocab, top = 4096, 500, 30.0
+    g = gen(rows)
+    u = rand(g, d, std=0.02)
+    w = (u + rand(g, vocab, d, std=0.002)).to(BF16)
+    target = torch.randint(0, vocab, (rows,), generator=g, device="cuda")
+    # z_v = other for all v, top at the target: rest = vocab exp(other - top)
+    other = top + float(torch.log(torch.tensor(rest / vocab)))
+    lift = w[target].float() - u
+    lift -= (lift @ u)[:, None] / u.square().sum() * u
+    h = other * u / u.square().sum() + (top - other) * lift / lift.square().sum(dim=1, keepdim=True)
+    h = h.to(BF16)
+    weight = torch.rand(rows, generator=g, device="cuda") + 0.5
+    ws = workspace(max(smdm.smdm_head_loss_workspace_bytes(rows, d, vocab, BF16, grad=b)
+                       for b in (False, True)))
+    nll, lse = (torch.full((rows,), float("nan"), device="cuda") for _ in range(2))
+    smdm.smdm_head_loss(h, w, target.int(), nll, lse, ws)
+    gh, gw = torch.empty_like(h), torch.empty_like(w)
+    smdm.smdm_head_loss_grad(h, w, target.int(), lse, weight, gh, gw, ws)
+    z = h.to(f64) @ w.to(f64).T
+    log_p = z - torch.logsumexp(z, dim=1, keepdim=True)
+    at = torch.arange(rows, device="cuda")
+    assert (log_p[at, target].neg().log() - torch.log(torch.tensor(rest))).abs().max() < 1
+    D = log_p.exp()
+    D[at, target] = torch.expm1(log_p[at, target])
+    ref = (D * weight.to(f64)[:, None]) @ w.to(f64)
+    dz = top * (2.0 ** -18 + 2.0 ** -22 + 3 * 2.0 ** -24) + 2.0 ** -22
+    err = (gh.to(f64) - ref).norm(dim=1) / ref.norm(dim=1)
+    tol = dz / -D[at, target] + 2.0 ** -8
+    assert (err <= tol).all(), (err / tol).max().item()
 
 
 def test_head_gradient_sums_over_very_many_rows():
