@@ -411,7 +411,8 @@ size_t smdm_rmsnorm_grad_workspace_bytes(const smdm_rmsnorm_shape* shape);
 
 /* With u = grad_y gain:  grad_x = rstd (u - x rstd^2 mean(u x)) + grad_add,
  * grad_gain = sum over rows of grad_y x rstd.  d_grad_add (optional, contiguous, x's type): the
- * gradient that reaches x past the norm (the residual branch). */
+ * gradient that reaches x past the norm (the residual branch).  There is no d_status: if a bounded
+ * wait gives up, the rows that did not arrive are NaN in grad_x, and grad_gain with them. */
 smdm_status smdm_rmsnorm_grad(const smdm_rmsnorm_shape* shape, const void* d_x,
                               const void* d_gain, const float* d_rstd, const void* d_grad_y,
                               const void* d_grad_add, void* d_grad_x, void* d_grad_gain,

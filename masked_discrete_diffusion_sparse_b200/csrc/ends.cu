@@ -358,7 +358,9 @@ __global__ void __launch_bounds__(TH, 512 / TH) train_rms_grad_ring_kernel(RmsAr
     if ((tid & 31) == 0) rd[tid >> 5] = dot;
     __syncthreads();                        // the stage has been read, too
     const long long next = row + (long long)q.stages * gridDim.x;
-    if (tid == 0 && next < a.rows) fetch((int)next, st);
+    // (after a wait that gave up the stage's copies may still be on their way, and its barrier still
+    // waits for them: nothing more is fetched, and the waits for it give up at once)
+    if (tid == 0 && next < a.rows && !*abort_flag) fetch((int)next, st);
     dot = 0.f;
 #pragma unroll
     for (int i = 0; i < TH / 32; ++i) dot += rd[i];
