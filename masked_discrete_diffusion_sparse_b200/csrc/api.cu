@@ -1401,6 +1401,14 @@ smdm_status smdm_loss_stepcausal(smdm_handle* h, const int32_t* d_ids, const int
     return fail(h, SMDM_EINVAL, "the workspace must be 256-byte aligned device memory");
   if (bytes < L.total)
     return fail(h, SMDM_ENOMEM, "workspace of %zu bytes, %zu needed", bytes, L.total);
+  auto off = [](const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a != 0; };
+  for (const void* p : {(const void*)d_ids, (const void*)d_pos, (const void*)d_type,
+                        (const void*)d_label, (const void*)d_loss_rows, (const void*)d_target,
+                        (const void*)d_nll, (const void*)d_lse, (const void*)d_grad_nll,
+                        (const void*)d_grad_x})
+    if (off(p, 4)) return fail(h, SMDM_EINVAL, "a tensor is off its element's boundary");
+  if (off(d_grad_final_norm, h->es()) || off(d_grad_lm_head, h->es()))
+    return fail(h, SMDM_EINVAL, "a gradient is off its element's boundary");
   if (head_needs_aligned_weight(c.d_model, c.d_model, !h->bf16) &&
       reinterpret_cast<uintptr_t>(h->lm_head) % 16)
     return fail(h, SMDM_EINVAL, "lm_head must start on a 16-byte boundary");

@@ -16,6 +16,10 @@ bool is_dtype(int t) { return t == SMDM_F32 || t == SMDM_BF16; }
 size_t size_of(int t) { return t == SMDM_F32 ? 4 : 2; }
 bool on_boundary(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
+// fp32 or 32-bit integer tensors (a null one lies on every boundary).
+template <typename... P>
+bool on_words(const P*... p) { return (on_boundary(p, 4) && ...); }
+
 // A workspace of `need` bytes: SMDM_EINVAL for none or a misaligned one, SMDM_ENOMEM for a
 // small one.
 smdm_status check_ws(const void* ws, size_t bytes, size_t need) {
@@ -97,6 +101,7 @@ smdm_status smdm_head_loss(const smdm_head_shape* s, const void* d_hidden, const
   smdm_status r;
   if ((r = check_head(s)) || (r = check_head_ptrs(s, d_hidden, d_lm_head, d_target))) return r;
   if (s->rows > 0 && (!d_nll || !d_lse)) return SMDM_EINVAL;
+  if (!on_words(d_nll, d_lse, d_status)) return SMDM_EINVAL;
   if ((r = check_ws(d_workspace, bytes, smdm_head_loss_workspace_bytes(s, 0)))) return r;
   if (s->rows == 0) return SMDM_OK;
   HeadArgs a = head_args(s, d_hidden, d_lm_head, d_target, d_workspace, d_status);
@@ -114,7 +119,8 @@ smdm_status smdm_head_loss_grad(const smdm_head_shape* s, const void* d_hidden,
   if ((r = check_head(s)) || (r = check_head_ptrs(s, d_hidden, d_lm_head, d_target))) return r;
   const size_t es = size_of(s->dtype);
   if ((!d_grad_hidden && !d_grad_lm_head) || !on_boundary(d_grad_hidden, es) ||
-      !on_boundary(d_grad_lm_head, es) || (s->rows > 0 && (!d_lse || !d_grad_nll)))
+      !on_boundary(d_grad_lm_head, es) || (s->rows > 0 && (!d_lse || !d_grad_nll)) ||
+      !on_words(d_lse, d_grad_nll, d_status))
     return SMDM_EINVAL;
   if ((r = check_ws(d_workspace, bytes, smdm_head_loss_workspace_bytes(s, 1)))) return r;
   if (s->rows == 0)   // a sum over no rows
@@ -134,7 +140,7 @@ smdm_status smdm_rmsnorm(const smdm_rmsnorm_shape* s, const void* d_x, const voi
   smdm_status r;
   if ((r = check_norm(s))) return r;
   const size_t xs = size_of(s->x_dtype), es = size_of(s->dtype);
-  if (!d_gain || !on_boundary(d_gain, es)) return SMDM_EINVAL;
+  if (!d_gain || !on_boundary(d_gain, es) || !on_words(d_rstd)) return SMDM_EINVAL;
   if (s->rows == 0) return SMDM_OK;
   if (!d_x || !d_y || !on_boundary(d_x, xs) || !on_boundary(d_y, es)) return SMDM_EINVAL;
   RmsArgs a{};
@@ -164,7 +170,8 @@ smdm_status smdm_rmsnorm_grad(const smdm_rmsnorm_shape* s, const void* d_x, cons
   smdm_status r;
   if ((r = check_norm(s))) return r;
   const size_t xs = size_of(s->x_dtype), es = size_of(s->dtype);
-  if (!d_gain || !d_grad_gain || !on_boundary(d_gain, es) || !on_boundary(d_grad_gain, es))
+  if (!d_gain || !d_grad_gain || !on_boundary(d_gain, es) || !on_boundary(d_grad_gain, es) ||
+      !on_words(d_rstd))
     return SMDM_EINVAL;
   if (s->rows > 0 && (!d_x || !d_rstd || !d_grad_y || !d_grad_x || !on_boundary(d_x, xs) ||
                       !on_boundary(d_grad_y, es) || !on_boundary(d_grad_add, xs) ||
@@ -195,7 +202,8 @@ smdm_status smdm_embed(const smdm_embed_shape* s, const int32_t* d_ids, const vo
                        void* d_out, uint32_t* d_status, cudaStream_t st) {
   smdm_status r;
   if ((r = check_embed(s))) return r;
-  if (!d_table || !on_boundary(d_table, size_of(s->dtype))) return SMDM_EINVAL;
+  if (!d_table || !on_boundary(d_table, size_of(s->dtype)) || !on_words(d_ids, d_status))
+    return SMDM_EINVAL;
   if (s->rows == 0) return SMDM_OK;
   if (!d_ids || !d_out || !on_boundary(d_out, size_of(s->out_dtype))) return SMDM_EINVAL;
   EmbedArgs a{};
@@ -224,7 +232,8 @@ smdm_status smdm_embed_grad(const smdm_embed_shape* s, const int32_t* d_ids,
   smdm_status r;
   if ((r = check_embed(s))) return r;
   const size_t es = size_of(s->dtype);
-  if (!d_grad_table || !on_boundary(d_grad_table, es)) return SMDM_EINVAL;
+  if (!d_grad_table || !on_boundary(d_grad_table, es) || !on_words(d_ids, d_status))
+    return SMDM_EINVAL;
   if (s->rows > 0 && (!d_ids || !d_grad_out || !on_boundary(d_grad_out, size_of(s->out_dtype))))
     return SMDM_EINVAL;
   if ((r = check_ws(d_workspace, bytes, smdm_embed_grad_workspace_bytes(s)))) return r;
