@@ -1161,6 +1161,7 @@ struct RowsArgs {
   long long ld;
   const void* hidden;
   const int* target;
+  int* counts;                 // [row_ctas] listed rows of every CTA; null: the CTAs count them
   HeadMeta* meta;
   int* row_idx;
   __nv_bfloat16* out;          // [parts][r_pad][d_pad]
@@ -1260,9 +1261,38 @@ SMDM_DEV void put_weights(const RowsArgs& a, const WeightArgs& w, int cta) {
   }
 }
 
-// List the rows that take part, in order, and copy them together.  Every CTA reads all targets
-// (from L2) to know how many listed rows precede its own and whether all rows are listed; a
-// device-wide scan would take a second launch.  The CTAs behind row_ctas lay out the first
+// Sum over a CTA of 256 threads.
+SMDM_DEV int cta_sum(int s, int* red) {
+  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = s;
+  __syncthreads();
+  s = 0;
+  for (int w = 0; w < 8; ++w) s += red[w];
+  return s;
+}
+
+// How many rows of every CTA of head_rows_kernel take part.
+__global__ void __launch_bounds__(256) head_count_kernel(RowsArgs a) {
+  griddep_launch();
+  griddep_wait();
+  __shared__ int red[8];
+  const int r0 = blockIdx.x * a.per, r1 = min(a.rows, r0 + a.per);
+  int s = 0;
+  for (int base = r0 + threadIdx.x; base < r1; base += 8 * 256) {
+    int t[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) t[k] = base + k * 256 < r1 ? a.target[base + k * 256] : -1;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) s += t[k] >= 0 && t[k] < a.vocab;
+  }
+  s = cta_sum(s, red);
+  if (threadIdx.x == 0) a.counts[blockIdx.x] = s;
+}
+
+// List the rows that take part, in order, and copy them together.  Every CTA needs to know how
+// many listed rows precede its own and whether all rows are listed: up to kListRows rows it reads
+// all targets (from L2), which takes less time than a second launch; of more rows a kernel in
+// front has counted each CTA's.  The CTAs behind row_ctas lay out the first
 // piece's weights meanwhile, where those cannot be read in place.
 __global__ void __launch_bounds__(256) head_rows_kernel(RowsArgs a, WeightArgs w) {
   griddep_launch();
@@ -1272,42 +1302,36 @@ __global__ void __launch_bounds__(256) head_rows_kernel(RowsArgs a, WeightArgs w
     return;
   }
   __shared__ int red[2][8];
-  __shared__ int s_before, s_total;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int r0 = blockIdx.x * a.per, r1 = min(a.rows, r0 + a.per);
   int before = 0, total = 0;
-  for (int base = tid; base < a.rows; base += 8 * 256) {
-    int t[8];
+  if (a.counts) {
+    for (int i = tid; i < a.row_ctas; i += 256) {
+      const int c = a.counts[i];
+      total += c;
+      if (i < (int)blockIdx.x) before += c;
+    }
+  } else {
+    for (int base = tid; base < a.rows; base += 8 * 256) {
+      int t[8];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) t[k] = a.target[min(base + k * 256, a.rows - 1)];
+      for (int k = 0; k < 8; ++k) t[k] = a.target[min(base + k * 256, a.rows - 1)];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const int r = base + k * 256;
-      const bool on = r < a.rows && t[k] >= 0 && t[k] < a.vocab;
-      total += on;
-      if (r < r0) before += on;
+      for (int k = 0; k < 8; ++k) {
+        const int r = base + k * 256;
+        const bool on = r < a.rows && t[k] >= 0 && t[k] < a.vocab;
+        total += on;
+        if (r < r0) before += on;
+      }
     }
   }
-  for (int o = 16; o > 0; o >>= 1) {
-    before += __shfl_xor_sync(0xffffffffu, before, o);
-    total += __shfl_xor_sync(0xffffffffu, total, o);
-  }
-  if (lane == 0) { red[0][warp] = before; red[1][warp] = total; }
-  __syncthreads();
-  if (tid == 0) {
-    int b = 0, t = 0;
-    for (int w = 0; w < 8; ++w) { b += red[0][w]; t += red[1][w]; }
-    s_before = b;
-    s_total = t;
-    if (blockIdx.x == 0) {
-      a.meta->n = t;
-      a.meta->dense = (a.in_place && t == a.rows) ? 1 : 0;
-    }
-  }
-  __syncthreads();
-  const int n = s_total;
+  const int n = cta_sum(total, red[0]);
+  int at = cta_sum(before, red[1]);
   const bool dense = a.in_place && n == a.rows;
-  int at = s_before;
+  if (tid == 0 && blockIdx.x == 0) {
+    a.meta->n = n;
+    a.meta->dense = dense ? 1 : 0;
+  }
   if (a.ids)
     for (int v = blockIdx.x * 256 + tid; v < a.vocab; v += a.row_ctas * 256)
       a.ids[v] = make_int2(0, 0);
@@ -1613,6 +1637,9 @@ __global__ void __launch_bounds__(256)
 // ------------------------------------------------------------------------------------------
 // Host side
 // ------------------------------------------------------------------------------------------
+// Rows up to which head_rows_kernel's CTAs read all targets, and its CTAs at most.
+constexpr int kListRows = 16384, kListCtas = 1024;
+
 size_t up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
 int sm_count() {
@@ -1632,7 +1659,7 @@ struct Plan {
   bool staged;        // weights go through a bf16 copy of each piece
   int piece, n_pieces;
   bool rest;          // D's remainders at the targets
-  size_t meta, row_idx, hid, part, tlogit, wst, dlog, acc, row_tgt, delta, ids, next, rest_rows, total;
+  size_t meta, counts, row_idx, hid, part, tlogit, wst, dlog, acc, row_tgt, delta, ids, next, rest_rows, total;
   int cfg, cfg_g;     // tile configuration of the logits' product and of the gradients'
   int splits, n_part;
   int narrow;         // > 0: head_narrow_kernel, with this many vocabulary slots (= splits)
@@ -1743,6 +1770,7 @@ Plan make_plan(int rows, int d, int vocab, long long ld_head, bool f32, bool gra
     return o;
   };
   p.meta = take(256);
+  p.counts = take(rows > kListRows ? kListCtas * 4 : 0);
   p.row_idx = take((size_t)p.r_pad * 4);
   p.hid = take((size_t)p.parts * p.r_pad * p.d_pad * 2);
   if (!grad) {
@@ -1909,7 +1937,7 @@ struct Call {
     r.d_pad = p.d_pad;
     r.vocab = h.vocab;
     r.r_pad = p.r_pad;
-    r.per = std::max(8, (h.rows + 1023) / 1024);   // (a row per warp)
+    r.per = std::max(8, (h.rows + kListCtas - 1) / kListCtas);   // (a row per warp)
     r.row_ctas = (h.rows + r.per - 1) / r.per;
     r.f32 = h.f32;
     r.in_place = in_place;
@@ -1918,6 +1946,7 @@ struct Call {
     r.ld = h.ld_hidden;
     r.hidden = h.hidden;
     r.target = h.target;
+    r.counts = h.rows > kListRows ? at<int>(p.counts) : nullptr;
     r.meta = at<HeadMeta>(p.meta);
     r.row_idx = at<int>(p.row_idx);
     r.out = at<__nv_bfloat16>(p.hid);
@@ -1954,12 +1983,15 @@ struct Call {
   // row of tiles either way, and a row of the product that takes no part touches no other.  (Not
   // the gradient: dW sums over the rows.)
   bool listed() const { return !(loss && in_place && !p.staged && h.rows <= 128); }
+  // Launches of rows().
+  int row_launches() const { return !listed() ? 0 : h.rows > kListRows ? 2 : 1; }
   HeadMeta* meta() const { return listed() ? at<HeadMeta>(p.meta) : nullptr; }
   // The rows that take part, and the first piece's weights.
   cudaError_t rows(cudaStream_t st) const {
     if (!listed()) return cudaSuccess;
     const RowsArgs r = row_args();
     const WeightArgs w = weight_args(0, std::min(p.piece, h.vocab));
+    if (r.counts) TRY(launch_pdl(head_count_kernel, dim3(r.row_ctas), dim3(256), 0, st, 1, r));
     return launch_pdl(head_rows_kernel, dim3(r.row_ctas + w.ctas), dim3(256), 0, st, 1, r, w);
   }
   // The weights of a later piece: read in place, or copied into the workspace.
@@ -2023,14 +2055,15 @@ int head_loss_launches(const HeadArgs& a) {
   const Call c(a, false);
   const Plan& p = c.p;
   if (p.few) return 1 + head_few_groups(a.rows, a.d);
-  return 1 + (c.listed() ? 1 : 0) + p.n_pieces + (p.staged ? p.n_pieces - 1 : 0);
+  return 1 + c.row_launches() + p.n_pieces + (p.staged ? p.n_pieces - 1 : 0);
 }
 
 int head_grad_launches(const HeadArgs& a) {
-  const Plan p = make_plan(a.rows, a.d, a.vocab, a.ld_head, a.f32, true);
+  const Call c(a, true);
+  const Plan& p = c.p;
   if (p.few) return 1 + head_few_groups(a.rows, a.d) + (a.grad_hidden ? 1 : 0);
   const bool sums = p.narrow || p.splits > 1 || p.n_pieces > 1;
-  return 1 + (p.rest && a.grad_head ? 3 : 2) * p.n_pieces + (p.staged ? p.n_pieces - 1 : 0) + (sums && a.grad_hidden ? 1 : 0);
+  return c.row_launches() + (p.rest && a.grad_head ? 3 : 2) * p.n_pieces + (p.staged ? p.n_pieces - 1 : 0) + (sums && a.grad_hidden ? 1 : 0);
 }
 
 cudaError_t launch_head_loss(const HeadArgs& h, cudaStream_t st) {
