@@ -456,7 +456,7 @@ __global__ void __launch_bounds__(256) embed_kernel(EmbedArgs a) {
 
 // Sorting (id, row) pairs as 64-bit words: all different, so any sorting method is a stable one
 // and the sums below always add a token's rows in the same order.
-constexpr int kChunk = 2048;
+constexpr int kChunk = kSortChunk;
 
 // Each of the first `chunks` CTAs sorts one chunk of `size` words (a power of two, up to kChunk): a
 // bitonic network, two words per thread.  Exchanges over distances below 64 stay within a warp
@@ -986,36 +986,55 @@ size_t embed_grad_bytes(int rows, int d, int n_emb) {
   return std::max<size_t>(256, embed_plan(rows, d).total);
 }
 
+// Runs merged per level: as few as one level takes, up to 32 (every search reads the list from L2).
+static int merge_ways(int n) {
+  const int chunks = (n + kChunk - 1) / kChunk;
+  return chunks <= 8 ? 8 : chunks <= 16 ? 16 : 32;
+}
+
+int sort_ids_launches(int n) {
+  int k = 1;
+  for (long long run = kChunk; run < n; run *= merge_ways(n)) ++k;
+  return k;
+}
+
+cudaError_t launch_sort_ids(const int* ids, int n, int n_ids, unsigned long long* a,
+                            unsigned long long* b, void* clear, size_t clear_bytes,
+                            uint32_t* status, cudaStream_t st, const unsigned long long** sorted) {
+  static_assert(kChunk == 1 << 11, "the 32-bit words hold a place of 11 bits");
+  auto sort = n_ids < (1 << 21) - 1 ? embed_sort_kernel<unsigned>
+                                    : embed_sort_kernel<unsigned long long>;
+  const int chunks = (n + kChunk - 1) / kChunk;
+  int size = 256;
+  while (size < kChunk && size < n) size *= 2;
+  const int threads = size / 2;
+  const int clears = (int)std::min<size_t>((size_t)device_sms() * (2048 / threads),
+                                           (clear_bytes + 16 * threads - 1) / (16 * threads));
+  cudaError_t e = launch_pdl(sort, dim3(chunks + clears), dim3(threads), 0, st, 1, ids, n, n_ids,
+                             size, chunks, a, static_cast<uint8_t*>(clear), clear_bytes, status);
+  if (e != cudaSuccess) return e;
+  const int ways = merge_ways(n);
+  for (long long run = kChunk; run < n; run *= ways) {
+    const long long searches = (long long)n * ways;
+    e = launch_pdl(embed_merge_kernel, dim3((unsigned)((searches + 255) / 256)), dim3(256), 0, st, 1,
+                   (const unsigned long long*)a, n, (int)run, ways, b);
+    if (e != cudaSuccess) return e;
+    std::swap(a, b);
+  }
+  *sorted = a;
+  return cudaSuccess;
+}
+
 cudaError_t launch_embed_grad(const EmbedArgs& a, cudaStream_t st) {
   const EmbedPlan p = embed_plan(a.rows, a.d);
   uint8_t* ws = static_cast<uint8_t*>(a.ws);
-  unsigned long long* list[2] = {reinterpret_cast<unsigned long long*>(ws + p.list[0]),
-                                 reinterpret_cast<unsigned long long*>(ws + p.list[1])};
-  static_assert(kChunk == 1 << 11, "the 32-bit words hold a place of 11 bits");
-  auto sort = a.n_emb < (1 << 21) - 1 ? embed_sort_kernel<unsigned>
-                                      : embed_sort_kernel<unsigned long long>;
-  int size = 256;
-  while (size < kChunk && size < a.rows) size *= 2;
-  const size_t bytes = (size_t)a.n_emb * a.d * (a.f32 ? 4 : 2);
-  const int threads = size / 2;
-  const int clear = (int)std::min<size_t>((size_t)device_sms() * (2048 / threads),
-                                          (bytes + 16 * threads - 1) / (16 * threads));
-  cudaError_t e = launch_pdl(sort, dim3(p.chunks + clear), dim3(threads), 0, st, 1, a.ids, a.rows,
-                             a.n_emb, size, p.chunks, list[0], static_cast<uint8_t*>(a.grad_table),
-                             bytes, a.status);
-  if (e != cudaSuccess) return e;
-  int cur = 0;
-  // as few runs per level as one level takes, up to 32 (every search reads the list from L2)
-  const int ways = p.chunks <= 8 ? 8 : p.chunks <= 16 ? 16 : 32;
-  for (long long run = kChunk; run < a.rows; run *= ways, cur ^= 1) {
-    const long long searches = (long long)a.rows * ways;
-    e = launch_pdl(embed_merge_kernel, dim3((unsigned)((searches + 255) / 256)), dim3(256), 0, st, 1,
-                   (const unsigned long long*)list[cur], a.rows, (int)run, ways, list[cur ^ 1]);
-    if (e != cudaSuccess) return e;
-  }
   EmbedGradArgs g{};
   g.e = a;
-  g.list = list[cur];
+  const cudaError_t e = launch_sort_ids(
+      a.ids, a.rows, a.n_emb, reinterpret_cast<unsigned long long*>(ws + p.list[0]),
+      reinterpret_cast<unsigned long long*>(ws + p.list[1]), a.grad_table,
+      (size_t)a.n_emb * a.d * (a.f32 ? 4 : 2), a.status, st, &g.list);
+  if (e != cudaSuccess) return e;
   g.part = reinterpret_cast<float*>(ws + p.part);
   g.per = p.per;
   g.pieces = p.pieces;

@@ -46,6 +46,13 @@ cudaError_t launch_train_rmsnorm_grad(const RmsArgs& a, cudaStream_t st);
 cudaError_t launch_embed(const EmbedArgs& a, cudaStream_t st);
 size_t embed_grad_bytes(int rows, int d, int n_emb);
 cudaError_t launch_embed_grad(const EmbedArgs& a, cudaStream_t st);
+// (id << 32 | row) of n rows in order, ids outside [0, n_ids) as n_ids; in a or b, n words each (b
+// is used above kSortChunk rows).  Bytes at `clear` are set to 0 meanwhile.
+constexpr int kSortChunk = 2048;
+int sort_ids_launches(int n);
+cudaError_t launch_sort_ids(const int* ids, int n, int n_ids, unsigned long long* a,
+                            unsigned long long* b, void* clear, size_t clear_bytes,
+                            uint32_t* status, cudaStream_t st, const unsigned long long** sorted);
 // out[i] = x[index[i]], rows of d fp32 (index out of [0, n): row 0 and kStatusBounds).
 cudaError_t launch_gather_f32(const float* x, const int* index, int rows, int n, int d, float* out,
                               uint32_t* status, cudaStream_t st);

@@ -35,6 +35,7 @@
 #include <algorithm>
 #include <type_traits>
 
+#include "ends.h"
 #include "tensormap.h"
 
 namespace smdm {
@@ -86,8 +87,8 @@ struct HeadDev {
   // D
   const int* row_tgt;       // [r_pad] targets of the listed rows
   float* delta;             // [r_pad] remainder of D at the row's target; null: not kept
-  int2* ids;                // [vocab] a listed row with the id as its target, and their number
-  int* next;                // [r_pad] the next listed row with the same target
+  const int* run;           // [r_pad] rows with its target if it is the first of them, else 0
+  int2* ids;                // [vocab] first listed row with the id as its target, and their number
   const __nv_bfloat16* rest;   // [r_pad][d_pad] sums of the remainders' part of dW (see RestArgs)
   const void* hidden;       // the caller's rows
   long long ld_hidden;
@@ -763,13 +764,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (!F32 && a.delta && row < n && rel >= 0 && rel < 32 * PC) {
               a.delta[row] = tv - __bfloat162float(__float2bfloat16_rn(tv));
-              if (a.ids) {
-                // (which row comes first depends on timing; the sums do not: they are made in
-                // row order)
-                int2* id = a.ids + (col + rel + a.v0);
-                a.next[row] = atomicExch(&id->x, row);
-                atomicAdd(&id->y, 1);
-              }
+              const int k = a.ids ? a.run[row] : 0;
+              if (k > 0) a.ids[a.v0 + col + rel] = make_int2(row, k);
             }
           }
           // the parts one after the other, each the rounding of what the ones before leave (more
@@ -1166,6 +1162,9 @@ struct RowsArgs {
   int* row_idx;
   __nv_bfloat16* out;          // [parts][r_pad][d_pad]
   int* row_tgt;                // [r_pad] targets of the listed rows; null: not wanted
+  int* perm;                   // [r_pad] listed rows in order of (target, row); null: not wanted
+  int* run;                    // [r_pad] (see HeadDev)
+  int* inv;                    // instead of those two, with counts: caller's row -> listed row
   int2* ids;                   // [vocab] to clear; null: not wanted
   float *nll, *lse;            // loss: zero for the rows that take no part
   void* grad_hidden;           // gradient: likewise
@@ -1294,6 +1293,11 @@ __global__ void __launch_bounds__(256) head_count_kernel(RowsArgs a) {
 // all targets (from L2), which takes less time than a second launch; of more rows a kernel in
 // front has counted each CTA's.  The CTAs behind row_ctas lay out the first
 // piece's weights meanwhile, where those cannot be read in place.
+// For the remainders of D the rows are also put in order of their targets: up to kListRows rows
+// with kOwn rows per CTA, which compares them with all targets as it reads them; more rows are
+// sorted (launch_sort_ids).
+constexpr int kOwn = 8;
+
 __global__ void __launch_bounds__(256) head_rows_kernel(RowsArgs a, WeightArgs w) {
   griddep_launch();
   griddep_wait();
@@ -1304,8 +1308,45 @@ __global__ void __launch_bounds__(256) head_rows_kernel(RowsArgs a, WeightArgs w
   __shared__ int red[2][8];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int r0 = blockIdx.x * a.per, r1 = min(a.rows, r0 + a.per);
+  __shared__ int2 s_rank[8][kOwn];
   int before = 0, total = 0;
-  if (a.counts) {
+  if (a.perm) {
+    // as below, and for the CTA's own rows (kOwn at most) how many listed rows have a smaller
+    // target, how many the same, and how many of those come before
+    int own[kOwn], less[kOwn], same[kOwn];       // same: << 16 those before
+#pragma unroll
+    for (int j = 0; j < kOwn; ++j) {
+      own[j] = r0 + j < r1 ? a.target[r0 + j] : -1;
+      less[j] = same[j] = 0;
+    }
+    for (int base = tid; base < a.rows; base += 8 * 256) {
+      int t[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) t[k] = a.target[min(base + k * 256, a.rows - 1)];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int r = base + k * 256;
+        const bool on = r < a.rows && t[k] >= 0 && t[k] < a.vocab;
+        if (!on) t[k] = 0x7fffffff;              // neither below nor equal to any target
+        total += on;
+        before += on && r < r0;
+        const int one = r < r0 ? 0x10001 : 1;    // (the own rows among themselves: below)
+#pragma unroll
+        for (int j = 0; j < kOwn; ++j) {
+          less[j] += t[k] < own[j];
+          same[j] += t[k] == own[j] ? one : 0;
+        }
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < kOwn; ++j) {
+      const int x = __reduce_add_sync(0xffffffffu, less[j]);
+      int y = __reduce_add_sync(0xffffffffu, same[j]);
+      if (warp == 0)
+        for (int i = 0; i < j; ++i) y += own[i] == own[j] ? 0x10000 : 0;
+      if (lane == 0) s_rank[warp][j] = make_int2(x, y);
+    }
+  } else if (a.counts) {
     for (int i = tid; i < a.row_ctas; i += 256) {
       const int c = a.counts[i];
       total += c;
@@ -1328,13 +1369,13 @@ __global__ void __launch_bounds__(256) head_rows_kernel(RowsArgs a, WeightArgs w
   const int n = cta_sum(total, red[0]);
   int at = cta_sum(before, red[1]);
   const bool dense = a.in_place && n == a.rows;
+  if (a.ids)
+    for (int v = blockIdx.x * 256 + tid; v < a.vocab; v += a.row_ctas * 256)
+      a.ids[v] = make_int2(0, 0);
   if (tid == 0 && blockIdx.x == 0) {
     a.meta->n = n;
     a.meta->dense = dense ? 1 : 0;
   }
-  if (a.ids)
-    for (int v = blockIdx.x * 256 + tid; v < a.vocab; v += a.row_ctas * 256)
-      a.ids[v] = make_int2(0, 0);
   // 32 rows at a time: every warp works out the same listed positions, then takes every 8th row
   for (int b = r0; b < r1; b += 32) {
     const int r = b + lane;
@@ -1348,6 +1389,16 @@ __global__ void __launch_bounds__(256) head_rows_kernel(RowsArgs a, WeightArgs w
       if (on) {
         a.row_idx[pos] = r;
         if (a.row_tgt) a.row_tgt[pos] = t;
+        if (a.inv) a.inv[r] = pos;
+        if (a.perm) {
+          int2 k = make_int2(0, 0);
+          for (int i = 0; i < 8; ++i) {
+            k.x += s_rank[i][r - r0].x;
+            k.y += s_rank[i][r - r0].y;
+          }
+          a.perm[k.x + (k.y >> 16)] = pos;
+          a.run[pos] = k.y < 0x10000 ? k.y : 0;
+        }
       } else if (a.nll) {
         a.nll[r] = 0.f;
         a.lse[r] = 0.f;
@@ -1385,18 +1436,42 @@ __global__ void __launch_bounds__(256) head_rows_kernel(RowsArgs a, WeightArgs w
   }
 }
 
+// The order of the listed rows by (target, row), and `run` of every row, from the sorted (target,
+// caller's row) words.
+__global__ void __launch_bounds__(256)
+    head_perm_kernel(const HeadMeta* meta, const unsigned long long* sorted, const int* inv,
+                     int* perm, int* run) {
+  griddep_launch();
+  griddep_wait();
+  const int n = meta->n, p = blockIdx.x * 256 + threadIdx.x;
+  if (p >= n) return;
+  const unsigned long long w = sorted[p];
+  const unsigned key = (unsigned)(w >> 32);
+  const int row = inv[(unsigned)w];
+  perm[p] = row;
+  int lo = p + 1, hi = n;                    // the end of the rows with this target
+  if (p > 0 && (unsigned)(sorted[p - 1] >> 32) == key) lo = hi = p;
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if ((unsigned)(sorted[mid] >> 32) == key) lo = mid + 1;
+    else hi = mid;
+  }
+  run[row] = lo - p;
+}
+
 // rest[x] = the sum of delta_r h_r over the listed rows r with one target, in row order, for the
-// targets of a piece that two or more rows have (one row's is added as it lies); x is the row
-// where their chain begins.  A warp takes 256 columns and looks at four listed rows.  Up to 32 rows it
-// finds by the chain and puts in order; more it looks up among all listed rows, 256 at a time.
-// Summed in fp32, eight rows in flight; kept in bf16, which is 2^-9 of 2^-9 of D's part of dW.
-// 4096 rows of 4096 over 8192 ids: 13.6 us, most of them the latency of looking.
+// targets of a piece that two or more rows have (one row's is added as it lies); x is the first of
+// them.  A CTA takes 256 columns and the targets that begin at 32 places of the rows in order of
+// their targets: a warp each, all warps together for one of more than kRestLong rows.  Summed in
+// fp32, eight rows in flight per warp; kept in bf16, which is 2^-9 of 2^-9 of D's part of dW.
+// 3072 rows of 4096 over 8192 ids: 13 us, mostly the latency of five loads in a row; 786432 rows of
+// 64 over 64 ids: 0.5 ms of 6.
 struct RestArgs {
   const HeadMeta* meta;
   const int* row_tgt;
+  const int* perm;
+  const int* run;
   const float* delta;
-  const int2* ids;
-  const int* next;
   const void* hidden;          // the caller's rows
   long long ld_hidden;
   const __nv_bfloat16* hid;    // the listed rows
@@ -1404,47 +1479,43 @@ struct RestArgs {
   __nv_bfloat16* out;          // [r_pad][d_pad]
 };
 
-constexpr int kRestWarps = 8, kRestRows = 4;
+constexpr int kRestWarps = 8, kRestLong = 64;
 
 __global__ void __launch_bounds__(kRestWarps * 32) head_rest_kernel(RestArgs a) {
   griddep_launch();
   griddep_wait();
-  __shared__ int lists[kRestWarps][288];
+  __shared__ __align__(16) float part[kRestWarps][256];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int n = a.meta->n;
-  const long long job = (long long)blockIdx.x * kRestWarps + warp;
-  const int row0 = (int)(job / a.slabs) * kRestRows, c = (int)(job % a.slabs) * 256 + lane * 8;
-  if (row0 >= n) return;
+  const int p0 = (int)(blockIdx.x / a.slabs) * 32, c = (int)(blockIdx.x % a.slabs) * 256 + lane * 8;
+  if (p0 >= n) return;
   // both kinds of rows start on 16 bytes and fill 16-byte words
   const bool dense = a.meta->dense != 0;
   const __nv_bfloat16* h = dense ? static_cast<const __nv_bfloat16*>(a.hidden) : a.hid;
   const long long ld = dense ? a.ld_hidden : a.d_pad;
   const bool in = c < (dense ? a.d : a.d_pad);
-  int* list = lists[warp];
-  int my_t = -1, my_count = 0;
-  if (lane < kRestRows && row0 + lane < n) {
-    my_t = a.row_tgt[row0 + lane];
-    if (my_t >= a.v0 && my_t < a.v0 + a.vc) {
-      const int2 id = a.ids[my_t];
-      if (id.x == row0 + lane) my_count = id.y;
-    }
+  // the target that begins at this lane's place
+  int row = 0, count = 0;
+  if (p0 + lane < n) {
+    row = a.perm[p0 + lane];
+    const int t = a.row_tgt[row];
+    if (t >= a.v0 && t < a.v0 + a.vc) count = a.run[row];
   }
-  for (uint32_t m = __ballot_sync(0xffffffffu, my_count > 1); m; m &= m - 1) {
-    const int i = __ffs(m) - 1, row = row0 + i;
-    const int t = __shfl_sync(0xffffffffu, my_t, i);
-    int left = __shfl_sync(0xffffffffu, my_count, i);
-    float s[8];
+  float s[8];
+  // the rows at the places [from, to)
+  auto sum = [&](int from, int to) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) s[j] = 0.f;
-    // the rows r of lanes 0 .. cnt - 1, in the lanes' order
-    auto add = [&](int r, int cnt) {
+    for (; from < to; from += 32) {
+      const int cnt = min(32, to - from);
+      const int r = lane < cnt ? a.perm[from + lane] : 0;
       const float delta = lane < cnt ? a.delta[r] : 0.f;
       for (int e0 = 0; e0 < cnt; e0 += 8) {
         uint4 x[8];
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-          const int from = __shfl_sync(0xffffffffu, r, e0 + k);
-          x[k] = in && e0 + k < cnt ? *reinterpret_cast<const uint4*>(h + (size_t)from * ld + c)
+          const int e = __shfl_sync(0xffffffffu, r, e0 + k);
+          x[k] = in && e0 + k < cnt ? *reinterpret_cast<const uint4*>(h + (size_t)e * ld + c)
                                     : make_uint4(0, 0, 0, 0);
         }
 #pragma unroll
@@ -1458,56 +1529,40 @@ __global__ void __launch_bounds__(kRestWarps * 32) head_rest_kernel(RestArgs a) 
           }
         }
       }
-    };
-    if (left <= 32) {
-      int r = row, mine = 0x7fffffff;
-      for (int k = 0; k < left; ++k) {
-        if (lane == k) mine = r;
-        if (k + 1 < left) r = a.next[r];
-      }
-      int rank = 0;
-      for (int k = 0; k < left; ++k) rank += __shfl_sync(0xffffffffu, mine, k) < mine;
-      if (lane < left) list[rank] = mine;
-      __syncwarp();
-      mine = lane < left ? list[lane] : row;
-      __syncwarp();
-      add(mine, left);
-    } else {
-      int cnt = 0;
-      for (int base = 0; base < n; base += 256) {
-        int v[8];
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const int r = base + k * 32 + lane;
-          v[k] = r < n ? a.row_tgt[r] : -1;
-        }
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const uint32_t hit = __ballot_sync(0xffffffffu, v[k] == t);
-          if (v[k] == t) list[cnt + __popc(hit & ((1u << lane) - 1u))] = base + k * 32 + lane;
-          cnt += __popc(hit);
-          left -= __popc(hit);
-        }
-        __syncwarp();
-        // 32 rows at a time; the last few wait for more
-        const bool end = left <= 0 || base + 256 >= n;
-        int e0 = 0;
-        for (; e0 + 32 <= cnt || (end && e0 < cnt); e0 += 32)
-          add(e0 + lane < cnt ? list[e0 + lane] : row, min(32, cnt - e0));
-        cnt = max(0, cnt - e0);
-        const int keep = lane < cnt ? list[e0 + lane] : 0;
-        __syncwarp();
-        if (lane < cnt) list[lane] = keep;
-        if (end) break;
-      }
     }
-    if (c < a.d_pad) {
-      uint32_t w[4];
+  };
+  auto put = [&](int to) {
+    if (c >= a.d_pad) return;
+    uint32_t w[4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) w[j] = pack_bf16(s[2 * j], s[2 * j + 1]);
-      *reinterpret_cast<uint4*>(a.out + (size_t)row * a.d_pad + c) =
-          make_uint4(w[0], w[1], w[2], w[3]);
+    for (int j = 0; j < 4; ++j) w[j] = pack_bf16(s[2 * j], s[2 * j + 1]);
+    *reinterpret_cast<uint4*>(a.out + (size_t)to * a.d_pad + c) = make_uint4(w[0], w[1], w[2], w[3]);
+  };
+  int turn = 0;
+  for (uint32_t m = __ballot_sync(0xffffffffu, count > 1 && count <= kRestLong); m; m &= m - 1, ++turn) {
+    if (turn % kRestWarps != warp) continue;
+    const int i = __ffs(m) - 1;
+    sum(p0 + i, p0 + i + __shfl_sync(0xffffffffu, count, i));
+    put(__shfl_sync(0xffffffffu, row, i));
+  }
+  for (uint32_t m = __ballot_sync(0xffffffffu, count > kRestLong); m; m &= m - 1) {
+    const int i = __ffs(m) - 1, k = __shfl_sync(0xffffffffu, count, i);
+    const int per = (k + kRestWarps - 1) / kRestWarps, from = p0 + i + min(k, warp * per);
+    sum(from, min(p0 + i + k, from + per));
+#pragma unroll
+    for (int j = 0; j < 8; j += 4)
+      *reinterpret_cast<float4*>(&part[warp][lane * 8 + j]) =
+          make_float4(s[j], s[j + 1], s[j + 2], s[j + 3]);
+    __syncthreads();
+    if (warp == 0) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        s[j] = 0.f;
+        for (int w = 0; w < kRestWarps; ++w) s[j] += part[w][lane * 8 + j];
+      }
+      put(__shfl_sync(0xffffffffu, row, i));
     }
+    __syncthreads();
   }
 }
 
@@ -1638,7 +1693,7 @@ __global__ void __launch_bounds__(256)
 // Host side
 // ------------------------------------------------------------------------------------------
 // Rows up to which head_rows_kernel's CTAs read all targets, and its CTAs at most.
-constexpr int kListRows = 16384, kListCtas = 1024;
+constexpr int kListRows = 8192, kListCtas = 1024;
 
 size_t up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
@@ -1659,7 +1714,7 @@ struct Plan {
   bool staged;        // weights go through a bf16 copy of each piece
   int piece, n_pieces;
   bool rest;          // D's remainders at the targets
-  size_t meta, counts, row_idx, hid, part, tlogit, wst, dlog, acc, row_tgt, delta, ids, next, rest_rows, total;
+  size_t meta, counts, row_idx, hid, part, tlogit, wst, dlog, acc, row_tgt, delta, ids, run, perm, inv, sort[2], rest_rows, total;
   int cfg, cfg_g;     // tile configuration of the logits' product and of the gradients'
   int splits, n_part;
   int narrow;         // > 0: head_narrow_kernel, with this many vocabulary slots (= splits)
@@ -1784,7 +1839,12 @@ Plan make_plan(int rows, int d, int vocab, long long ld_head, bool f32, bool gra
       p.row_tgt = take((size_t)p.r_pad * 4);
       p.delta = take((size_t)p.r_pad * 4);
       p.ids = take((size_t)vocab * 8);
-      p.next = take((size_t)p.r_pad * 4);
+      p.run = take((size_t)p.r_pad * 4);
+      p.perm = take((size_t)p.r_pad * 4);
+      if (rows > kListRows) {
+        p.inv = take((size_t)rows * 4);
+        for (size_t& k : p.sort) k = take((size_t)rows * 8);
+      }
       p.rest_rows = take((size_t)p.r_pad * p.d_pad * 2);
     }
     if (p.narrow || p.splits > 1 || p.n_pieces > 1) p.acc = take((size_t)p.splits * p.r_pad * p.d_pad * 4);
@@ -1937,7 +1997,8 @@ struct Call {
     r.d_pad = p.d_pad;
     r.vocab = h.vocab;
     r.r_pad = p.r_pad;
-    r.per = std::max(8, (h.rows + kListCtas - 1) / kListCtas);   // (a row per warp)
+    const bool order = p.rest && h.grad_head, counted = h.rows > kListRows;
+    r.per = order && !counted ? kOwn : std::max(8, (h.rows + kListCtas - 1) / kListCtas);
     r.row_ctas = (h.rows + r.per - 1) / r.per;
     r.f32 = h.f32;
     r.in_place = in_place;
@@ -1946,7 +2007,7 @@ struct Call {
     r.ld = h.ld_hidden;
     r.hidden = h.hidden;
     r.target = h.target;
-    r.counts = h.rows > kListRows ? at<int>(p.counts) : nullptr;
+    r.counts = counted ? at<int>(p.counts) : nullptr;
     r.meta = at<HeadMeta>(p.meta);
     r.row_idx = at<int>(p.row_idx);
     r.out = at<__nv_bfloat16>(p.hid);
@@ -1954,7 +2015,13 @@ struct Call {
     r.lse = h.lse_out;
     if (p.rest) {
       r.row_tgt = at<int>(p.row_tgt);
-      if (h.grad_head) r.ids = at<int2>(p.ids);
+      if (order) r.ids = at<int2>(p.ids);
+      if (order && counted) {
+        r.inv = at<int>(p.inv);
+      } else if (order) {
+        r.perm = at<int>(p.perm);
+        r.run = at<int>(p.run);
+      }
     }
     r.grad_hidden = h.grad_hidden;
     r.gvec = whole_words(h.grad_hidden, h.d);
@@ -1984,7 +2051,11 @@ struct Call {
   // the gradient: dW sums over the rows.)
   bool listed() const { return !(loss && in_place && !p.staged && h.rows <= 128); }
   // Launches of rows().
-  int row_launches() const { return !listed() ? 0 : h.rows > kListRows ? 2 : 1; }
+  int row_launches() const {
+    if (!listed()) return 0;
+    if (h.rows <= kListRows) return 1;
+    return 2 + (p.rest && h.grad_head ? sort_ids_launches(h.rows) + 1 : 0);
+  }
   HeadMeta* meta() const { return listed() ? at<HeadMeta>(p.meta) : nullptr; }
   // The rows that take part, and the first piece's weights.
   cudaError_t rows(cudaStream_t st) const {
@@ -1992,7 +2063,14 @@ struct Call {
     const RowsArgs r = row_args();
     const WeightArgs w = weight_args(0, std::min(p.piece, h.vocab));
     if (r.counts) TRY(launch_pdl(head_count_kernel, dim3(r.row_ctas), dim3(256), 0, st, 1, r));
-    return launch_pdl(head_rows_kernel, dim3(r.row_ctas + w.ctas), dim3(256), 0, st, 1, r, w);
+    TRY(launch_pdl(head_rows_kernel, dim3(r.row_ctas + w.ctas), dim3(256), 0, st, 1, r, w));
+    if (!r.inv) return cudaSuccess;
+    const unsigned long long* sorted = nullptr;
+    TRY(launch_sort_ids(h.target, h.rows, h.vocab, at<unsigned long long>(p.sort[0]),
+                        at<unsigned long long>(p.sort[1]), nullptr, 0, nullptr, st, &sorted));
+    return launch_pdl(head_perm_kernel, dim3((h.rows + 255) / 256), dim3(256), 0, st, 1,
+                      (const HeadMeta*)r.meta, sorted, (const int*)r.inv, at<int>(p.perm),
+                      at<int>(p.run));
   }
   // The weights of a later piece: read in place, or copied into the workspace.
   cudaError_t weights(int v0, int vc, cudaStream_t st) const {
@@ -2123,8 +2201,8 @@ cudaError_t launch_head_grad(const HeadArgs& h, cudaStream_t st) {
       a.row_tgt = c.at<int>(p.row_tgt);
       a.delta = c.at<float>(p.delta);
       if (h.grad_head) {
+        a.run = c.at<int>(p.run);
         a.ids = c.at<int2>(p.ids);
-        a.next = c.at<int>(p.next);
         a.hidden = h.hidden;
         a.ld_hidden = h.ld_hidden;
         a.hid = c.at<__nv_bfloat16>(p.hid);
@@ -2138,12 +2216,11 @@ cudaError_t launch_head_grad(const HeadArgs& h, cudaStream_t st) {
     TRY(launch_mode<kDlog>(p.parts, p.cfg, m, a, units, c.sms, st));
     if (a.rest) {
       const int slabs = (p.d_pad + 255) / 256;
-      const RestArgs r{a.meta, a.row_tgt, a.delta, a.ids, a.next, h.hidden, h.ld_hidden,
+      const RestArgs r{a.meta, a.row_tgt, c.at<int>(p.perm), a.run, a.delta, h.hidden, h.ld_hidden,
                        c.at<__nv_bfloat16>(p.hid), h.d, p.d_pad, slabs, v0, vc,
                        c.at<__nv_bfloat16>(p.rest_rows)};
-      const long long jobs = (long long)((h.rows + kRestRows - 1) / kRestRows) * slabs;
-      TRY(launch_pdl(head_rest_kernel, dim3((unsigned)((jobs + kRestWarps - 1) / kRestWarps)),
-                     dim3(kRestWarps * 32), 0, st, 1, r));
+      const long long ctas = (long long)((h.rows + 31) / 32) * slabs;
+      TRY(launch_pdl(head_rest_kernel, dim3((unsigned)ctas), dim3(kRestWarps * 32), 0, st, 1, r));
     }
     // both products of D: 64-row boxes for the MN-major operands
     if (!c.hidden_maps(&m.h, &m.hc, 64) || !c.weight_map(&m.w, vc, 64) ||

@@ -4,12 +4,13 @@ import pytest
 import torch
 
 from test_training_ends import BF16, F32, Head, _gpu, gen  # noqa: F401
+from test_training_ends_precision import norm_error_bounds
 
 pytestmark = pytest.mark.gpu
 
 
 @pytest.mark.parametrize("rows,d,vocab,dt,ignored,pad", [
-    (16384, 64, 130, BF16, 0.3, 0), (16385, 64, 130, BF16, 0.3, 0), (70001, 72, 100, BF16, 0.0, 0),
+    (8192, 64, 130, BF16, 0.3, 0), (8193, 64, 130, BF16, 0.3, 0), (16385, 64, 130, BF16, 0.3, 0), (70001, 72, 100, BF16, 0.0, 0),
     (70001, 72, 100, BF16, 0.9, 3), (20000, 30, 70, F32, 0.5, 0), (40000, 64, 9, BF16, 0.9999, 8)])
 def test_head_of_many_rows(rows, d, vocab, dt, ignored, pad):
     x = Head(rows, d, vocab, dt, ignored, pad, seed=rows + vocab)
@@ -33,3 +34,20 @@ def test_head_of_many_rows_with_few_or_none_that_take_part():
     assert (nll[:49999] == 0).all() and nll[49999] > 0
     gh, gw = x.grad(lse)
     assert (gh[:49999] == 0).all() and (gh[49999] != 0).any() and (gw[7] != 0).any()
+
+
+@pytest.mark.parametrize("rows,vocab,hot", [(8000, 64, 0.0), (8000, 5000, 0.6), (30000, 64, 0.0),
+                                            (30000, 5000, 0.6), (9000, 3, 0.0), (40000, 70000, 0.3)])
+def test_head_gradient_of_many_rows_with_one_target(rows, vocab, hot):
+    """Hundreds or thousands of rows share a target: their remainders are summed over the row's id."""
+    x = Head(rows, 72, vocab, BF16, 0.2, seed=vocab)
+    if hot:
+        x.target[torch.rand(rows, generator=gen(2), device="cuda") < hot] = vocab - 2
+    x.weight.fill_(1 / rows)
+    _, lse = x.check_loss()
+    a = x.check_grad(lse)
+    ref, bound = norm_error_bounds(x, lse)[1]
+    err = (a[1].to(torch.float64) - ref).norm().item()
+    assert err <= 1.05 * bound, err / bound
+    b = x.grad(lse)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
