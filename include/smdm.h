@@ -444,13 +444,16 @@ smdm_status smdm_embed_grad(const smdm_embed_shape* shape, const int32_t* d_ids,
 
 /* The loss of the training form: smdm_forward_stepcausal's forward over n step-labelled rows,
  * then for the rows in d_loss_rows (n_rows of them, at most max_rows) the final RMSNorm and
- * smdm_head_loss against d_target [n_rows] instead of logits.  The normalised rows are rounded
- * to the model's dtype and multiplied with the lm_head as given.
+ * smdm_head_loss against d_target [n_rows] instead of logits.  The logits are those of
+ * smdm_forward_stepcausal (for a bf16 model fp16 rows and the handle's fp16 copy of lm_head); the
+ * gradients are products with the normalised rows in the model's dtype and lm_head as given.
  *  - d_nll, d_lse: fp32 [n_rows].
  *  - d_grad_nll NULL: the loss only.  Otherwise the gradients through the head: d_grad_x, fp32
  *    [n_rows][d_model], with respect to the residual rows that the last layer leaves;
  *    d_grad_final_norm [d_model] and d_grad_lm_head [vocab][d_model] in the model's dtype; all
  *    three are then required.  A row listed twice gets one gradient row per listing.
+ *  - The forward adds into its residual rows in an order that depends on timing: two calls agree to
+ *    its rounding, not to the bit.
  *  - d_workspace: smdm_loss_stepcausal_workspace_bytes(cfg, n_rows, grad). */
 size_t smdm_loss_stepcausal_workspace_bytes(const smdm_config* cfg, int n_rows, int grad);
 smdm_status smdm_loss_stepcausal(smdm_handle* h, const int32_t* d_ids, const int32_t* d_pos,

@@ -1343,8 +1343,8 @@ smdm_status smdm_forward_stepcausal(smdm_handle* h, const int32_t* d_ids, const 
 
 namespace {
 
-// Workspace of the training form's loss: the loss rows of the residual stream, their norm, and
-// what the head's loss (and the gradients) need.
+// Workspace of the training form's loss: what the head's loss needs; for the gradients also the loss
+// rows of the residual stream, their norm, and what their kernels need.
 struct LossLayout {
   size_t x, hid, rstd, ghid, head, norm, total;
 };
@@ -1359,15 +1359,15 @@ LossLayout loss_layout(const smdm_config* c, int n_rows, bool grad) {
     off = align_up(off + bytes, 1024);
     return o;
   };
-  L.x = take(n_rows * d * 4);
-  L.hid = take(n_rows * d * es);
-  L.rstd = take((size_t)n_rows * 4);
   if (grad) {
+    L.x = take(n_rows * d * 4);
+    L.hid = take(n_rows * d * es);
+    L.rstd = take((size_t)n_rows * 4);
     L.ghid = take(n_rows * d * es);
     L.norm = take(rmsnorm_grad_bytes(n_rows, c->d_model));
   }
-  size_t head = head_workspace_bytes(n_rows, c->d_model, c->vocab, f32, false);
-  if (grad) head = std::max(head, head_workspace_bytes(n_rows, c->d_model, c->vocab, f32, true));
+  size_t head = head_workspace_bytes(n_rows, c->d_model, c->vocab, f32, false, !f32);
+  if (grad) head = std::max(head, head_workspace_bytes(n_rows, c->d_model, c->vocab, f32, true, !f32));
   L.head = take(head);
   L.total = off;
   return L;
@@ -1416,11 +1416,35 @@ smdm_status smdm_loss_stepcausal(smdm_handle* h, const int32_t* d_ids, const int
                                  st);
   if (s) return s;
   uint8_t* ws = static_cast<uint8_t*>(d_workspace);
+  const int d = c.d_model;
+  // The logits of the forward's LM head: its norm's rows (fp16 for a bf16 model) and its copy of
+  // lm_head.  (The listed rows were checked and copied into rows.qrow by the forward.)
+  void* hq = h->at<uint8_t>(h->L.hq);
+  if ((s = norm(h, h->at<float>(h->L.x), h->final_norm, hq, h->rows.qrow, nullptr, nullptr, n_rows, st)))
+    return s;
+  const void* lm16 = h->bf16 ? h->at<uint8_t>(h->L.w16) + h->L.w16_lm : nullptr;
+  HeadArgs ha{};
+  ha.rows = n_rows;
+  ha.d = d;
+  ha.vocab = c.vocab;
+  ha.f32 = !h->bf16;
+  ha.half = h->bf16;
+  ha.ld_hidden = ha.ld_head = d;
+  ha.hidden = hq;
+  ha.head = h->bf16 ? lm16 : h->lm_head;
+  ha.target = d_target;
+  ha.nll = d_nll;
+  ha.lse_out = d_lse;
+  ha.ws = ws + L.head;
+  ha.status = h->status();
+  {
+    Launch lg_(h, SMDM_K_GEMM_LMHEAD, st, head_loss_launches(ha));
+    CK(launch_head_loss(ha, st));
+  }
+  if (!grad) return SMDM_OK;
   float* x = reinterpret_cast<float*>(ws + L.x);
   float* rstd = reinterpret_cast<float*>(ws + L.rstd);
-  const int d = c.d_model;
   {
-    // (the listed rows were checked and copied into rows.qrow by the forward)
     Launch lg_(h, SMDM_K_OTHER, st);
     CK(launch_gather_f32(h->at<float>(h->L.x), h->rows.qrow, n_rows, n, d, x, h->status(), st));
   }
@@ -1436,24 +1460,12 @@ smdm_status smdm_loss_stepcausal(smdm_handle* h, const int32_t* d_ids, const int
   na.y = ws + L.hid;
   na.rstd_out = rstd;
   { Launch lg_(h, SMDM_K_NORM, st); CK(launch_train_rmsnorm(na, st)); }
-  HeadArgs ha{};
-  ha.rows = n_rows;
-  ha.d = d;
-  ha.vocab = c.vocab;
-  ha.f32 = !h->bf16;
-  ha.ld_hidden = ha.ld_head = d;
-  ha.hidden = ws + L.hid;
-  ha.head = h->lm_head;
-  ha.target = d_target;
-  ha.nll = d_nll;
-  ha.lse_out = d_lse;
-  ha.ws = ws + L.head;
-  ha.status = h->status();
-  {
-    Launch lg_(h, SMDM_K_GEMM_LMHEAD, st, head_loss_launches(ha));
-    CK(launch_head_loss(ha, st));
+  if (h->bf16) {
+    ha.hidden = ws + L.hid;
+    ha.head = h->lm_head;
+    ha.hidden16 = hq;
+    ha.head16 = lm16;
   }
-  if (!grad) return SMDM_OK;
   ha.nll = ha.lse_out = nullptr;
   ha.lse = d_lse;
   ha.grad_nll = d_grad_nll;

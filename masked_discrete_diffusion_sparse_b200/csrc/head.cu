@@ -25,7 +25,7 @@
 // accumulators in tensor memory while eight warps drain the other one.  K-major and MN-major
 // operands differ in their boxes and descriptors only, so D and W are multiplied as they lie.
 //
-// bf16: products of the given values, fp32 sums.  D is rounded to bf16 (half a step, 2^-8
+// bf16 (or fp16 operands of the logits): products of the given values, fp32 sums.  D is rounded to bf16 (half a step, 2^-8
 // relative to each of its values); "What rounding D to bf16 costs" below says what becomes of the
 // remainders.
 // fp32: every operand is split into three bf16 parts (8 + 8 + 8 significant bits) and the six
@@ -79,6 +79,7 @@ struct HeadDev {
   // Loss of 8 / 128 rows of 1024 x 32000 19.0 -> 18.3, 20.1 -> 18.8 us, 100 rows of 4096 x 8192
   // 23.2 -> 20.3; rows of 1 or 3 KB are no faster for it (13.4 -> 13.8, 19.4 -> 19.7).
   int spread;
+  int half;                 // the logits' operands are fp16
   // loss
   float2* part;             // [column group][r_pad]
   int part0;                // first column group of this piece
@@ -538,7 +539,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         // K-major: the next 16 K values lie 32 bytes on; MN-major: 16 rows of 128 bytes on,
         // with 8192 bytes between 64-element runs along M or N
         const int a_mn = u.kind == 2, b_mn = u.kind != 0;
-        const uint32_t idesc = idesc_bf16(128 * CG, BN, a_mn, b_mn);
+        const uint32_t idesc = kMode != kGrad && P == 1 && a.half
+                                   ? idesc_f16(128 * CG, BN, a_mn, b_mn)
+                                   : idesc_bf16(128 * CG, BN, a_mn, b_mn);
         const uint32_t a_lbo = a_mn ? 8192 : 16, b_lbo = b_mn ? 8192 : 16;
         const uint32_t a_step = a_mn ? 2048 >> 4 : 32 >> 4, b_step = b_mn ? 2048 >> 4 : 32 >> 4;
         // (no chunks at all: nothing to sum, the epilogue writes zeros)
@@ -1161,6 +1164,8 @@ struct RowsArgs {
   HeadMeta* meta;
   int* row_idx;
   __nv_bfloat16* out;          // [parts][r_pad][d_pad]
+  const void* hidden16;        // fp16 rows of the same shape, contiguous; null: none
+  __nv_bfloat16* out16;        // their copies
   int* row_tgt;                // [r_pad] targets of the listed rows; null: not wanted
   int* perm;                   // [r_pad] listed rows in order of (target, row); null: not wanted
   int* run;                    // [r_pad] (see HeadDev)
@@ -1225,6 +1230,9 @@ SMDM_DEV void put_row(const T* x, int d, int d_pad, bool vec, __nv_bfloat16* o, 
 }
 
 SMDM_DEV void copy_row(const RowsArgs& a, int src, __nv_bfloat16* out, int dst, int lane) {
+  if (a.hidden16)              // (moved as they are, whatever two-byte type they have)
+    put_row(static_cast<const __nv_bfloat16*>(a.hidden16) + (size_t)src * a.d, a.d, a.d_pad, true,
+            a.out16 + (size_t)dst * a.d_pad, 0, lane);
   const size_t plane = (size_t)a.r_pad * a.d_pad;
   __nv_bfloat16* o = out + (size_t)dst * a.d_pad;
   if (a.f32)
@@ -1714,7 +1722,7 @@ struct Plan {
   bool staged;        // weights go through a bf16 copy of each piece
   int piece, n_pieces;
   bool rest;          // D's remainders at the targets
-  size_t meta, counts, row_idx, hid, part, tlogit, wst, dlog, acc, row_tgt, delta, ids, run, perm, inv, sort[2], rest_rows, total;
+  size_t meta, counts, row_idx, hid, hid16, part, tlogit, wst, dlog, acc, row_tgt, delta, ids, run, perm, inv, sort[2], rest_rows, total;
   int cfg, cfg_g;     // tile configuration of the logits' product and of the gradients'
   int splits, n_part;
   int narrow;         // > 0: head_narrow_kernel, with this many vocabulary slots (= splits)
@@ -1761,7 +1769,7 @@ int pick_cfg(long long m, long long n, int sms, int parts) {
 // Vocabulary slots of head_narrow_kernel: one column group per CTA, a CTA per SM.
 int narrow_slots(int d, int sms) { return std::max(1, sms / ((d + 127) / 128)); }
 
-Plan make_plan(int rows, int d, int vocab, long long ld_head, bool f32, bool grad) {
+Plan make_plan(int rows, int d, int vocab, long long ld_head, bool f32, bool grad, bool half) {
   Plan p{};
   const int sms = sm_count();
   p.parts = f32 ? 3 : 1;
@@ -1828,6 +1836,7 @@ Plan make_plan(int rows, int d, int vocab, long long ld_head, bool f32, bool gra
   p.counts = take(rows > kListRows ? kListCtas * 4 : 0);
   p.row_idx = take((size_t)p.r_pad * 4);
   p.hid = take((size_t)p.parts * p.r_pad * p.d_pad * 2);
+  if (grad && half) p.hid16 = take((size_t)p.r_pad * p.d_pad * 2);
   if (!grad) {
     p.part = take((size_t)p.n_part * p.r_pad * 8);
     p.tlogit = take((size_t)p.r_pad * 4);
@@ -1985,7 +1994,7 @@ struct Call {
   template <typename T> T* at(size_t off) const { return reinterpret_cast<T*>(ws + off); }
 
   Call(const HeadArgs& a, bool grad)
-      : h(a), p(make_plan(a.rows, a.d, a.vocab, a.ld_head, a.f32, grad)), sms(sm_count()),
+      : h(a), p(make_plan(a.rows, a.d, a.vocab, a.ld_head, a.f32, grad, a.half)), sms(sm_count()),
         ws(static_cast<uint8_t*>(a.ws)), loss(!grad) {
     in_place = !a.f32 && a.d % 8 == 0 && a.ld_hidden % 8 == 0 && aligned16(a.hidden);
   }
@@ -2011,6 +2020,10 @@ struct Call {
     r.meta = at<HeadMeta>(p.meta);
     r.row_idx = at<int>(p.row_idx);
     r.out = at<__nv_bfloat16>(p.hid);
+    if (!loss && h.half) {
+      r.hidden16 = h.hidden16;
+      r.out16 = at<__nv_bfloat16>(p.hid16);
+    }
     r.nll = h.nll;
     r.lse = h.lse_out;
     if (p.rest) {
@@ -2078,6 +2091,12 @@ struct Call {
     const WeightArgs w = weight_args(v0, vc);
     return launch_pdl(head_weights_kernel, dim3(w.ctas), dim3(256), 0, st, 1, row_args(), w);
   }
+  // The operands of the logits, where they are others than the gradient's products have.
+  bool half_maps(Maps* m, uint32_t h_rows, uint32_t w_rows) const {
+    return encode_bf16(&m->h, h.hidden16, h.d, h.rows, h.d, 64, h_rows) &&
+           encode_bf16(&m->hc, at<uint8_t>(p.hid16), p.d_pad, p.r_pad, p.d_pad, 64, h_rows) &&
+           encode_bf16(&m->w, h.head16, h.d, h.vocab, h.d, 64, w_rows);
+  }
   bool weight_map(CUtensorMap* m, int vc, uint32_t box_rows) const {
     if (p.staged)
       return encode_bf16(m, at<uint8_t>(p.wst), p.d_pad, (uint64_t)p.parts * up(vc, 256), p.d_pad,
@@ -2109,7 +2128,12 @@ struct Call {
     a.r_pad = p.r_pad;
     a.d_pad = p.d_pad;
     a.status = h.status;
+    a.half = h.half;
     return a;
+  }
+  // fp16 operands are read in place only
+  bool half_ok() const {
+    return !h.half || (!h.f32 && in_place && !p.staged && (loss || (h.hidden16 && h.head16 && aligned16(h.hidden16) && aligned16(h.head16))));
   }
   // Rows of D that head_narrow_kernel reads for rows that take part: its steps over them.
   int narrow_rows() const { return h.rows <= 16 ? 16 : h.rows <= 64 ? 64 : 128; }
@@ -2119,10 +2143,10 @@ struct Call {
 
 }  // namespace
 
-size_t head_workspace_bytes(int rows, int d, int vocab, bool f32, bool grad) {
+size_t head_workspace_bytes(int rows, int d, int vocab, bool f32, bool grad, bool half) {
   // the layout that copies the weights is the larger one; it serves every row stride
-  return std::max(make_plan(rows, d, vocab, 0, f32, grad).total,
-                  make_plan(rows, d, vocab, 1, f32, grad).total);
+  return std::max(make_plan(rows, d, vocab, 0, f32, grad, half).total,
+                  make_plan(rows, d, vocab, 1, f32, grad, half).total);
 }
 
 bool head_needs_aligned_weight(int d, long long ld_head, bool f32) {
@@ -2147,6 +2171,7 @@ int head_grad_launches(const HeadArgs& a) {
 cudaError_t launch_head_loss(const HeadArgs& h, cudaStream_t st) {
   const Call c(h, false);
   const Plan& p = c.p;
+  if (!c.half_ok()) return cudaErrorInvalidValue;
   if (p.few) return launch_head_few_loss(h, c.sms, st);
   TRY(c.rows(st));
   const int cg = kCfgCG[p.cfg], bn = kCfgBN[p.cfg];
@@ -2176,6 +2201,7 @@ cudaError_t launch_head_loss(const HeadArgs& h, cudaStream_t st) {
 cudaError_t launch_head_grad(const HeadArgs& h, cudaStream_t st) {
   const Call c(h, true);
   const Plan& p = c.p;
+  if (!c.half_ok()) return cudaErrorInvalidValue;
   if (p.few) return launch_head_few_grad(h, c.sms, st);
   TRY(c.rows(st));
   const int cg = kCfgCG[p.cfg], bn = kCfgBN[p.cfg];
@@ -2188,7 +2214,8 @@ cudaError_t launch_head_grad(const HeadArgs& h, cudaStream_t st) {
     Maps m;
     HeadDev a = c.dev(v0, vc);
     a.a_box = c.a_box();
-    if (!c.hidden_maps(&m.h, &m.hc, a.a_box) || !c.weight_map(&m.w, vc, bn / cg))
+    if (!(h.half ? c.half_maps(&m, a.a_box, bn / cg)
+                 : c.hidden_maps(&m.h, &m.hc, a.a_box) && c.weight_map(&m.w, vc, bn / cg)))
       return cudaErrorInvalidValue;
     m.dk = m.dm = m.hc;
     a.d_parts = p.d_parts;

@@ -17,12 +17,17 @@ struct HeadArgs {
   const float* grad_nll;     // gradient: [rows]
   void* grad_hidden;         // gradient: [rows][d] or null
   void* grad_head;           // gradient: [vocab][d] or null
+  // Logits from fp16 operands: the loss's hidden and head are fp16; the gradient makes its logits
+  // from these two (contiguous, on 16 bytes, d a multiple of 8), its products from hidden and head.
+  bool half;
+  const void* hidden16;
+  const void* head16;
   void* ws;
   uint32_t* status;          // optional
 };
 
-// Bytes of workspace for one call (grad: the gradient's, else the loss's).
-size_t head_workspace_bytes(int rows, int d, int vocab, bool f32, bool grad);
+// Bytes of workspace for one call (grad: the gradient's, else the loss's; half as in HeadArgs).
+size_t head_workspace_bytes(int rows, int d, int vocab, bool f32, bool grad, bool half = false);
 // True when lm_head must start on a 16-byte boundary (its rows are then read by TMA in place).
 bool head_needs_aligned_weight(int d, long long ld_head, bool f32);
 // Kernels that a call launches.
