@@ -522,7 +522,7 @@ def _call(fn: str, stream, tensors, *args):
 def _status(t: Optional[torch.Tensor]):
     if t is None:
         return None
-    if t.numel() < 1 or t.element_size() != 4:
+    if t.numel() < 1 or t.dtype not in (torch.int32, torch.uint32):
         raise ValueError("status: expected a 32-bit integer tensor of one element")
     return _adr(t, "status")
 

@@ -70,6 +70,14 @@ def test_pointers_off_their_boundary_are_refused(call):
             assert r == smdm.SMDM_EINVAL, f"{entry}: {name} {shift} bytes off gives {r}"
 
 
+def test_the_status_is_a_32_bit_integer():
+    for bad in (torch.zeros(1), torch.zeros(1, dtype=torch.int64), torch.zeros(0, dtype=torch.int32)):
+        with pytest.raises(ValueError, match="32-bit integer"):
+            smdm._status(bad)
+    with pytest.raises(ValueError, match="CUDA"):
+        smdm._status(torch.zeros(1, dtype=torch.int32))
+
+
 @pytest.mark.gpu
 def test_loss_of_the_training_form_refuses_them_too():
     if not torch.cuda.is_available():
