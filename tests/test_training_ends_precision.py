@@ -6,7 +6,7 @@ import pytest
 import torch
 
 import masked_discrete_diffusion_sparse_b200 as smdm
-from test_training_ends import BF16, Head, _gpu, f64, gen, rand, workspace  # noqa: F401
+from test_training_ends import BF16, F32, Head, _gpu, f64, gen, rand, workspace  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -133,3 +133,48 @@ def test_head_gradient_of_targets_with_many_rows(rows, d, vocab):
         assert err <= 1.05 * bound, err / bound
     again = x.grad(lse)
     assert torch.equal(got[0], again[0]) and torch.equal(got[1], again[1])
+
+
+@pytest.mark.parametrize("rows,d,vocab", [(96, 64, 200), (12, 64, 200), (300, 96, 700)])
+def test_head_gradients_against_differences(rows, d, vocab):
+    """Each gradient alone against the central difference of the kernel's loss along it (fp32).
+
+    The loss f is the weighted sum of nll, its weights add up to 1.  The difference over 2 e is off
+    by what the same difference of the definition in 64 bits is off from its derivative, and by
+    1 / e times the error of nll: at most 2^-20 of exp and log, 2^-23 of values up to 32, and a
+    logit's, six products of d / 16 steps of 2^-23 of about (d / 2)^0.5 (the terms' signs are random),
+    twice."""
+    x = Head(rows, d, vocab, F32, 0.2, seed=11, std=0.3)
+    x.weight /= x.weight[x.target >= 0].sum()
+    _, lse = x.loss()
+    gh, gw = x.grad(lse)
+    on = x.target >= 0
+    wt = torch.where(on, x.weight, torch.zeros_like(x.weight)).to(f64)
+    t = x.target.long().clamp(min=0)[:, None]
+    h0, w0 = x.h.clone(), x.w.clone()
+
+    def exact(h, w):
+        z = h.to(f64) @ w.to(f64).T
+        return ((torch.logsumexp(z, 1) - z.gather(1, t)[:, 0]) * wt).sum().item()
+
+    def kernel(h, w):
+        x.h.copy_(h)
+        x.w.copy_(w)
+        return (x.loss()[0].to(f64) * wt).sum().item()
+
+    err = 2 * (2.0 ** -20 + 2.0 ** -18 + 2 * 6 * d / 16 * 2.0 ** -23 * (d / 2) ** 0.5)
+    e = 0.05
+    for which, got in ((0, gh), (1, gw)):
+        z = h0.to(f64).requires_grad_(which == 0), w0.to(f64).requires_grad_(which == 1)
+        logits = z[0] @ z[1].T
+        f = ((torch.logsumexp(logits, 1) - logits.gather(1, t)[:, 0]) * wt).sum()
+        ref, = torch.autograd.grad(f, z[which])
+        dirn = (ref / ref.norm()).float()
+        at = lambda s: (h0 + s * dirn, w0) if which == 0 else (h0, w0 + s * dirn)  # noqa: E731
+        true = (ref * dirn.to(f64)).sum().item()
+        trunc = abs((exact(*at(e)) - exact(*at(-e))) / (2 * e) - true)
+        diff = (kernel(*at(e)) - kernel(*at(-e))) / (2 * e)
+        tol = trunc + err / e
+        mine = (got.to(f64) * dirn.to(f64)).sum().item()
+        assert tol < 0.1 * abs(diff), (which, tol, diff)
+        assert abs(mine - diff) <= tol, (which, mine, diff, tol)
