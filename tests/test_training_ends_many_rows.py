@@ -51,3 +51,14 @@ def test_head_gradient_of_many_rows_with_one_target(rows, vocab, hot):
     assert err <= 1.05 * bound, err / bound
     b = x.grad(lse)
     assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+@pytest.mark.parametrize("rows,d,vocab,pad", [
+    (6000, 63, 32768, 0), (6000, 64, 32768, 3),     # weights copied, D in pieces
+    (40, 16384, 20000, 0), (100, 16384, 16385, 8)])  # one row tile, a slot's ids in pieces
+def test_head_gradient_in_several_pieces_of_other_kinds(rows, d, vocab, pad):
+    x = Head(rows, d, vocab, BF16, 0.1, pad, seed=rows + d, wpad=pad if d == 64 else 0)
+    _, lse = x.check_loss()
+    a = x.check_grad(lse)
+    b = x.grad(lse)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
