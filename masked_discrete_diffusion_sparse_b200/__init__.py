@@ -347,7 +347,7 @@ class Model:
         With grad_nll (fp32, the loss weight of every row) also the gradients through the head:
         grad_x (fp32 [n_rows][d_model]), grad_final_norm and grad_lm_head (model dtype).
         workspace: uint8 tensor of smdm_loss_stepcausal_workspace_bytes."""
-        m = loss_rows.numel()
+        m = _count(loss_rows.numel())
         d, v = self.cfg.d_model, self.cfg.vocab
         dt = torch.float32 if self.cfg.dtype == SMDM_F32 else torch.bfloat16
         for t in (pos, types, labels):
@@ -363,13 +363,13 @@ class Model:
                 _typed(t, want, name)
         self._check(lib().smdm_loss_stepcausal(
             self.h, _ptr(_i32(ids)), _ptr(_i32(pos)), _ptr(_i32(types)), _ptr(_i32(labels)),
-            ids.numel(), _ptr(_i32(loss_rows)), m, _ptr(target), _ptr(nll), _ptr(lse),
+            _count(ids.numel()), _ptr(_i32(loss_rows)), m, _ptr(target), _ptr(nll), _ptr(lse),
             _ptr(grad_nll), _ptr(grad_x), _ptr(grad_final_norm), _ptr(grad_lm_head),
             _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream)))
 
     def smdm_loss_stepcausal_workspace_bytes(self, n_rows: int, grad: bool = False) -> int:
-        return _bytes(lib().smdm_loss_stepcausal_workspace_bytes(ctypes.byref(self.cfg), n_rows,
-                                                                 1 if grad else 0))
+        return _bytes(lib().smdm_loss_stepcausal_workspace_bytes(
+            ctypes.byref(self.cfg), _count(n_rows), 1 if grad else 0))
 
     def smdm_debug_mask(self, types, labels, bitmap, stream=None):
         self._check(lib().smdm_debug_mask(self.h, _ptr(_i32(types)), _ptr(_i32(labels)),
@@ -443,9 +443,23 @@ def _dtype(dt) -> int:
     return c
 
 
+def _count(n: int) -> int:
+    if not -2 ** 31 <= n < 2 ** 31:
+        raise SmdmError(SMDM_ESHAPE, f"{n} elements")
+    return n
+
+
+def _struct(t, *a):
+    """A shape struct; a size that its field cannot hold is refused, not cut."""
+    for (_, kind), v in zip(t._fields_, a):
+        if kind is ctypes.c_int:
+            _count(v)
+    return ctypes.byref(t(*a))
+
+
 # Shape arguments of recent calls: building one takes as long as the call that it is passed to.
 _head_struct, _norm_struct, _embed_struct = (
-    functools.lru_cache(maxsize=256)(lambda *a, t=t: ctypes.byref(t(*a)))
+    functools.lru_cache(maxsize=256)(functools.partial(_struct, t))
     for t in (smdm_head_shape, smdm_rmsnorm_shape, smdm_embed_shape))
 
 

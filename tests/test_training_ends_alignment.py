@@ -70,6 +70,19 @@ def test_pointers_off_their_boundary_are_refused(call):
             assert r == smdm.SMDM_EINVAL, f"{entry}: {name} {shift} bytes off gives {r}"
 
 
+def test_sizes_past_32_bits_are_refused_not_cut():
+    for rows in (2 ** 32 + 8, 2 ** 31, -2 ** 32 + 8):
+        with pytest.raises(smdm.SmdmError):
+            smdm.smdm_head_loss_workspace_bytes(rows, 64, 100, torch.bfloat16)
+        with pytest.raises(smdm.SmdmError):
+            smdm.smdm_head_loss_workspace_bytes(8, 64, rows, torch.bfloat16)
+        with pytest.raises(smdm.SmdmError):
+            smdm.smdm_rmsnorm_grad_workspace_bytes(rows, 64)
+        with pytest.raises(smdm.SmdmError):
+            smdm.smdm_embed_grad_workspace_bytes(rows, 64, 100)
+    assert smdm.smdm_head_loss_workspace_bytes(8, 64, 100, torch.bfloat16) > 0
+
+
 def test_the_status_is_a_32_bit_integer():
     for bad in (torch.zeros(1), torch.zeros(1, dtype=torch.int64), torch.zeros(0, dtype=torch.int32)):
         with pytest.raises(ValueError, match="32-bit integer"):
