@@ -361,6 +361,12 @@ class Model:
             if t is not None:
                 _shape(t, shape, name)
                 _typed(t, want, name)
+        if stream is not None and stream != torch.cuda.current_stream(stream.device):
+            # (the allocator must not hand their memory out while the kernels run)
+            for t in (ids, pos, types, labels, loss_rows, target, nll, lse, grad_nll, grad_x,
+                      grad_final_norm, grad_lm_head, workspace):
+                if t is not None and t.is_cuda:
+                    t.record_stream(stream)
         self._check(lib().smdm_loss_stepcausal(
             self.h, _ptr(_i32(ids)), _ptr(_i32(pos)), _ptr(_i32(types)), _ptr(_i32(labels)),
             _count(ids.numel()), _ptr(_i32(loss_rows)), m, _ptr(target), _ptr(nll), _ptr(lse),

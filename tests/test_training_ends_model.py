@@ -197,6 +197,30 @@ def test_loss_on_another_stream_and_after_other_targets(traj):
     assert traj.model.smdm_device_status() == 0
 
 
+def test_loss_on_another_stream_keeps_its_tensors(traj):
+    """Tensors that the caller lets go of right after the call still hold their values when its
+    kernels run."""
+    traj.run()
+    torch.cuda.synchronize()
+    on = traj.target >= 0
+    s = torch.cuda.Stream()
+    target = traj.target.clone()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(100_000_000)               # (about 50 ms: the call waits behind it)
+    kept, traj.target = traj.target, target
+    traj.clear()
+    s.wait_stream(torch.cuda.current_stream())
+    traj.run(grad=False, stream=s)
+    traj.target = kept
+    where = target.data_ptr()
+    del target
+    others = [torch.full_like(kept, -1) for _ in range(64)]     # would land in its memory
+    assert all(t.data_ptr() != where for t in others)
+    torch.cuda.synchronize()
+    assert (traj.nll[on] != 0).all()
+
+
 def test_loss_captured_and_replayed(traj):
     runs = eager(traj)
     g = torch.cuda.CUDAGraph()
