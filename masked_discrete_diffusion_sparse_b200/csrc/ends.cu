@@ -122,7 +122,7 @@ constexpr int kNormThreads = 256;
 
 // y = x r gain, r = (mean x^2 + eps)^-1/2.  TPR threads per row, NU units of VEC elements each: a
 // warp up to 1024 elements (no barrier in the row's sum), a CTA above.  66 rows of 4096: 2.5 us,
-// a launch's time.
+// a launch's time; 12544 rows (fp32 to bf16) of 4096: 48 us, 6.4 TB/s, of 1024: 17.6 us, 4.4 TB/s.
 template <typename X, typename T, int TPR, int VEC, int NU>
 __global__ void __launch_bounds__(kNormThreads) train_rms_kernel(RmsArgs a) {
   griddep_launch();
@@ -168,7 +168,8 @@ __global__ void __launch_bounds__(kNormThreads) train_rms_kernel(RmsArgs a) {
 
 // u = gy gain;  gx = r (u - x r^2 mean(u x)) + add;  ggain = sum over rows of gy x r.
 // Persistent CTAs: the gain and this CTA's share of its gradient stay in registers over all the
-// CTA's rows; the shares go to ws[CTA][d] and are added up in order by rms_gain_kernel.
+// CTA's rows; the shares go to ws[CTA][d] and are added up in order by rms_gain_kernel.  12544 rows of
+// 1024 (fp32 x and add, bf16 grad_y): 37.6 us, 4.8 TB/s.
 template <typename X, typename T, int TPR, int VEC, int NU>
 __global__ void __launch_bounds__(kNormThreads) train_rms_grad_kernel(RmsArgs a) {
   griddep_launch();
@@ -415,8 +416,8 @@ __global__ void __launch_bounds__(1024) rms_gain_kernel(const float* ws, int par
 // ------------------------------------------------------------------------------------------
 // One warp per row.  A lane takes as many elements as fill 16 bytes of the wider of the two types,
 // so that every store instruction of a warp writes whole 32-byte sectors in a row.  A negative id
-// gives a row of zeros.  12544 rows of 4096, bf16 to fp32: 41 us, 5.9 TB/s of rows read and
-// written; 65 with each lane's 32 bytes written in two halves, 48 with loads between the stores.
+// gives a row of zeros.  12544 rows of 4096, bf16 to fp32: 41 us, 5.7 TB/s of rows written
+// and of the about 3340 different ones read; 65 with each lane's 32 bytes written in two halves, 48 with loads between the stores.
 template <typename T, typename O, bool VECT>
 __global__ void __launch_bounds__(256) embed_kernel(EmbedArgs a) {
   griddep_launch();

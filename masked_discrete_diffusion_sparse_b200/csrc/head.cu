@@ -15,9 +15,9 @@
 // What bounds it and what it reaches (B200, other inputs on every pass):
 //   loss, 4096 rows, 4096 x 8192     187 us   1.47 PFLOP/s  (a plain bf16 product sustains 1.40,
 //                                             in bursts 1.67: tensor pipe and power)
-//   gradient, a quarter left out     460 us   1.34 PFLOP/s  likewise
+//   gradient, a quarter left out     468 us   1.32 PFLOP/s  likewise
 //   loss, 8 rows, 1024 x 32000       18.6 us  3.5 TB/s      reading 65 MB (a bare read: 14), two tails
-//   gradient, 128 rows, likewise     62 us    2.1 TB/s      see head_narrow_kernel
+//   gradient, 128 rows, likewise     63 us    2.1 TB/s      see head_narrow_kernel
 //   fp32 loss, 331 rows, 256 x 1001  12.3 us                latency of three kernels
 //
 // One kernel does all products (`head_gemm_kernel`): persistent CTAs (or pairs, cta_group::2),
@@ -25,9 +25,9 @@
 // accumulators in tensor memory while eight warps drain the other one.  K-major and MN-major
 // operands differ in their boxes and descriptors only, so D and W are multiplied as they lie.
 //
-// bf16 (or fp16 operands of the logits): products of the given values, fp32 sums.  D is rounded to bf16 (half a step, 2^-8
-// relative to each of its values); "What rounding D to bf16 costs" below says what becomes of the
-// remainders.
+// bf16 (the logits' operands may be fp16): products of the given values, fp32 sums.  D is rounded
+// to bf16 (half a step, 2^-8 relative to each of its values); "What rounding D to bf16 costs"
+// below says what becomes of the remainders.
 // fp32: every operand is split into three bf16 parts (8 + 8 + 8 significant bits) and the six
 // products that reach 2^-16 of the largest are summed, smallest first (2^-23 is left out).
 #include "head.h"
@@ -2133,7 +2133,9 @@ struct Call {
   }
   // fp16 operands are read in place only
   bool half_ok() const {
-    return !h.half || (!h.f32 && in_place && !p.staged && (loss || (h.hidden16 && h.head16 && aligned16(h.hidden16) && aligned16(h.head16))));
+    if (!h.half) return true;
+    if (h.f32 || !in_place || p.staged) return false;
+    return loss || (h.hidden16 && h.head16 && aligned16(h.hidden16) && aligned16(h.head16));
   }
   // Rows of D that head_narrow_kernel reads for rows that take part: its steps over them.
   int narrow_rows() const { return h.rows <= 16 ? 16 : h.rows <= 64 ? 64 : 128; }

@@ -8,8 +8,9 @@
 //
 // It takes the calls whose weights would have to be written out (fp32 ones, and bf16 ones whose rows
 // do not start on 16-byte boundaries).  fp32, 1024 x 32000: loss of 4 / 16 rows 36 / 70 us against
-// 112 / 112 through the parts, gradient 103 / 151 us against 205 / 206.  What bounds it: HBM up to
-// eight rows (36 us are 3.6 TB/s), then the multiply-adds and the loads that feed them.
+// 112 / 112 through the parts, gradient 103 / 151 us against 205 / 206.  What bounds it: up to eight
+// rows the loads in flight (36 us are 3.6 TB/s, 0.56 of the measured peak: registers leave room for
+// one to three blocks per SM), then the multiply-adds and the loads that feed them.
 #include <algorithm>
 
 #include "head.h"
