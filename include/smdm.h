@@ -384,8 +384,8 @@ smdm_status smdm_head_loss(const smdm_head_shape* shape, const void* d_hidden,
  * grad_lm_head = D^T hidden [vocab][d_model].  Either output may be NULL.  D exists one piece of
  * the vocabulary at a time (at most 256 MiB of it, or 256 columns).  For bf16 D is rounded to bf16;
  * what that rounding leaves is kept where it counts, at each row's target (with 128 rows or fewer
- * everywhere), so that the gradients' error stays near their own rounding; a row that is certain of a wrong id
- * adds the rounding of one more entry to that. */
+ * everywhere), so that the gradients' error stays near their own rounding; a row that is certain
+ * of a wrong id adds the rounding of one more entry to that. */
 smdm_status smdm_head_loss_grad(const smdm_head_shape* shape, const void* d_hidden,
                                 const void* d_lm_head, const int32_t* d_target,
                                 const float* d_lse, const float* d_grad_nll, void* d_grad_hidden,

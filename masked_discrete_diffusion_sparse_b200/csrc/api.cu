@@ -1420,7 +1420,8 @@ smdm_status smdm_loss_stepcausal(smdm_handle* h, const int32_t* d_ids, const int
   // The logits of the forward's LM head: its norm's rows (fp16 for a bf16 model) and its copy of
   // lm_head.  (The listed rows were checked and copied into rows.qrow by the forward.)
   void* hq = h->at<uint8_t>(h->L.hq);
-  if ((s = norm(h, h->at<float>(h->L.x), h->final_norm, hq, h->rows.qrow, nullptr, nullptr, n_rows, st)))
+  if ((s = norm(h, h->at<float>(h->L.x), h->final_norm, hq, h->rows.qrow, nullptr, nullptr, n_rows,
+                st)))
     return s;
   const void* lm16 = h->bf16 ? h->at<uint8_t>(h->L.w16) + h->L.w16_lm : nullptr;
   HeadArgs ha{};

@@ -417,7 +417,8 @@ __global__ void __launch_bounds__(1024) rms_gain_kernel(const float* ws, int par
 // One warp per row.  A lane takes as many elements as fill 16 bytes of the wider of the two types,
 // so that every store instruction of a warp writes whole 32-byte sectors in a row.  A negative id
 // gives a row of zeros.  12544 rows of 4096, bf16 to fp32: 41 us, 5.7 TB/s of rows written
-// and of the about 3340 different ones read; 65 with each lane's 32 bytes written in two halves, 48 with loads between the stores.
+// and of the about 3340 different ones read; 65 with each lane's 32 bytes written in two halves, 48
+// with loads between the stores.
 template <typename T, typename O, bool VECT>
 __global__ void __launch_bounds__(256) embed_kernel(EmbedArgs a) {
   griddep_launch();

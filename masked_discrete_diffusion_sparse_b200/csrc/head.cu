@@ -1167,7 +1167,8 @@ struct RowsArgs {
   const void* hidden16;        // fp16 rows of the same shape, contiguous; null: none
   __nv_bfloat16* out16;        // their copies
   int* row_tgt;                // [r_pad] targets of the listed rows; null: not wanted
-  int* perm;                   // [r_pad] listed rows in order of (target, row); null: not wanted
+  int4* perm;                  // [r_pad] listed rows in order of (target, row), as (row, its `run`,
+                               // target, 0); null: not wanted
   int* run;                    // [r_pad] (see HeadDev)
   int* inv;                    // instead of those two, with counts: caller's row -> listed row
   int2* ids;                   // [vocab] to clear; null: not wanted
@@ -1404,8 +1405,9 @@ __global__ void __launch_bounds__(256) head_rows_kernel(RowsArgs a, WeightArgs w
             k.x += s_rank[i][r - r0].x;
             k.y += s_rank[i][r - r0].y;
           }
-          a.perm[k.x + (k.y >> 16)] = pos;
-          a.run[pos] = k.y < 0x10000 ? k.y : 0;
+          const int run = k.y < 0x10000 ? k.y : 0;
+          a.perm[k.x + (k.y >> 16)] = make_int4(pos, run, t, 0);
+          a.run[pos] = run;
         }
       } else if (a.nll) {
         a.nll[r] = 0.f;
@@ -1448,7 +1450,7 @@ __global__ void __launch_bounds__(256) head_rows_kernel(RowsArgs a, WeightArgs w
 // caller's row) words.
 __global__ void __launch_bounds__(256)
     head_perm_kernel(const HeadMeta* meta, const unsigned long long* sorted, const int* inv,
-                     int* perm, int* run) {
+                     int4* perm, int* run) {
   griddep_launch();
   griddep_wait();
   const int n = meta->n, p = blockIdx.x * 256 + threadIdx.x;
@@ -1456,7 +1458,6 @@ __global__ void __launch_bounds__(256)
   const unsigned long long w = sorted[p];
   const unsigned key = (unsigned)(w >> 32);
   const int row = inv[(unsigned)w];
-  perm[p] = row;
   int lo = p + 1, hi = n;                    // the end of the rows with this target
   if (p > 0 && (unsigned)(sorted[p - 1] >> 32) == key) lo = hi = p;
   while (lo < hi) {
@@ -1464,6 +1465,7 @@ __global__ void __launch_bounds__(256)
     if ((unsigned)(sorted[mid] >> 32) == key) lo = mid + 1;
     else hi = mid;
   }
+  perm[p] = make_int4(row, lo - p, (int)key, 0);
   run[row] = lo - p;
 }
 
@@ -1472,13 +1474,11 @@ __global__ void __launch_bounds__(256)
 // them.  A CTA takes 256 columns and the targets that begin at 32 places of the rows in order of
 // their targets: a warp each, all warps together for one of more than kRestLong rows.  Summed in
 // fp32, eight rows in flight per warp; kept in bf16, which is 2^-9 of 2^-9 of D's part of dW.
-// 3072 rows of 4096 over 8192 ids: 13 us, mostly the latency of five loads in a row; 786432 rows of
-// 64 over 64 ids: 0.5 ms of 6.
+// 3072 rows of 4096 over 8192 ids: 13 us, mostly the latency of loads that follow one another;
+// 786432 rows of 64 over 64 ids: 0.5 ms of 6.
 struct RestArgs {
   const HeadMeta* meta;
-  const int* row_tgt;
-  const int* perm;
-  const int* run;
+  const int4* perm;
   const float* delta;
   const void* hidden;          // the caller's rows
   long long ld_hidden;
@@ -1494,8 +1494,9 @@ __global__ void __launch_bounds__(kRestWarps * 32) head_rest_kernel(RestArgs a) 
   griddep_wait();
   __shared__ __align__(16) float part[kRestWarps][256];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int n = a.meta->n;
   const int p0 = (int)(blockIdx.x / a.slabs) * 32, c = (int)(blockIdx.x % a.slabs) * 256 + lane * 8;
+  const int4 at = a.perm[p0 + lane];         // (past the last row: nothing that is used)
+  const int n = a.meta->n;
   if (p0 >= n) return;
   // both kinds of rows start on 16 bytes and fill 16-byte words
   const bool dense = a.meta->dense != 0;
@@ -1503,12 +1504,8 @@ __global__ void __launch_bounds__(kRestWarps * 32) head_rest_kernel(RestArgs a) 
   const long long ld = dense ? a.ld_hidden : a.d_pad;
   const bool in = c < (dense ? a.d : a.d_pad);
   // the target that begins at this lane's place
-  int row = 0, count = 0;
-  if (p0 + lane < n) {
-    row = a.perm[p0 + lane];
-    const int t = a.row_tgt[row];
-    if (t >= a.v0 && t < a.v0 + a.vc) count = a.run[row];
-  }
+  const int row = at.x;
+  const int count = p0 + lane < n && at.z >= a.v0 && at.z < a.v0 + a.vc ? at.y : 0;
   float s[8];
   // the rows at the places [from, to)
   auto sum = [&](int from, int to) {
@@ -1516,7 +1513,7 @@ __global__ void __launch_bounds__(kRestWarps * 32) head_rest_kernel(RestArgs a) 
     for (int j = 0; j < 8; ++j) s[j] = 0.f;
     for (; from < to; from += 32) {
       const int cnt = min(32, to - from);
-      const int r = lane < cnt ? a.perm[from + lane] : 0;
+      const int r = lane < cnt ? a.perm[from + lane].x : 0;
       const float delta = lane < cnt ? a.delta[r] : 0.f;
       for (int e0 = 0; e0 < cnt; e0 += 8) {
         uint4 x[8];
@@ -1528,6 +1525,7 @@ __global__ void __launch_bounds__(kRestWarps * 32) head_rest_kernel(RestArgs a) 
         }
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
+          if (e0 + k >= cnt) break;
           const float f = __shfl_sync(0xffffffffu, delta, e0 + k);
           const uint32_t w[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
 #pragma unroll
@@ -1547,7 +1545,8 @@ __global__ void __launch_bounds__(kRestWarps * 32) head_rest_kernel(RestArgs a) 
     *reinterpret_cast<uint4*>(a.out + (size_t)to * a.d_pad + c) = make_uint4(w[0], w[1], w[2], w[3]);
   };
   int turn = 0;
-  for (uint32_t m = __ballot_sync(0xffffffffu, count > 1 && count <= kRestLong); m; m &= m - 1, ++turn) {
+  const uint32_t few = __ballot_sync(0xffffffffu, count > 1 && count <= kRestLong);
+  for (uint32_t m = few; m; m &= m - 1, ++turn) {
     if (turn % kRestWarps != warp) continue;
     const int i = __ffs(m) - 1;
     sum(p0 + i, p0 + i + __shfl_sync(0xffffffffu, count, i));
@@ -1722,7 +1721,8 @@ struct Plan {
   bool staged;        // weights go through a bf16 copy of each piece
   int piece, n_pieces;
   bool rest;          // D's remainders at the targets
-  size_t meta, counts, row_idx, hid, hid16, part, tlogit, wst, dlog, acc, row_tgt, delta, ids, run, perm, inv, sort[2], rest_rows, total;
+  size_t meta, counts, row_idx, hid, hid16, part, tlogit, wst, dlog, acc, total;
+  size_t row_tgt, delta, ids, run, perm, inv, sort[2], rest_rows;      // (rest)
   int cfg, cfg_g;     // tile configuration of the logits' product and of the gradients'
   int splits, n_part;
   int narrow;         // > 0: head_narrow_kernel, with this many vocabulary slots (= splits)
@@ -1794,7 +1794,7 @@ Plan make_plan(int rows, int d, int vocab, long long ld_head, bool f32, bool gra
   if (per_col) p.piece = (int)std::min<size_t>(v_pad, std::max<size_t>(256, kPieceBytes / per_col / 256 * 256));
   // one row tile: no slot of head_narrow_kernel sums more than kNarrowBlocks blocks into its dH
   if (grad && !f32 && rows <= 128)
-    p.piece = (int)std::min<long long>(p.piece, (long long)narrow_slots(d, sms) * kNarrowBlocks * 64 / 256 * 256);
+    p.piece = (int)std::min<long long>(p.piece, (long long)narrow_slots(d, sms) * kNarrowBlocks * 64);
   p.n_pieces = (vocab + p.piece - 1) / p.piece;
   // pieces of equal width
   p.piece = (int)up((vocab + p.n_pieces - 1) / p.n_pieces, 256);
@@ -1849,7 +1849,7 @@ Plan make_plan(int rows, int d, int vocab, long long ld_head, bool f32, bool gra
       p.delta = take((size_t)p.r_pad * 4);
       p.ids = take((size_t)vocab * 8);
       p.run = take((size_t)p.r_pad * 4);
-      p.perm = take((size_t)p.r_pad * 4);
+      p.perm = take((size_t)p.r_pad * 16);
       if (rows > kListRows) {
         p.inv = take((size_t)rows * 4);
         for (size_t& k : p.sort) k = take((size_t)rows * 8);
@@ -2032,7 +2032,7 @@ struct Call {
       if (order && counted) {
         r.inv = at<int>(p.inv);
       } else if (order) {
-        r.perm = at<int>(p.perm);
+        r.perm = at<int4>(p.perm);
         r.run = at<int>(p.run);
       }
     }
@@ -2082,7 +2082,7 @@ struct Call {
     TRY(launch_sort_ids(h.target, h.rows, h.vocab, at<unsigned long long>(p.sort[0]),
                         at<unsigned long long>(p.sort[1]), nullptr, 0, nullptr, st, &sorted));
     return launch_pdl(head_perm_kernel, dim3((h.rows + 255) / 256), dim3(256), 0, st, 1,
-                      (const HeadMeta*)r.meta, sorted, (const int*)r.inv, at<int>(p.perm),
+                      (const HeadMeta*)r.meta, sorted, (const int*)r.inv, at<int4>(p.perm),
                       at<int>(p.run));
   }
   // The weights of a later piece: read in place, or copied into the workspace.
@@ -2167,7 +2167,8 @@ int head_grad_launches(const HeadArgs& a) {
   const Plan& p = c.p;
   if (p.few) return 1 + head_few_groups(a.rows, a.d) + (a.grad_hidden ? 1 : 0);
   const bool sums = p.narrow || p.splits > 1 || p.n_pieces > 1;
-  return c.row_launches() + (p.rest && a.grad_head ? 3 : 2) * p.n_pieces + (p.staged ? p.n_pieces - 1 : 0) + (sums && a.grad_hidden ? 1 : 0);
+  return c.row_launches() + (p.rest && a.grad_head ? 3 : 2) * p.n_pieces +
+         (p.staged ? p.n_pieces - 1 : 0) + (sums && a.grad_hidden ? 1 : 0);
 }
 
 cudaError_t launch_head_loss(const HeadArgs& h, cudaStream_t st) {
@@ -2245,7 +2246,7 @@ cudaError_t launch_head_grad(const HeadArgs& h, cudaStream_t st) {
     TRY(launch_mode<kDlog>(p.parts, p.cfg, m, a, units, c.sms, st));
     if (a.rest) {
       const int slabs = (p.d_pad + 255) / 256;
-      const RestArgs r{a.meta, a.row_tgt, c.at<int>(p.perm), a.run, a.delta, h.hidden, h.ld_hidden,
+      const RestArgs r{a.meta, c.at<int4>(p.perm), a.delta, h.hidden, h.ld_hidden,
                        c.at<__nv_bfloat16>(p.hid), h.d, p.d_pad, slabs, v0, vc,
                        c.at<__nv_bfloat16>(p.rest_rows)};
       const long long ctas = (long long)((h.rows + 31) / 32) * slabs;

@@ -10,7 +10,8 @@ pytestmark = pytest.mark.gpu
 
 
 @pytest.mark.parametrize("rows,d,vocab,dt,ignored,pad", [
-    (8192, 64, 130, BF16, 0.3, 0), (8193, 64, 130, BF16, 0.3, 0), (16385, 64, 130, BF16, 0.3, 0), (70001, 72, 100, BF16, 0.0, 0),
+    (8192, 64, 130, BF16, 0.3, 0), (8193, 64, 130, BF16, 0.3, 0), (16385, 64, 130, BF16, 0.3, 0),
+    (70001, 72, 100, BF16, 0.0, 0),
     (70001, 72, 100, BF16, 0.9, 3), (20000, 30, 70, F32, 0.5, 0), (40000, 64, 9, BF16, 0.9999, 8)])
 def test_head_of_many_rows(rows, d, vocab, dt, ignored, pad):
     x = Head(rows, d, vocab, dt, ignored, pad, seed=rows + vocab)

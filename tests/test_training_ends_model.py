@@ -21,7 +21,8 @@ class Trajectory:
         self.wl = wl = synth.WORKLOADS[name]
         w = synth.make_weights(wl.model, wl.seed, gain_std=0.02)
         prompt = synth.make_prompt(wl)
-        _, recs = oracle.generate(oracle.Model(w), prompt, wl.gen_len, synth.make_plan(wl), max_steps=3)
+        _, recs = oracle.generate(oracle.Model(w), prompt, wl.gen_len, synth.make_plan(wl),
+                                  max_steps=3)
         ids, pos, types, labels, qrows = oracle.trajectory(prompt, wl.model, wl.gen_len, recs)
         rows = np.concatenate([qrows[k] for k in sorted(qrows)])
         rng = np.random.default_rng(seed)
@@ -156,7 +157,8 @@ def test_gradients_of_many_rows_are_those_of_its_parts(traj, ignored):
     target[:40] = target[100]                       # shared targets
     target[torch.rand(m, generator=g, device="cuda") < ignored] = -1
     weight = torch.rand(m, generator=g, device="cuda") / m
-    ws = workspace(max(traj.model.smdm_loss_stepcausal_workspace_bytes(k, grad=True) for k in (100, m)))
+    ws = workspace(max(traj.model.smdm_loss_stepcausal_workspace_bytes(k, grad=True)
+                       for k in (100, m)))
 
     def grads(a, b):
         k = b - a
