@@ -1474,8 +1474,8 @@ __global__ void __launch_bounds__(256)
 // them.  A CTA takes 256 columns and the targets that begin at 32 places of the rows in order of
 // their targets: a warp each, all warps together for one of more than kRestLong rows.  Summed in
 // fp32, eight rows in flight per warp; kept in bf16, which is 2^-9 of 2^-9 of D's part of dW.
-// 3072 rows of 4096 over 8192 ids: 13 us, mostly the latency of loads that follow one another;
-// 786432 rows of 64 over 64 ids: 0.5 ms of 6.
+// 4096 rows with a quarter left out, 4096 x 8192: 13 us, mostly the latency of loads that follow one
+// another; 786432 rows of 64 over 64 ids: 0.5 ms of 6.
 struct RestArgs {
   const HeadMeta* meta;
   const int4* perm;
